@@ -122,6 +122,10 @@ def _dtype_code(t: torch.Tensor) -> int:
     raise TypeError(f"logits must be bfloat16 (or int16 bf16 bit patterns) or float32, got {t.dtype}")
 
 
+def _torch_dtype(code: int) -> torch.dtype:
+    return torch.bfloat16 if code == SV_BF16 else torch.float32
+
+
 def spec_verify_workspace_bytes(B: int, gamma_max: int, V: int, dtype: int) -> int:
     return int(lib().spec_verify_workspace_bytes(B, gamma_max, V, dtype))
 
@@ -265,10 +269,28 @@ class Verifier:
         self.pq = torch.empty((B, gamma_max, 2), dtype=torch.float32, device=dev) if with_pq else None
 
     def __call__(self, p_logits, q_logits, draft_tokens, uniforms, temperature, top_k=None, top_p=None,
-                 gamma_len=None, stream=None, lenience=None):
+                 gamma_len=None, stream=None, lenience=None, processor=None, mask_rows=None):
+        """With `processor` (logits.LogitProcessor), p_logits are adjusted in
+        place before the verify, position by position of the drafts; mask_rows
+        [B, gamma_max+1] picks its grammar masks.  q_logits must be what the
+        drafts were sampled from: a Sampler given the same processor leaves
+        them so."""
+        if processor is not None:
+            rows = None
+            if gamma_len is not None:   # target rows beyond gamma_b stay as they are
+                from .logits import on_stream
+                with on_stream(stream):
+                    rows = gamma_len + 1
+            processor(p_logits, draft_tokens, 0, mask_rows, rows, stream=stream)
         spec_verify(p_logits, q_logits, draft_tokens, gamma_len, uniforms, temperature, top_k, top_p,
                     self.tokens, self.n_accepted, self.alpha, self.pq, self.workspace, stream, lenience, self.hints)
         return self.tokens, self.n_accepted, self.alpha, self.pq
+
+    def from_hidden(self, hidden, head, q_logits, draft_tokens, uniforms, temperature, stream=None, **kw):
+        """The same from the target's hidden states [B, gamma_max+1, K] and its
+        4-bit head (logits.W4Head); the logits stay in self.p_logits."""
+        self.p_logits = head(hidden, getattr(self, "p_logits", None), _torch_dtype(self.dtype), stream)
+        return self(self.p_logits, q_logits, draft_tokens, uniforms, temperature, stream=stream, **kw)
 
 
 def gumbel_workspace(B: int, gamma_max: int, V: int, dtype: int, device) -> torch.Tensor:
@@ -359,10 +381,17 @@ class Sampler:
             raise SpecVerifyError(rc, "spec_sample_workspace_init")
         self.tokens = torch.empty((R,), dtype=torch.int32, device=dev)
 
-    def __call__(self, logits, uniforms, temperature, top_k=None, top_p=None, stream=None):
+    def __call__(self, logits, uniforms, temperature, top_k=None, top_p=None, stream=None, processor=None,
+                 draft_tokens=None, mask_rows=None):
+        """With `processor` (logits.LogitProcessor), the logits are adjusted in
+        place before the draw: they follow the history and draft_tokens [R, n],
+        the sequence's drafts so far; mask_rows [R] picks grammar masks."""
         if logits.dim() != 2:
             raise ValueError("logits must be [R, V]")
         R, V = logits.shape
+        if processor is not None:
+            processor(logits, draft_tokens, 0 if draft_tokens is None else draft_tokens.shape[1], mask_rows,
+                      stream=stream)
         dev = logits.device
         dt = _dtype_code(logits)
         _check(logits, "logits", logits.dtype, (self.R, self.V), dev)
@@ -376,6 +405,15 @@ class Sampler:
         if rc != SV_OK:
             raise SpecVerifyError(rc, "spec_sample")
         return self.tokens
+
+    def from_hidden(self, hidden, head, uniforms, temperature, out=None, stream=None, **kw):
+        """The same from the drafter's hidden states [R, K] and its 4-bit head
+        (logits.W4Head).  The logits, which the verify needs as its q rows, go to
+        `out` [R, V] (None: self.logits, overwritten by the next call)."""
+        if out is None:
+            out = getattr(self, "logits", None)
+        self.logits = head(hidden, out, _torch_dtype(self.dtype), stream)
+        return self(self.logits, uniforms, temperature, stream=stream, **kw)
 
 
 def spec_sample_gumbel(logits: torch.Tensor, noise: torch.Tensor, temperature: torch.Tensor,

@@ -1,6 +1,7 @@
-"""Build libspecverify.so (the verify library) and libsvprobe.so (the
-streaming-read ceiling probe that bench.py times beside it) for gfx950 with
-hipcc, in-tree, next to this file."""
+"""Build libspecverify.so (the verify library), libspeclogits.so (the logits
+operators around it) and libsvprobe.so (the streaming-read ceiling probe that
+bench.py times beside the verify) for gfx950 with hipcc, in-tree, next to this
+file."""
 from __future__ import annotations
 
 import os
@@ -11,6 +12,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SRC = os.path.join(HERE, "csrc", "spec_verify.hip")
 OUT = os.path.join(HERE, "libspecverify.so")
+LOGITS_SRC = os.path.join(HERE, "csrc", "spec_logits.hip")
+LOGITS_OUT = os.path.join(HERE, "libspeclogits.so")
 PROBE_SRC = os.path.join(HERE, "csrc", "read_probe.hip")
 PROBE_OUT = os.path.join(HERE, "libsvprobe.so")
 
@@ -37,8 +40,9 @@ def _hipcc(src: str, out: str, verbose: bool) -> str:
 
 
 def build_library(verbose: bool = False) -> str:
-    """Compile both libraries (always); returns the verify library's path."""
+    """Compile the libraries (always); returns the verify library's path."""
     _hipcc(PROBE_SRC, PROBE_OUT, verbose)
+    _hipcc(LOGITS_SRC, LOGITS_OUT, verbose)
     return _hipcc(SRC, OUT, verbose)
 
 

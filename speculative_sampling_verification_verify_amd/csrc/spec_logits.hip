@@ -1,0 +1,210 @@
+// The operators between a model and the verify / sampling calls, for MI355X
+// (gfx950): kernels and their C ABI (see spec_logits.h).
+
+#include "sl_w4.h"
+#include "sl_process.h"
+
+#include <stdio.h>
+#include <string.h>
+
+namespace sl {
+
+static thread_local char g_errbuf[256];
+
+static int hip_status(hipError_t e) {
+  if (e == hipSuccess) return SV_OK;
+  snprintf(g_errbuf, sizeof g_errbuf, "HIP error: %s", hipGetErrorString(e));
+  return SV_ERR_HIP;
+}
+
+static bool known(int dtype) { return dtype == SV_BF16 || dtype == SV_FP32; }
+static size_t size_of(int dtype) { return dtype == SV_BF16 ? 2 : 4; }
+static bool misaligned(const void* p, size_t n) { return (uintptr_t)p % n != 0; }
+
+// ---------------------------------------------------------------------------
+// spec_logits_w4
+// ---------------------------------------------------------------------------
+
+template <typename XT, typename ST, typename OT>
+static hipError_t launch_w4(const W4Args& a, int group, hipStream_t st) {
+  const long long tiles = (long long)a.row_tiles * ((a.N + 15) / 16);
+  const dim3 grid((unsigned)((tiles + 3) / 4)), block(256);
+  if (group == 32) hipLaunchKernelGGL((w4_kernel<XT, ST, OT, 4>), grid, block, 0, st, a);
+  else if (group == 64) hipLaunchKernelGGL((w4_kernel<XT, ST, OT, 2>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((w4_kernel<XT, ST, OT, 1>), grid, block, 0, st, a);
+  return hipGetLastError();
+}
+
+template <typename XT, typename ST>
+static hipError_t launch_w4(const W4Args& a, int group, int out_dtype, hipStream_t st) {
+  return out_dtype == SV_BF16 ? launch_w4<XT, ST, uint16_t>(a, group, st) : launch_w4<XT, ST, float>(a, group, st);
+}
+
+}  // namespace sl
+
+using namespace sl;
+
+extern "C" int spec_logits_w4(const void* hidden, int hidden_dtype, const uint8_t* weights, const void* scales,
+                              int scale_dtype, const uint8_t* zeros, int group, int R, int K, int N, void* out,
+                              int out_dtype, void* stream) {
+  if (!known(hidden_dtype) || !known(scale_dtype) || !known(out_dtype)) return SV_ERR_UNSUPPORTED;
+  if (R > SL_MAX_ROWS || K > SL_MAX_K || N > SV_MAX_VOCAB) return SV_ERR_UNSUPPORTED;
+  if (R < 0 || K < 1 || N < 1 || group < 1) return SV_ERR_ARG;
+  if (group != 32 && group != 64 && group % 128 != 0) return SV_ERR_UNSUPPORTED;
+  if (K % group != 0) return SV_ERR_ARG;
+  if (R == 0) return SV_OK;
+  if (!hidden || !weights || !scales || !out) return SV_ERR_ARG;
+  if (misaligned(hidden, 16) || misaligned(weights, 16) || misaligned(scales, size_of(scale_dtype)) ||
+      misaligned(out, size_of(out_dtype)))
+    return SV_ERR_ARG;
+  W4Args a;
+  memset(&a, 0, sizeof a);
+  a.x = hidden;
+  a.w = weights;
+  a.s = scales;
+  a.z = zeros;
+  a.out = out;
+  a.R = R;
+  a.K = K;
+  a.N = N;
+  a.G = K / group;
+  a.gb = group >= 128 ? group / 128 : 1;
+  a.row_tiles = (R + 15) / 16;
+  if ((long long)a.row_tiles * ((N + 15) / 16) > 0x7FFFFFFFLL) return SV_ERR_UNSUPPORTED;
+  hipStream_t st = (hipStream_t)stream;
+  hipError_t e;
+  if (hidden_dtype == SV_BF16)
+    e = scale_dtype == SV_BF16 ? launch_w4<uint16_t, uint16_t>(a, group, out_dtype, st)
+                               : launch_w4<uint16_t, float>(a, group, out_dtype, st);
+  else
+    e = scale_dtype == SV_BF16 ? launch_w4<float, uint16_t>(a, group, out_dtype, st)
+                               : launch_w4<float, float>(a, group, out_dtype, st);
+  return hip_status(e);
+}
+
+// ---------------------------------------------------------------------------
+// The token history
+// ---------------------------------------------------------------------------
+
+// The checks of both calls; SV_OK with *run = false: nothing to do.
+static int check_history(const void* counts, const void* ids, const void* num, int S, int V, const void* slots, int B,
+                         bool* run) {
+  *run = false;
+  if (V > SV_MAX_VOCAB || B > SL_MAX_ROWS) return SV_ERR_UNSUPPORTED;
+  if (S < 0 || V < 1 || B < 0) return SV_ERR_ARG;
+  if (!slots && B > S) return SV_ERR_ARG;
+  if (B == 0 || S == 0) return SV_OK;
+  if (!counts || !ids || !num) return SV_ERR_ARG;
+  if (misaligned(counts, 4) || misaligned(ids, 4) || misaligned(num, 4) || misaligned(slots, 4)) return SV_ERR_ARG;
+  *run = true;
+  return SV_OK;
+}
+
+extern "C" int spec_history_append(int32_t* counts, int32_t* ids, int32_t* num, int S, int V, const int32_t* slots,
+                                   const int32_t* tokens, int B, int T, int prompt, void* stream) {
+  if (T < 1) return SV_ERR_ARG;
+  if (T > (1 << 24)) return SV_ERR_UNSUPPORTED;
+  bool run;
+  const int rc = check_history(counts, ids, num, S, V, slots, B, &run);
+  if (rc != SV_OK || !run) return rc;
+  if (!tokens || misaligned(tokens, 4)) return SV_ERR_ARG;
+  const int chunks = (T + HA_NT - 1) / HA_NT;
+  const long long grid = (long long)B * chunks;
+  if (grid > 0x7FFFFFFFLL) return SV_ERR_UNSUPPORTED;
+  const HistoryArgs a = {(uint32_t*)counts, ids, num, slots, tokens, S, V, B, T, prompt != 0, chunks};
+  hipLaunchKernelGGL(history_append_kernel, dim3((unsigned)grid), dim3(HA_NT), 0, (hipStream_t)stream, a);
+  return hip_status(hipGetLastError());
+}
+
+extern "C" int spec_history_reset(int32_t* counts, const int32_t* ids, int32_t* num, int S, int V,
+                                  const int32_t* slots, int B, void* stream) {
+  bool run;
+  const int rc = check_history(counts, ids, num, S, V, slots, B, &run);
+  if (rc != SV_OK || !run) return rc;
+  const HistoryArgs a = {(uint32_t*)counts, const_cast<int32_t*>(ids), num, slots, nullptr, S, V, B, 0, 0, 1};
+  hipLaunchKernelGGL(history_reset_kernel, dim3((unsigned)B), dim3(HR_NT), 0, (hipStream_t)stream, a);
+  return hip_status(hipGetLastError());
+}
+
+// ---------------------------------------------------------------------------
+// spec_process_logits
+// ---------------------------------------------------------------------------
+
+// Workgroups to spread a call of few rows over, and the least elements worth one.
+constexpr int PR_TARGET = 1024;
+constexpr int PR_MIN_PIECE = 4096;
+
+extern "C" int spec_process_logits(const void* logits, void* out, int dtype, const int32_t* counts, const int32_t* ids,
+                                   const int32_t* num, int S, const int32_t* slots, const int32_t* draft_tokens,
+                                   int draft_stride, int first, const float* repetition, const float* presence,
+                                   const float* frequency, const int32_t* bias_ids, const float* bias_values, int NB,
+                                   const uint32_t* masks, int M, const int32_t* mask_rows, const int32_t* rows, int B,
+                                   int J, int V, void* stream) {
+  if (!known(dtype)) return SV_ERR_UNSUPPORTED;
+  if (V > SV_MAX_VOCAB || NB > SL_MAX_BIAS || M > SL_MAX_MASKS) return SV_ERR_UNSUPPORTED;
+  if (B < 0 || J < 1 || V < 1 || S < 0 || NB < 0 || M < 0 || first < 0) return SV_ERR_ARG;
+  if ((long long)B * J > SL_MAX_ROWS) return SV_ERR_UNSUPPORTED;
+  if (B == 0) return SV_OK;
+  if (!logits || !out) return SV_ERR_ARG;
+  if ((counts != nullptr) != (ids != nullptr) || (counts != nullptr) != (num != nullptr)) return SV_ERR_ARG;
+  if ((counts == nullptr) != (S == 0)) return SV_ERR_ARG;
+  if (counts && !slots && B > S) return SV_ERR_ARG;
+  if (draft_tokens && (long long)first + J - 1 > draft_stride) return SV_ERR_ARG;
+  if (draft_tokens && (long long)first + J - 1 > SL_MAX_DRAFT) return SV_ERR_UNSUPPORTED;
+  if ((bias_ids != nullptr) != (NB > 0) || (bias_values != nullptr) != (NB > 0)) return SV_ERR_ARG;
+  if ((masks != nullptr) != (M > 0) || (mask_rows != nullptr) != (M > 0)) return SV_ERR_ARG;
+  const void* words[] = {counts, ids, num, slots, draft_tokens, repetition, presence, frequency, bias_ids, bias_values,
+                         masks, mask_rows, rows};
+  for (const void* p : words)
+    if (misaligned(p, 4)) return SV_ERR_ARG;
+  if (misaligned(logits, size_of(dtype)) || misaligned(out, size_of(dtype))) return SV_ERR_ARG;
+
+  ProcessArgs a;
+  memset(&a, 0, sizeof a);
+  a.in = logits;
+  a.out = out;
+  a.counts = (const uint32_t*)counts;
+  a.ids = ids;
+  a.num = num;
+  a.S = S;
+  a.slots = slots;
+  a.drafts = draft_tokens;
+  a.draft_stride = draft_stride;
+  a.first = first;
+  a.rep = repetition;
+  a.pres = presence;
+  a.freq = frequency;
+  a.bias_ids = bias_ids;
+  a.bias_vals = bias_values;
+  a.NB = NB;
+  a.masks = masks;
+  a.M = M;
+  a.mask_rows = mask_rows;
+  a.rows = rows;
+  a.B = B;
+  a.J = J;
+  a.V = V;
+  a.W = (V + 31) / 32;
+  a.wide = !misaligned(logits, 16) && !misaligned(out, 16);
+  const int nrows = B * J;
+  int chunks = (PR_TARGET + nrows - 1) / nrows;
+  const int most = (V + PR_MIN_PIECE - 1) / PR_MIN_PIECE;
+  if (chunks > most) chunks = most;
+  a.piece = ((V + chunks - 1) / chunks + 31) / 32 * 32;
+  a.chunks = (V + a.piece - 1) / a.piece;
+  const dim3 grid((unsigned)((long long)nrows * a.chunks));
+  hipStream_t st = (hipStream_t)stream;
+  if (dtype == SV_BF16) hipLaunchKernelGGL((process_kernel<uint16_t>), grid, dim3(PR_NT), 0, st, a);
+  else hipLaunchKernelGGL((process_kernel<float>), grid, dim3(PR_NT), 0, st, a);
+  return hip_status(hipGetLastError());
+}
+
+extern "C" const char* spec_logits_strerror(int code) {
+  switch (code) {
+    case SV_OK: return "ok";
+    case SV_ERR_ARG: return "invalid argument (null pointer, size out of range or misaligned pointer)";
+    case SV_ERR_UNSUPPORTED: return "unsupported dtype, group or size";
+    case SV_ERR_HIP: return g_errbuf[0] ? g_errbuf : "HIP error";
+    default: return "unknown error code";
+  }
+}

@@ -1,0 +1,177 @@
+"""spec_logits_w4 on the GPU against the float64 product.
+
+Two kinds of inputs.  Where hidden states are small integers and scales powers
+of two, every float32 partial sum is exact, so the result is the correctly
+rounded exact product and has to be equal bit for bit.  Where they are real
+numbers, the result may be off by the roundings of the float32 sums
+(oracle.logits.w4_error_bound) and by half a step of the output's type."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from speculative_sampling_verification_verify_amd import logits as L
+from logits_util import HALF, TYPES, dev, head_arrays, host, make_head
+
+pytestmark = pytest.mark.gpu
+
+# (R, K, N, group): one value of everything, tails of 16 rows and columns, K that ends inside a 128-block,
+# several blocks per group, odd N, both sides of every change of tile.
+SHAPES = [(1, 32, 1, 32), (1, 128, 16, 128), (3, 96, 17, 32), (2, 160, 33, 32), (16, 256, 33, 64), (17, 320, 50, 64),
+          (33, 512, 100, 128), (5, 1024, 1000, 256), (2, 384, 7, 384), (64, 160, 130, 32), (100, 128, 300, 32),
+          (130, 640, 257, 128), (15, 2048, 515, 64), (32, 4096, 271, 128), (65, 192, 64, 64), (257, 256, 385, 128),
+          (1, 8192, 130, 128), (9, 4128, 90, 32), (4, 1088, 2049, 64), (1, 512, 32000, 128), (48, 96, 31, 32)]
+
+
+def small_ints(rng, R, K, x):
+    """Integers whose sums of 31 * |x| stay below 2^21 over all of K; of an fp32
+    hidden state, up to 11 bits, more than one bf16 part holds."""
+    most = min(255 if x == "bf16" else 2047, int(2 ** 21 / (31 * K)))
+    return rng.integers(-most, most + 1, (R, K)).astype(np.float64)
+
+
+@pytest.mark.parametrize("x,scale,out", [("bf16", "bf16", "bf16"), ("bf16", "fp32", "fp32"), ("fp32", "bf16", "fp32"),
+                                         ("fp32", "fp32", "bf16")])
+@pytest.mark.parametrize("R,K,N,group", SHAPES)
+def test_exact_integers(R, K, N, group, x, scale, out):
+    rng = np.random.default_rng(R * 7919 + K * 31 + N)
+    h = small_ints(rng, R, K, x)
+    w, s, z = make_head(rng, N, K, group, scale, zeros=(R + N) % 2 == 0, power=True)
+    got = L.spec_logits_w4(dev(h, TYPES[x]), w, s, z, out_dtype=TYPES[out])
+    arrays = head_arrays(w, s, z)
+    ref = oracle.logits.w4_product(h, *arrays)
+    # Inside a group the sums are integers below 2^21.  A scale is 2^-3 to 2, so
+    # every later partial sum is a multiple of 2^-3 below 2 * 15 / 31 * 2^21.
+    assert np.abs(h).sum(axis=1).max() * 31 <= 2 ** 21 and arrays[1].max() <= 2 and arrays[1].min() >= 2 ** -3
+    assert torch.equal(got.cpu(), torch.from_numpy(ref).float().to(TYPES[out])), (R, K, N, group)
+
+
+@pytest.mark.parametrize("x,scale,out", [("bf16", "bf16", "bf16"), ("bf16", "bf16", "fp32"), ("fp32", "fp32", "fp32"),
+                                         ("fp32", "bf16", "bf16")])
+@pytest.mark.parametrize("R,K,N,group", SHAPES)
+def test_real_values(R, K, N, group, x, scale, out):
+    rng = np.random.default_rng(R * 104729 + K * 17 + N)
+    h = dev(rng.standard_normal((R, K)) + (0.5 if N % 3 == 0 else 0.0), TYPES[x])
+    w, s, z = make_head(rng, N, K, group, scale, zeros=(R + N) % 2 == 1)
+    got = host(L.spec_logits_w4(h, w, s, z, out_dtype=TYPES[out]))
+    arrays = head_arrays(w, s, z)
+    ref = oracle.logits.w4_product(host(h), *arrays)
+    bound = oracle.logits.w4_error_bound(host(h), *arrays, parts=3 if x == "fp32" else 1)
+    tol = bound + HALF[out] * (np.abs(ref) + bound)
+    bad = ~(np.abs(got - ref) <= tol)
+    assert not bad.any(), (R, K, N, group, np.argwhere(bad)[:4], np.abs(got - ref).max())
+
+
+@pytest.mark.parametrize("group", [32, 64, 128, 256])
+@pytest.mark.parametrize("R", [1, 20, 70])
+def test_fp32_hidden_keeps_all_bits(R, group):
+    """One value per row, with a 24-bit significand.  Its product with 16 + w
+    is rounded once for each of the three parts that add to it (at most
+    31 |v|), the correction once, the scale and the sum once each."""
+    rng = np.random.default_rng(group)
+    K, N = 512, 40
+    h = np.zeros((R, K), dtype=np.float32)
+    h[np.arange(R), rng.integers(0, K, R)] = (rng.random(R) + 1).astype(np.float32)
+    w, s, z = make_head(rng, N, K, group, "fp32", zeros=True)
+    got = host(L.spec_logits_w4(dev(h), w, s, z))
+    arrays = head_arrays(w, s, z)
+    ref = oracle.logits.w4_product(h, *arrays)
+    v = h.max(axis=1).astype(np.float64)[:, None] * arrays[1].max(axis=1)[None, :]
+    tol = 2.0 ** -24 * (3 * 31 + 31 + 2 * 15) * v
+    assert (np.abs(got - ref) <= tol).all()
+    assert tol.max() < 2.0 ** -16 * v.max()      # a lost third part would show
+
+
+@pytest.mark.parametrize("R", [1, 5, 16, 40, 200])
+@pytest.mark.parametrize("x", ["bf16", "fp32"])
+def test_non_finite_rows_stay_alone(R, x):
+    rng = np.random.default_rng(R)
+    K, N = 256, 70
+    h = rng.integers(-3, 4, (R, K)).astype(np.float32)
+    w, s, z = make_head(rng, N, K, 64, power=True)
+    ref = oracle.logits.w4_product(h, *head_arrays(w, s, z))
+    bad = {0: np.nan, R // 2: np.inf, R - 1: -np.inf}
+    for r, v in bad.items():
+        h[r, (37 * r) % K] = v
+    got = host(L.spec_logits_w4(dev(h, TYPES[x]), w, s, z, out_dtype=torch.float32))
+    keep = [r for r in range(R) if r not in bad]
+    assert np.isnan(got[list(bad)]).all()
+    assert (got[keep] == ref[keep]).all()
+
+
+def test_leading_dimensions_alignment_and_out():
+    """[B, J, K] hidden states, an output that starts at an odd element, bytes of
+    zeros above their low four bits, and nothing written around the output."""
+    rng = np.random.default_rng(3)
+    B, J, K, N = 3, 5, 256, 77
+    h = rng.integers(-3, 4, (B, J, K)).astype(np.float64)
+    w, s, z = make_head(rng, N, K, 128, power=True)
+    ref = oracle.logits.w4_product(h.reshape(-1, K), *head_arrays(w, s, z)).reshape(B, J, N)
+    for t in (torch.bfloat16, torch.float32):
+        room = torch.full((B * J * N + 9,), 123.0, dtype=t, device="cuda")
+        out = room[1:1 + B * J * N].view(B, J, N)
+        got = L.W4Head(w, s, z | 0xA0)(dev(h, torch.bfloat16), out=out)
+        assert got is out
+        assert torch.equal(out.cpu(), torch.from_numpy(ref).float().to(t))
+        assert (room[0] == 123) and (room[1 + B * J * N:] == 123).all()
+
+
+def test_empty_call():
+    w, s, z = make_head(np.random.default_rng(0), 8, 64, 32)
+    assert L.spec_logits_w4(torch.empty((0, 64), device="cuda", dtype=torch.bfloat16), w, s, z).shape == (0, 8)
+
+
+@pytest.mark.parametrize("R", [1, 18])
+def test_weights_past_32_bits(R):
+    """More than 2^32 bytes of weights: the last rows against the product."""
+    K, N = 65536, 132000
+    rng = np.random.default_rng(5)
+    w = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device="cuda")
+    s = torch.ones((N, K // 256), dtype=torch.bfloat16, device="cuda")
+    h = np.zeros((R, K))
+    h[:, rng.integers(0, K, 200)] = rng.integers(-3, 4, (R, 200))
+    got = L.spec_logits_w4(dev(h, torch.bfloat16), w, s, out_dtype=torch.float32)
+    for lo in (0, 65535, N - 40):
+        part = slice(lo, lo + 40)
+        ref = oracle.logits.w4_product(h, w[part].cpu().numpy(), np.ones((40, K // 256)))
+        assert (host(got[:, part]) == ref).all()
+
+
+def test_output_past_32_bits():
+    """More than 2^31 output elements."""
+    R, K, N = 17000, 32, 130001
+    rng = np.random.default_rng(6)
+    h = rng.integers(-3, 4, (R, K)).astype(np.float64)
+    w, s, _ = make_head(rng, N, K, 32, power=True, zeros=False)
+    out = torch.full((R, N), 5.0, dtype=torch.bfloat16, device="cuda")
+    L.spec_logits_w4(dev(h, torch.bfloat16), w, s, out=out)
+    for r in (0, 16, 8191, R - 1):
+        ref = oracle.logits.w4_product(h[r:r + 1], *head_arrays(w, s, None))
+        assert torch.equal(out[r:r + 1].cpu(), torch.from_numpy(ref).float().bfloat16())
+
+
+@pytest.mark.parametrize("R,N", [(1, 2000), (40, 700), (200, 300)])
+def test_repeatable_and_on_another_stream(R, N):
+    """The same bits every time, on a side stream and from a replayed graph."""
+    rng = np.random.default_rng(R)
+    K = 1024
+    h = dev(rng.standard_normal((R, K)), torch.bfloat16)
+    w, s, z = make_head(rng, N, K, 128)
+    ref = L.spec_logits_w4(h, w, s, z)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        a = L.spec_logits_w4(h, w, s, z)
+    b = torch.empty_like(ref)
+    torch.cuda.synchronize()
+    L.spec_logits_w4(h, w, s, z, out=b, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(a, ref) and torch.equal(b, ref)
+    graph, c = torch.cuda.CUDAGraph(), torch.empty_like(ref)
+    with torch.cuda.graph(graph):
+        L.spec_logits_w4(h, w, s, z, out=c)
+    for k in range(3):
+        h.copy_(dev(rng.standard_normal((R, K)), torch.bfloat16))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(c, L.spec_logits_w4(h, w, s, z)), k

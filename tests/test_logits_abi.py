@@ -1,0 +1,162 @@
+"""The logits library: it loads, exports every entry point declared in
+include/spec_logits.h, and refuses bad arguments on the host before touching
+the GPU (no compute calls here)."""
+import glob
+import os
+import re
+import subprocess
+import sys
+
+import pytest
+import torch
+
+from speculative_sampling_verification_verify_amd import logits as L
+from speculative_sampling_verification_verify_amd.binding import (SV_BF16, SV_ERR_ARG, SV_ERR_UNSUPPORTED, SV_FP32,
+                                                                  SV_OK)
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "spec_logits.h")
+SRC = os.path.join(ROOT, "speculative_sampling_verification_verify_amd", "csrc", "spec_logits.hip")
+HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+
+FAKE = 0x100000   # never dereferenced: every case below ends on the host
+
+
+def _lib():
+    if not os.path.exists(L.LIB_PATH):
+        from speculative_sampling_verification_verify_amd import build
+        build.build_library()
+    return L.lib()
+
+
+def declared_functions():
+    txt = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    return sorted(set(re.findall(r"^[A-Za-z_][\w\s\*]*?\b(spec_\w*)\s*\(", txt, flags=re.M)))
+
+
+def test_exports_every_declared_symbol():
+    assert set(declared_functions()) == set(L.EXPORTED)
+    for name in L.EXPORTED:
+        assert hasattr(_lib(), name), name
+
+
+def w4(x=FAKE, xt=SV_BF16, w=FAKE, s=FAKE, st=SV_BF16, z=None, group=64, R=2, K=128, N=10, out=FAKE, ot=SV_FP32):
+    return _lib().spec_logits_w4(x, xt, w, s, st, z, group, R, K, N, out, ot, None)
+
+
+def test_w4_refusals():
+    assert w4(R=0) == SV_OK
+    assert w4(xt=2) == w4(st=-1) == w4(ot=7) == SV_ERR_UNSUPPORTED
+    assert w4(R=L.SL_MAX_ROWS + 1) == w4(N=(1 << 20) + 1) == SV_ERR_UNSUPPORTED
+    assert w4(K=L.SL_MAX_K + 64) == SV_ERR_UNSUPPORTED
+    assert w4(group=16) == w4(group=96, K=192) == w4(group=160, K=320) == SV_ERR_UNSUPPORTED
+    assert w4(R=-1) == w4(K=0) == w4(N=0) == w4(group=0) == w4(group=-32) == SV_ERR_ARG
+    assert w4(K=96) == w4(group=256, K=128) == w4(K=100, group=32) == SV_ERR_ARG
+    for k in ("x", "w", "s", "out"):
+        assert w4(**{k: None}) == SV_ERR_ARG, k
+    assert w4(x=FAKE + 8) == w4(w=FAKE + 4) == w4(s=FAKE + 1) == w4(out=FAKE + 2) == SV_ERR_ARG
+    assert w4(s=FAKE + 2, st=SV_FP32) == w4(out=FAKE + 1, ot=SV_BF16) == SV_ERR_ARG
+
+
+def test_history_refusals():
+    def append(c=FAKE, i=FAKE, n=FAKE, S=4, V=100, slots=FAKE, t=FAKE, B=3, T=5):
+        return _lib().spec_history_append(c, i, n, S, V, slots, t, B, T, 0, None)
+
+    def reset(c=FAKE, i=FAKE, n=FAKE, S=4, V=100, slots=FAKE, B=3):
+        return _lib().spec_history_reset(c, i, n, S, V, slots, B, None)
+
+    for f in (append, reset):
+        assert f(B=0) == f(S=0, c=None) == SV_OK
+        assert f(B=-1) == f(S=-1) == f(V=0) == SV_ERR_ARG
+        assert f(V=(1 << 20) + 1) == f(B=L.SL_MAX_ROWS + 1) == SV_ERR_UNSUPPORTED
+        assert f(slots=None, B=5) == SV_ERR_ARG
+        for k in ("c", "i", "n"):
+            assert f(**{k: None}) == f(**{k: FAKE + 2}) == SV_ERR_ARG, k
+        assert f(slots=FAKE + 1) == SV_ERR_ARG
+    assert append(T=0) == append(t=None) == append(t=FAKE + 2) == SV_ERR_ARG
+    assert append(T=(1 << 24) + 1) == append(T=1 << 24, B=1 << 20) == SV_ERR_UNSUPPORTED
+
+
+def test_process_refusals():
+    names = ("logits out dtype counts ids num S slots draft_tokens draft_stride first repetition presence frequency "
+             "bias_ids bias_values NB masks M mask_rows rows B J V").split()
+    base = dict(logits=FAKE, out=FAKE, dtype=SV_BF16, counts=FAKE, ids=FAKE, num=FAKE, S=4, slots=FAKE,
+                draft_tokens=FAKE, draft_stride=8, first=1, repetition=FAKE, presence=FAKE, frequency=FAKE,
+                bias_ids=FAKE, bias_values=FAKE, NB=3, masks=FAKE, M=2, mask_rows=FAKE, rows=FAKE, B=3, J=4, V=100)
+
+    def call(**kw):
+        a = dict(base, **kw)
+        return _lib().spec_process_logits(*[a[n] for n in names], None)
+
+    assert call(B=0) == SV_OK
+    assert call(dtype=2) == call(V=(1 << 20) + 1) == call(NB=L.SL_MAX_BIAS + 1) == SV_ERR_UNSUPPORTED
+    assert call(M=L.SL_MAX_MASKS + 1) == call(B=1 << 19, J=4) == SV_ERR_UNSUPPORTED
+    assert call(draft_stride=100, J=65, first=1) == SV_ERR_UNSUPPORTED
+    assert call(draft_stride=1 << 30, J=2, first=(1 << 31) - 1) == SV_ERR_ARG
+    for k in ("B", "S", "NB", "M", "first"):
+        assert call(**{k: -1}) == SV_ERR_ARG, k
+    assert call(J=0) == call(V=0) == SV_ERR_ARG
+    assert call(logits=None) == call(out=None) == SV_ERR_ARG
+    assert call(counts=None) == call(ids=None) == call(num=None) == call(S=0) == SV_ERR_ARG
+    assert call(counts=None, ids=None, num=None) == SV_ERR_ARG        # S without a history
+    assert call(slots=None, B=5) == SV_ERR_ARG
+    assert call(draft_stride=3) == call(first=6) == SV_ERR_ARG
+    assert call(bias_ids=None) == call(bias_values=None) == call(NB=0) == SV_ERR_ARG
+    assert call(masks=None) == call(mask_rows=None) == call(M=0) == SV_ERR_ARG
+    for k in ("counts", "ids", "num", "slots", "draft_tokens", "repetition", "presence", "frequency", "bias_ids",
+              "bias_values", "masks", "mask_rows", "rows"):
+        assert call(**{k: FAKE + 2}) == SV_ERR_ARG, k
+    assert call(logits=FAKE + 1) == call(out=FAKE + 1) == call(out=FAKE + 2, dtype=SV_FP32) == SV_ERR_ARG
+
+
+def test_strerror_and_missing_library(monkeypatch, tmp_path):
+    _lib()
+    for code in (0, -1, -2, -4, 17):
+        assert L.spec_logits_strerror(code)
+    monkeypatch.setattr(L, "_lib", None)
+    monkeypatch.setattr(L, "LIB_PATH", str(tmp_path / "absent.so"))
+    with pytest.raises(RuntimeError, match="missing"):
+        L.lib()
+
+
+def test_host_tensors_are_refused():
+    z = torch.zeros
+    with pytest.raises(ValueError, match="GPU memory"):
+        L.spec_logits_w4(z(1, 64), z((4, 32), dtype=torch.uint8), z(4, 1))
+    with pytest.raises(ValueError, match="GPU memory"):
+        L.spec_process_logits(z(2, 3, 10))
+    h = L.History.new(2, 10, device="cpu")
+    with pytest.raises(ValueError, match="GPU memory"):
+        L.spec_history_append(h, z((2, 3), dtype=torch.int32))
+    with pytest.raises(ValueError, match="GPU memory"):
+        L.spec_history_reset(h)
+
+
+def _runtime():
+    found = sorted(glob.glob("/opt/rocm/llvm/lib/clang/*/lib/linux/libclang_rt.asan-x86_64.so"))
+    return found[-1] if found else None
+
+
+@pytest.mark.skipif("SL_LIBRARY" in os.environ or not os.path.exists(HIPCC) or _runtime() is None,
+                    reason="hipcc or the sanitizers' runtime is missing, or this is the sanitized run")
+def test_refusals_under_host_sanitizers(tmp_path):
+    """The library's host half built with AddressSanitizer and
+    UndefinedBehaviorSanitizer (its device code as in the product build), and
+    the tests above run against it in a child process."""
+    lib = str(tmp_path / "libspeclogits_hostsan.so")
+    cmd = [HIPCC, "--offload-arch=gfx950", "-O1", "-g", "-std=c++17", "-fPIC", "-shared",
+           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
+           "-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
+           "-Xarch_host", "-fno-sanitize-recover=all", "-Xarch_host", "-shared-libsan",
+           "-Xarch_host", "-fno-omit-frame-pointer",
+           "-I", os.path.join(ROOT, "include"), "-o", lib, SRC]
+    r = subprocess.run(cmd, capture_output=True, text=True, timeout=900)
+    assert r.returncode == 0, r.stderr[-4000:]
+    env = dict(os.environ, SL_LIBRARY=lib, LD_PRELOAD=_runtime(), ASAN_OPTIONS="detect_leaks=0:abort_on_error=1",
+               UBSAN_OPTIONS="halt_on_error=1:print_stacktrace=1")
+    r = subprocess.run([sys.executable, "-m", "pytest", os.path.abspath(__file__), "-q", "-p", "no:cacheprovider"],
+                       env=env, capture_output=True, text=True, timeout=900, cwd=ROOT)
+    out = r.stdout + r.stderr
+    assert r.returncode == 0, out[-4000:]
+    assert "AddressSanitizer" not in out and "runtime error" not in out, out[-4000:]
+    assert " passed" in out
