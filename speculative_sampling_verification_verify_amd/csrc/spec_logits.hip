@@ -25,19 +25,63 @@ static bool misaligned(const void* p, size_t n) { return (uintptr_t)p % n != 0; 
 // spec_logits_w4
 // ---------------------------------------------------------------------------
 
-template <typename XT, typename ST, typename OT>
-static hipError_t launch_w4(const W4Args& a, int group, hipStream_t st) {
-  const long long tiles = (long long)a.row_tiles * ((a.N + 15) / 16);
-  const dim3 grid((unsigned)((tiles + 3) / 4)), block(256);
-  if (group == 32) hipLaunchKernelGGL((w4_kernel<XT, ST, OT, 4>), grid, block, 0, st, a);
-  else if (group == 64) hipLaunchKernelGGL((w4_kernel<XT, ST, OT, 2>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((w4_kernel<XT, ST, OT, 1>), grid, block, 0, st, a);
+// LDS bytes of a block of 128 k: its operands and the sums of its groups.
+template <typename XT>
+static int block_bytes(int sub, int mt, int rp) {
+  return 4 * W4Hidden<XT>::PARTS * mt * 64 * rp + sub * mt * 64;
+}
+
+constexpr int W4S_GRID = 256;   // one workgroup per CU
+
+template <typename XT, typename ST, int SUB, int MT>
+static hipError_t launch_stream(W4Args a, hipStream_t st) {
+  const int tiles = (a.N + 15) / 16;
+  hipLaunchKernelGGL((w4_stream_kernel<XT, ST, SUB, MT>), dim3((unsigned)(tiles < W4S_GRID ? tiles : W4S_GRID)),
+                     dim3(W4S_NT), 0, st, a);
   return hipGetLastError();
 }
 
+template <typename XT, typename ST, int SUB, int MT, int NT, int U>
+static hipError_t launch_tile(W4Args a, hipStream_t st) {
+  const int nblk = (a.K + 127) / 128;
+  a.row_tiles = (a.R + 16 * MT - 1) / (16 * MT);
+  const int per_block = block_bytes<XT>(SUB, MT, 16);
+  a.kc = W4_LDS / per_block;
+  if (a.kc > nblk) a.kc = nblk;
+  const int chunks = (nblk + a.kc - 1) / a.kc;
+  a.kc = (nblk + chunks - 1) / chunks;
+  // Few columns: wavefronts share them until there are about 2048.
+  a.KS = 1;
+  while (a.KS < W4_WAVES && 2 * a.KS * U <= a.kc &&
+         (long long)((a.N + 16 * NT - 1) / (16 * NT)) * a.row_tiles * a.KS * 2 <= 4096)
+    a.KS *= 2;
+  const int red = W4_WAVES * MT * NT * 1024;
+  int lds = a.kc * per_block;
+  if (a.KS > 1 && lds < red) lds = red;
+  const int cols = W4_WAVES / a.KS * NT * 16;
+  const long long sets = (long long)((a.N + cols - 1) / cols) * a.row_tiles;
+  if (sets > 0x7FFFFFF0LL) return hipErrorInvalidValue;
+  a.per_xcd = (int)((sets + 7) / 8);
+  hipLaunchKernelGGL((w4_tile_kernel<XT, ST, SUB, MT, NT, U>), dim3((unsigned)a.per_xcd * 8), dim3(W4_NT), lds, st, a);
+  return hipGetLastError();
+}
+
+template <typename XT, typename ST, int SUB>
+static hipError_t launch_w4(W4Args a, hipStream_t st) {
+  const int nblk = (a.K + 127) / 128;
+  a.rp = 16;
+  while (a.rp / 2 >= a.R) a.rp /= 2;
+  if (a.R <= 16 && (long long)nblk * block_bytes<XT>(SUB, 1, a.rp) <= W4S_LDS) return launch_stream<XT, ST, SUB, 1>(a, st);
+  if (a.R > 16 && a.R <= 32 && (long long)nblk * block_bytes<XT>(SUB, 2, 16) <= W4S_LDS)
+    return launch_stream<XT, ST, SUB, 2>(a, st);
+  if (a.R <= 16) return launch_tile<XT, ST, SUB, 1, 2, 2>(a, st);
+  if (a.R <= 32) return launch_tile<XT, ST, SUB, 2, 2, 2>(a, st);
+  return launch_tile<XT, ST, SUB, 4, 2, 1>(a, st);
+}
+
 template <typename XT, typename ST>
-static hipError_t launch_w4(const W4Args& a, int group, int out_dtype, hipStream_t st) {
-  return out_dtype == SV_BF16 ? launch_w4<XT, ST, uint16_t>(a, group, st) : launch_w4<XT, ST, float>(a, group, st);
+static hipError_t launch_w4(const W4Args& a, int group, hipStream_t st) {
+  return group == 32 ? launch_w4<XT, ST, 4>(a, st) : group == 64 ? launch_w4<XT, ST, 2>(a, st) : launch_w4<XT, ST, 1>(a, st);
 }
 
 }  // namespace sl
@@ -69,16 +113,13 @@ extern "C" int spec_logits_w4(const void* hidden, int hidden_dtype, const uint8_
   a.N = N;
   a.G = K / group;
   a.gb = group >= 128 ? group / 128 : 1;
-  a.row_tiles = (R + 15) / 16;
-  if ((long long)a.row_tiles * ((N + 15) / 16) > 0x7FFFFFFFLL) return SV_ERR_UNSUPPORTED;
+  a.out_bf16 = out_dtype == SV_BF16;
   hipStream_t st = (hipStream_t)stream;
   hipError_t e;
   if (hidden_dtype == SV_BF16)
-    e = scale_dtype == SV_BF16 ? launch_w4<uint16_t, uint16_t>(a, group, out_dtype, st)
-                               : launch_w4<uint16_t, float>(a, group, out_dtype, st);
+    e = scale_dtype == SV_BF16 ? launch_w4<uint16_t, uint16_t>(a, group, st) : launch_w4<uint16_t, float>(a, group, st);
   else
-    e = scale_dtype == SV_BF16 ? launch_w4<float, uint16_t>(a, group, out_dtype, st)
-                               : launch_w4<float, float>(a, group, out_dtype, st);
+    e = scale_dtype == SV_BF16 ? launch_w4<float, uint16_t>(a, group, st) : launch_w4<float, float>(a, group, st);
   return hip_status(e);
 }
 
