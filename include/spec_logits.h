@@ -18,9 +18,9 @@
  * Conventions are those of spec_verify.h: device pointers are the caller's,
  * dense and row-major; work is enqueued on `stream` (a hipStream_t of the
  * current device, NULL = the default stream) and runs asynchronously, with no
- * host synchronisation, no allocation and no workspace, so every call may be
- * captured into a HIP graph and calls on different streams are independent as
- * far as their buffers are.  Argument errors are returned (SV_ERR_*) before
+ * host synchronisation and no allocation, so every call may be captured into a
+ * HIP graph, and calls on different streams are independent as far as their
+ * buffers are.  Argument errors are returned (SV_ERR_*) before
  * anything is enqueued.  Types are SV_BF16 and SV_FP32.  Bad data never makes
  * a kernel read or write outside the arrays; what it gives is said at each
  * call.
@@ -53,17 +53,21 @@ extern "C" {
  *  R, K, N  R >= 0 and <= SL_MAX_ROWS (R == 0 is a no-op), 32 <= K <= SL_MAX_K, 1 <= N <= SV_MAX_VOCAB.
  *  out      [R][N] bf16 or fp32 (out_dtype), aligned to its element; overlaps no input.
  *
+ *  workspace  device buffer of spec_logits_w4_workspace_bytes(hidden_dtype, group, R, K) bytes,
+ *           256-byte aligned (NULL where that is 0, as it is for few rows); it needs no
+ *           preparation and holds nothing after the call.  Calls that share one must be ordered.
+ *
  * The products are exact, the sums are held in float32 and rounded once, to
  * nearest even, at the end.  A row of `hidden` with a NaN or an infinity gives
  * a row of NaN (which the verify reports as invalid); other rows are not
  * affected.  A value of `hidden` beyond 2^115 may give NaN too, because the
  * sums inside a group are formed before its scale.
- * Results do not depend on R: a row of `hidden` gives the same bits alone and
- * among others -- within one of the two ranges R <= 16 and R > 16.
  * Returns SV_OK or a negative code (nothing enqueued).
  */
+size_t spec_logits_w4_workspace_bytes(int hidden_dtype, int group, int R, int K);
 int spec_logits_w4(const void* hidden, int hidden_dtype, const uint8_t* weights, const void* scales, int scale_dtype,
-                   const uint8_t* zeros, int group, int R, int K, int N, void* out, int out_dtype, void* stream);
+                   const uint8_t* zeros, int group, int R, int K, int N, void* out, int out_dtype, void* workspace,
+                   size_t workspace_bytes, void* stream);
 
 /*
  * The token history of S sequences (slots) over a vocabulary of V, in three

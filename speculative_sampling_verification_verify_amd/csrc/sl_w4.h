@@ -23,6 +23,7 @@ namespace sl {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 struct W4Args {
   const void* x;
@@ -33,12 +34,12 @@ struct W4Args {
   int R, K, N;
   int G;              // groups per weight row
   int gb;             // 128-k blocks per group (1 where the group is 32 or 64)
-  int row_tiles;      // tiles of MT * 16 rows
-  int rp;             // rows staged of a tile (a power of two, 16 unless R is smaller)
-  int kc;             // blocks of 128 k staged at a time
-  int KS;             // wavefronts that share a column tile
-  int per_xcd;        // workgroups of one XCD
   int out_bf16;
+  int rp;             // few rows: rows staged of a tile (a power of two, 16 unless R is smaller)
+  int row_tiles;      // more rows: tiles of MT * 16 rows
+  int per_xcd;        // workgroups of one XCD
+  char* xop;          // x in operand order and its sums per group (workspace)
+  char* xsum;
 };
 
 // The eight weights of a word as bf16 numbers 16 + w, in the order 0 4 1 5 2 6 3 7.
@@ -118,7 +119,7 @@ template <typename ST, int SUB, int U>
 struct W4Ahead {
   static constexpr int NS = U * SUB;                               // scales
   static constexpr int SW = (NS * (int)sizeof(ST) + 3) / 4, ZW = (NS + 3) / 4;
-  uint4 w[U];
+  u32x4 w[U];
   uint32_t s[SW], z[ZW];
 };
 
@@ -129,46 +130,90 @@ __device__ __forceinline__ float w4_get(const uint32_t* w, int i, const float*) 
 __device__ __forceinline__ void w4_put(uint32_t* w, int i, uint16_t v) { w[i >> 1] |= (uint32_t)v << (16 * (i & 1)); }
 __device__ __forceinline__ void w4_put(uint32_t* w, int i, float v) { w[i] = __float_as_uint(v); }
 
-// Blocks b .. b + U - 1 of weight row `row` (those before block `end`; the
-// others, and what lies beyond K, come as zeros).
-template <typename ST, int SUB, int U>
-__device__ __forceinline__ void w4_fetch(const W4Args& a, W4Ahead<ST, SUB, U>& h, int row, int quad, int b, int end) {
-  typedef W4Ahead<ST, SUB, U> Ahead;
-  const uint8_t* w = a.w + (size_t)row * (a.K / 2) + b * 64 + quad * 16;
-  const size_t srow = (size_t)row * a.G;
-  const ST* s = reinterpret_cast<const ST*>(a.s) + srow;
-  const bool whole = b + U <= end && (b + U) * 128 <= a.K;
-  if (whole) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) h.w[u] = *reinterpret_cast<const uint4*>(w + u * 64);
+// 16 + z of entry i.
+__device__ __forceinline__ float w4_shift(const W4Args& a, const uint32_t* z, int i) {
+  return 16.0f + (float)(a.z ? (z[i >> 2] >> (8 * (i & 3))) & 15u : 8u);
+}
+
+// Sixteen weight rows of a column tile: their first row (uniform over the
+// wavefront), and the lane's row from there on (the last one of the matrix
+// where the tile goes on behind it).
+struct W4Rows {
+  size_t first;
+  uint32_t local;
+};
+__device__ __forceinline__ W4Rows w4_rows(const W4Args& a, int n0, int l16) {
+  W4Rows r;
+  const int n = min(n0, a.N - 1);
+  r.first = (size_t)n;
+  r.local = (uint32_t)min(l16, a.N - 1 - n);
+  return r;
+}
+
+// The group of entry j (an entry: 128 / SUB of k).
+__device__ __forceinline__ uint32_t w4_group(const W4Args& a, int j) {
+  return (uint32_t)min(a.gb == 1 ? j : j / a.gb, a.G - 1);
+}
+
+// COUNT scales and, with ZEROS, zeros of the lane's row from entry j on.
+// TOGETHER: they lie side by side inside the row; else one by one, and entries
+// behind the row's end repeat its last.
+template <typename ST, int COUNT, bool ZEROS, bool TOGETHER, int SW, int ZW>
+__device__ __forceinline__ void w4_fetch_scales(const W4Args& a, uint32_t (&sw)[SW], uint32_t (&zw)[ZW], const W4Rows& r,
+                                                int j) {
+  const ST* s = reinterpret_cast<const ST*>(a.s) + r.first * a.G;
+  const uint8_t* z = a.z + r.first * a.G;
+  const uint32_t row = r.local * (uint32_t)a.G;
+  if (TOGETHER) {
+    __builtin_memcpy(sw, s + (row + (uint32_t)j), COUNT * sizeof(ST));
+    if (ZEROS && a.z) __builtin_memcpy(zw, z + (row + (uint32_t)j), COUNT);
   } else {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const bool in = b + u < end && (b + u) * 128 + quad * 32 < a.K;
-      h.w[u] = in ? *reinterpret_cast<const uint4*>(w + u * 64) : make_uint4(0, 0, 0, 0);
-    }
-  }
-  if (whole && a.gb == 1) {
-    __builtin_memcpy(h.s, s + b * SUB, Ahead::NS * sizeof(ST));
-    if (a.z) __builtin_memcpy(h.z, a.z + srow + b * SUB, Ahead::NS);
-  } else {
+    for (int i = 0; i < SW; ++i) sw[i] = 0;
 #pragma unroll
-    for (int i = 0; i < Ahead::SW; ++i) h.s[i] = 0;
+    for (int i = 0; i < COUNT; ++i) w4_put(sw, i, s[row + w4_group(a, j + i)]);
+    if (ZEROS && a.z) {
 #pragma unroll
-    for (int i = 0; i < Ahead::ZW; ++i) h.z[i] = 0;
+      for (int i = 0; i < ZW; ++i) zw[i] = 0;
 #pragma unroll
-    for (int i = 0; i < Ahead::NS; ++i) {
-      const int g = min(a.gb == 1 ? b * SUB + i : (b + i) / a.gb, a.G - 1);
-      w4_put(h.s, i, s[g]);
-      if (a.z) h.z[i >> 2] |= (uint32_t)a.z[srow + g] << (8 * (i & 3));
+      for (int i = 0; i < COUNT; ++i) zw[i >> 2] |= (uint32_t)z[row + w4_group(a, j + i)] << (8 * (i & 3));
     }
   }
 }
 
-// Block u of what was fetched, times the staged rows of block lb, onto tot.
-template <typename XT, typename ST, int SUB, int MT, int NT, int U>
-__device__ __forceinline__ void w4_block(const W4Args& a, const W4Ahead<ST, SUB, U> (&h)[NT], int u, int lb, const char* xs,
-                                         const float* sums, int frag, int loff, int quad, f32x4 (&tot)[MT][NT]) {
+// Blocks b .. b + U - 1 of NT column tiles.  What lies beyond K repeats the
+// row's end: it meets zeros of x.
+template <typename ST, int SUB, int U, int NT, bool ZEROS>
+__device__ __forceinline__ void w4_fetch(const W4Args& a, W4Ahead<ST, SUB, U> (&h)[NT], const W4Rows (&r)[NT], int quad, int b) {
+  constexpr int NS = W4Ahead<ST, SUB, U>::NS;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const uint8_t* w = a.w + r[nt].first * (size_t)(a.K / 2);
+    const uint32_t row = r[nt].local * (uint32_t)(a.K / 2);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      h[nt].w[u] = *reinterpret_cast<const u32x4*>(w + (row + (uint32_t)min((b + u) * 64 + quad * 16, a.K / 2 - 16)));
+  }
+  if (NS <= 2 && !ZEROS) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) w4_fetch_scales<ST, NS, ZEROS, false>(a, h[nt].s, h[nt].z, r[nt], b * SUB);
+  } else if (a.gb == 1 && (b + U) * SUB <= a.G) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) w4_fetch_scales<ST, NS, ZEROS, true>(a, h[nt].s, h[nt].z, r[nt], b * SUB);
+  } else {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) w4_fetch_scales<ST, NS, ZEROS, false>(a, h[nt].s, h[nt].z, r[nt], b * SUB);
+  }
+}
+
+// Block u of what was fetched, times the rows of x in LDS, onto tot.  x: the
+// operands of this block and lane, `mx` bytes from one row tile to the next,
+// `frag` from one operand to the next.  With SHIFT, 16 + z is taken out here:
+// xsum: the sums of this block and lane, `ms` bytes from one row tile to the
+// next.
+template <typename XT, typename ST, int SUB, int MT, int NT, int U, bool SHIFT>
+__device__ __forceinline__ void w4_block(const W4Args& a, const W4Ahead<ST, SUB, U> (&h)[NT], int u, const char* x, int mx,
+                                         int frag, const char* xsum, int ms, f32x4 (&tot)[MT][NT]) {
   constexpr int P = W4Hidden<XT>::PARTS;
   uint32_t d[NT][4];
 #pragma unroll
@@ -179,46 +224,76 @@ __device__ __forceinline__ void w4_block(const W4Args& a, const W4Ahead<ST, SUB,
     d[nt][3] = h[nt].w[u].w;
     if (SUB > 1) w4_transpose(d[nt]);
   }
-  f32x4 blk[MT][NT];
+  // The block's groups, IG operands of 32 k each.
+  constexpr int IG = 4 / SUB;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const bool begin = SUB == 4 || (SUB == 2 && !(i & 1)) || i == 0;
-    const bool end = SUB == 4 || (SUB == 2 && (i & 1)) || i == 3;
-    bf16x8 wv[NT];
+  for (int sg = 0; sg < SUB; ++sg) {
+    f32x4 blk[MT][NT];
+    if constexpr (SUB == 1) {
+      // Four operands a group: one after the other, over all tiles.
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) wv[nt] = w4_expand(d[nt][i]);
+      for (int i = 0; i < 4; ++i) {
+        bf16x8 wv[NT];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-#pragma unroll
-      for (int p = P - 1; p >= 0; --p) {
-        const bf16x8 f = *reinterpret_cast<const bf16x8*>(xs + (((lb * 4 + i) * P + p) * MT + m) * frag + loff);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          blk[m][nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              f, wv[nt], begin && p == P - 1 ? f32x4{0, 0, 0, 0} : blk[m][nt], 0, 0, 0);
-      }
-    }
-    if (end) {
-      const int sg = SUB == 4 ? i : SUB == 2 ? i >> 1 : 0, e = u * SUB + sg;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const float sc = w4_get(h[nt].s, e, (const ST*)nullptr);
-        const float zz = 16.0f + (float)(a.z ? (h[nt].z[e >> 2] >> (8 * (e & 3))) & 15u : 8u);
+        for (int nt = 0; nt < NT; ++nt) wv[nt] = w4_expand(d[nt][i]);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-          const f32x4 x4 = *reinterpret_cast<const f32x4*>(sums + ((lb * SUB + sg) * MT + m) * 16 + quad * 4);
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            tot[m][nt][r] = __builtin_fmaf(sc, __builtin_fmaf(-zz, x4[r], blk[m][nt][r]), tot[m][nt][r]);
+          for (int p = P - 1; p >= 0; --p) {
+            const bf16x8 f = *reinterpret_cast<const bf16x8*>(x + m * mx + (i * P + p) * frag);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              blk[m][nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                  f, wv[nt], i == 0 && p == P - 1 ? f32x4{0, 0, 0, 0} : blk[m][nt], 0, 0, 0);
+          }
+        }
+        if (MT * NT >= 16) __builtin_amdgcn_sched_barrier(0);   // no operand is loaded far ahead: registers are full
+      }
+    } else {
+      // One or two: a row tile after the other, whose results are used up at once.
+      bf16x8 wv[IG][NT];
+#pragma unroll
+      for (int i = 0; i < IG; ++i)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) wv[i][nt] = w4_expand(d[nt][sg * IG + i]);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+#pragma unroll
+        for (int i = 0; i < IG; ++i) {
+#pragma unroll
+          for (int p = P - 1; p >= 0; --p) {
+            const bf16x8 f = *reinterpret_cast<const bf16x8*>(x + m * mx + ((sg * IG + i) * P + p) * frag);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              blk[m][nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                  f, wv[i][nt], i == 0 && p == P - 1 ? f32x4{0, 0, 0, 0} : blk[m][nt], 0, 0, 0);
+          }
         }
       }
     }
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      f32x4 x4 = {0, 0, 0, 0};
+      if (SHIFT) x4 = *reinterpret_cast<const f32x4*>(xsum + m * ms + sg * 64);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int e = u * SUB + sg;
+        const float sc = w4_get(h[nt].s, e, (const ST*)nullptr);
+        const float zz = SHIFT ? w4_shift(a, h[nt].z, e) : 0.0f;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float v = SHIFT ? __builtin_fmaf(-zz, x4[r], blk[m][nt][r]) : blk[m][nt][r];
+          tot[m][nt][r] = __builtin_fmaf(sc, v, tot[m][nt][r]);
+        }
+      }
+    }
+    if (SUB > 1 && MT * NT >= 16) __builtin_amdgcn_sched_barrier(0);
   }
 }
 
 // Rows rt * MT * 16 .. of x, blocks b0 .. b1 - 1, into LDS as the products'
-// operands: [block][i][part][MT][quad][rp] 16 bytes, and their sums per group
-// (products with ones): [block][SUB][MT][16].  The caller has synchronised;
+// operands: [MT][block][i][part][quad][rp] 16 bytes, and their sums per group
+// (products with ones): [MT][block][SUB][16].  The caller has synchronised;
 // the rows are ready when this returns.
 template <typename XT, int SUB, int MT, int NTHR>
 __device__ __forceinline__ void w4_stage(const W4Args& a, int rt, int b0, int b1, int rp, char* xs, float* sums) {
@@ -242,7 +317,7 @@ __device__ __forceinline__ void w4_stage(const W4Args& a, int rt, int b0, int b1
     }
 #pragma unroll
     for (int p = 0; p < P; ++p)
-      *reinterpret_cast<bf16x8*>(xs + (((lb * 4 + i) * P + p) * MT + m) * frag + (qd * rp + r) * 16) = f[p];
+      *reinterpret_cast<bf16x8*>(xs + (((m * (b1 - b0) + lb) * 4 + i) * P + p) * frag + (qd * rp + r) * 16) = f[p];
   }
   __syncthreads();
   for (int q = wave; q < (b1 - b0) * MT; q += NTHR / 64) {
@@ -253,10 +328,10 @@ __device__ __forceinline__ void w4_stage(const W4Args& a, int rt, int b0, int b1
 #pragma unroll
       for (int p = P - 1; p >= 0; --p)
         sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-            *reinterpret_cast<const bf16x8*>(xs + (((lb * 4 + i) * P + p) * MT + m) * frag + loff), ones, sum, 0, 0, 0);
+            *reinterpret_cast<const bf16x8*>(xs + (((m * (b1 - b0) + lb) * 4 + i) * P + p) * frag + loff), ones, sum, 0, 0, 0);
       if (SUB == 4 || (SUB == 2 && (i & 1)) || i == 3) {
         const int sg = SUB == 4 ? i : SUB == 2 ? i >> 1 : 0;
-        if (l16 == 0) *reinterpret_cast<f32x4*>(sums + ((lb * SUB + sg) * MT + m) * 16 + quad * 4) = sum;
+        if (l16 == 0) *reinterpret_cast<f32x4*>(sums + ((m * (b1 - b0) + lb) * SUB + sg) * 16 + quad * 4) = sum;
         sum = f32x4{0, 0, 0, 0};
       }
     }
@@ -314,7 +389,8 @@ __global__ __launch_bounds__(W4S_NT) void w4_stream_kernel(W4Args a) {
   int ftile = tile, fstep = step;                                  // of what is fetched
 
   auto fetch = [&](W4Ahead<ST, SUB, U> (&h)[1]) {
-    w4_fetch<ST, SUB, U>(a, h[0], min(ftile * 16 + l16, a.N - 1), quad, fstep * U, nblk);
+    const W4Rows rows[1] = {w4_rows(a, ftile * 16, l16)};
+    w4_fetch<ST, SUB, U, 1, true>(a, h, rows, quad, fstep * U);
     if (++fstep == steps) {
       fstep = 0;
       ++ftile;
@@ -327,7 +403,11 @@ __global__ __launch_bounds__(W4S_NT) void w4_stream_kernel(W4Args a) {
   auto compute = [&](const W4Ahead<ST, SUB, U> (&h)[1]) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (step * U + u < nblk) w4_block<XT, ST, SUB, MT, 1, U>(a, h, u, step * U + u, smem, sums, frag, loff, quad, tot);
+      if (step * U + u < nblk) {
+        const int b = step * U + u;
+        w4_block<XT, ST, SUB, MT, 1, U, true>(a, h, u, smem + b * 4 * P * frag + loff, nblk * 4 * P * frag, frag,
+                                        reinterpret_cast<const char*>(sums + b * SUB * 16 + quad * 4), nblk * SUB * 64, tot);
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
     if (++step == steps) {
@@ -378,85 +458,198 @@ __global__ __launch_bounds__(W4S_NT) void w4_stream_kernel(W4Args a) {
 }
 
 // ---------------------------------------------------------------------------
-// More rows than that.
+// More rows than that: two launches.  The first puts the rows of x into the
+// order of the products' operands in a workspace (small: it stays in the L2);
+// the second is tiled over rows and columns.
+//
+// Here the 16 + z that a weight is too much costs more than it may: an
+// operation for each result and group.  So it is taken out by a product of its
+// own, tot = - sum_j t[n][j] * X[r][j] over the groups j, t = s * (16 + z): both
+// sides float32, split into three bf16 parts each, of whose products the six
+// above 2^-24 are formed -- 6 products for 32 groups, which have 32 to 128 of
+// their own.
 // ---------------------------------------------------------------------------
+
+__device__ __forceinline__ void w4_split(float v, uint32_t (&o)[3]) {
+  o[0] = __float_as_uint(v) & 0xFFFF0000u;
+  const float r = v - __uint_as_float(o[0]);
+  o[1] = __float_as_uint(r) & 0xFFFF0000u;
+  o[2] = __float_as_uint(r - __uint_as_float(o[1])) & 0xFFFF0000u;
+}
+
+// One workgroup per 16 rows and 128 k.  xop: [row tile][block][i][part] of 1 KB
+// ([quad][row] 16 bytes), the rows' values; xsum: [row tile][32 entries][part]
+// of 1 KB ([quad][row] 8 entries), their sums over each 128 / SUB of k.  Rows
+// beyond R, k beyond K and entries beyond the last are zeros.
+template <typename XT, int SUB>
+__global__ __launch_bounds__(256) void w4_order_kernel(W4Args a) {
+  constexpr int P = W4Hidden<XT>::PARTS;
+  __shared__ float part[16][17];
+  const int nblk = (a.K + 127) / 128, n32 = (nblk * SUB + 31) / 32;
+  const int rt = (int)(blockIdx.x / (unsigned)nblk), b = (int)(blockIdx.x % (unsigned)nblk);
+  const int r = threadIdx.x >> 4, u = threadIdx.x & 15;   // u: 8 of the block's 128 k
+  const int row = rt * 16 + r, k = b * 128 + u * 8;
+  const int i = SUB > 1 ? u >> 2 : u & 3, quad = SUB > 1 ? u & 3 : u >> 2;
+  bf16x8 f[P];
+  float sum = 0.0f;
+  if (row < a.R && k < a.K) {
+    const XT* x = reinterpret_cast<const XT*>(a.x) + (size_t)row * a.K + k;
+    W4Hidden<XT>::load(x, f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum += load_in(x + e);
+  } else {
+#pragma unroll
+    for (int p = 0; p < P; ++p) f[p] = __builtin_bit_cast(bf16x8, make_uint4(0, 0, 0, 0));
+  }
+  char* o = a.xop + (((size_t)blockIdx.x * 4 + i) * P) * 1024 + (quad * 16 + r) * 16;
+#pragma unroll
+  for (int p = 0; p < P; ++p) *reinterpret_cast<bf16x8*>(o + p * 1024) = f[p];
+  part[u][r] = sum;
+  __syncthreads();
+  // The block's entries, and behind the last block those up to the next 32.
+  const int j1 = b + 1 == nblk ? n32 * 32 : (b + 1) * SUB;
+  for (int q = threadIdx.x; q < (j1 - b * SUB) * 16; q += 256) {
+    const int sg = q >> 4, rr = q & 15, j = b * SUB + sg;
+    float t = 0.0f;
+    if (sg < SUB) {
+#pragma unroll
+      for (int e = 0; e < 16 / SUB; ++e) t += part[sg * (16 / SUB) + e][rr];
+    }
+    uint32_t v[3];
+    w4_split(t, v);
+#pragma unroll
+    for (int p = 0; p < 3; ++p)
+      *reinterpret_cast<uint16_t*>(a.xsum + (((size_t)rt * n32 + (j >> 5)) * 3 + p) * 1024 + (((j >> 3) & 3) * 16 + rr) * 16 +
+                                   (j & 7) * 2) = (uint16_t)(v[p] >> 16);
+  }
+}
+
+template <int NL> struct W4Stage { u32x4 v[NL]; };
+
 constexpr int W4_NT = 512;                 // threads per workgroup
 constexpr int W4_WAVES = W4_NT / 64;
-constexpr int W4_LDS = 64 * 1024;          // per workgroup: two fit a CU
 
-// MT * 16 rows of x by NT * 16 columns a wavefront.  A workgroup stages its
-// rows of x a chunk of K at a time and streams weights from memory into
-// registers, fetching one step ahead.  KS wavefronts share a column tile, each
-// with a part of K, and add up in LDS in a fixed order.
-template <typename XT, typename ST, int SUB, int MT, int NT, int U>
+// MT * 16 rows by NT * 16 columns a wavefront, eight wavefronts side by side.
+// Operands of x come KC blocks at a time through two LDS buffers: the next
+// chunk's are loaded into registers before this one is computed and written
+// after it, one barrier a chunk.  Weights go from memory to registers, U
+// blocks ahead.
+template <typename XT, typename ST, int SUB, int MT, int NT, int U, int KC>
 __global__ __launch_bounds__(W4_NT) __attribute__((amdgpu_waves_per_eu(2))) void w4_tile_kernel(W4Args a) {
   constexpr int P = W4Hidden<XT>::PARTS;
-  extern __shared__ __align__(16) char dsmem[];
-  char* smem = dsmem;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, l16 = lane & 15, quad = lane >> 4;
-  constexpr int rp = 16, frag = 64 * rp;
-  float* sums = reinterpret_cast<float*>(smem + a.kc * 4 * P * MT * frag);
-  const int loff = (quad * rp + l16) * 16;
-  const int nblk = (a.K + 127) / 128;
-  const int ks = a.KS > 1 ? wave % a.KS : 0, wn = a.KS > 1 ? wave / a.KS : wave;
-  const int cols = W4_WAVES / a.KS * NT * 16;
-  const long long sets = (long long)((a.N + cols - 1) / cols) * a.row_tiles;
-  const int chunks = (nblk + a.kc - 1) / a.kc;
+  constexpr int ROW = KC * 4 * P * 1024, OPS = MT * ROW;   // bytes of a chunk: one row tile's, all
+  constexpr int NL = OPS / 16 / W4_NT;                     // 16-byte loads a thread
+  static_assert(OPS % (16 * W4_NT) == 0 && KC % U == 0, "chunk does not fit the workgroup");
+  __shared__ __align__(16) char xs[2][OPS];
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, l16 = lane & 15, quad = lane >> 4;
+  const int nblk = (a.K + 127) / 128, chunks = (nblk + KC - 1) / KC;
+  const long long sets = (long long)((a.N + W4_WAVES * NT * 16 - 1) / (W4_WAVES * NT * 16)) * a.row_tiles;
   // The row tiles of a column tile run on one XCD, one after the other.
   const long long set = (long long)(blockIdx.x & 7) * a.per_xcd + (blockIdx.x >> 3);
   if (set >= sets) return;
   const int rt = (int)(set % a.row_tiles);
-  const int n0 = (int)(set / a.row_tiles) * cols + wn * NT * 16;
+  const int n0 = ((int)(set / a.row_tiles) * W4_WAVES + __builtin_amdgcn_readfirstlane(wave)) * NT * 16;
+  const uint32_t len = (uint32_t)nblk * 4 * P * 1024;      // operands of a row tile
+  const char* xop = a.xop + (size_t)rt * MT * len;
+  W4Rows rows[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) rows[nt] = w4_rows(a, n0 + nt * 16, l16);
+
+  W4Stage<NL> sr;
+  // Chunk c's operands, ROW bytes of each row tile (what a last, partial chunk
+  // lacks is neither read nor used).
+  auto stage_load = [&](W4Stage<NL>& g, int c) __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < NL; ++q) {
+      const int o = (q * W4_NT + tid) * 16, m = o / ROW;
+      const uint32_t at = (uint32_t)c * ROW + o % ROW;
+      g.v[q] = *reinterpret_cast<const u32x4*>(xop + ((size_t)m * len + (at < len ? at : 0)));
+    }
+  };
+  auto stage_write = [&](const W4Stage<NL>& g, int buf) __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < NL; ++q) *reinterpret_cast<u32x4*>(xs[buf] + (q * W4_NT + tid) * 16) = g.v[q];
+  };
+  auto fetch = [&](W4Ahead<ST, SUB, U> (&h)[NT], int b) __attribute__((always_inline)) {
+    w4_fetch<ST, SUB, U, NT, false>(a, h, rows, quad, b);
+  };
+
+  W4Ahead<ST, SUB, U> ha[NT], hb[NT];
+  fetch(ha, 0);
+  stage_load(sr, 0);
+
+  // tot = - sum_j s * (16 + z) * X.
   f32x4 tot[MT][NT];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) tot[m][nt] = f32x4{0, 0, 0, 0};
-
-  for (int c = 0; c < chunks; ++c) {
-    const int b0 = c * a.kc, b1 = min(nblk, b0 + a.kc);
-    // This wavefront's blocks of the chunk.
-    const int w0 = b0 + (b1 - b0) * ks / a.KS, w1 = b0 + (b1 - b0) * (ks + 1) / a.KS;
-    auto fetch = [&](W4Ahead<ST, SUB, U> (&h)[NT], int b) {
+  const int n32 = (nblk * SUB + 31) / 32;
+  for (int j = 0; j < n32; ++j) {
+    // The lane's eight entries of each column; behind the last they meet zeros.
+    uint32_t sw[NT][8 * sizeof(ST) / 4], zw[NT][2];
+    if (a.gb == 1 && (j + 1) * 32 <= a.G) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) w4_fetch<ST, SUB, U>(a, h[nt], min(n0 + nt * 16 + l16, a.N - 1), quad, b, w1);
-    };
-    auto compute = [&](const W4Ahead<ST, SUB, U> (&h)[NT], int b) {
+      for (int nt = 0; nt < NT; ++nt) w4_fetch_scales<ST, 8, true, true>(a, sw[nt], zw[nt], rows[nt], j * 32 + quad * 8);
+    } else {
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (b + u < w1) w4_block<XT, ST, SUB, MT, NT, U>(a, h, u, b + u - b0, smem, sums, frag, loff, quad, tot);
-    };
-    W4Ahead<ST, SUB, U> ha[NT], hb[NT];
-    if (w0 < w1) fetch(ha, w0);
-    __syncthreads();
-    w4_stage<XT, SUB, MT, W4_NT>(a, rt, b0, b1, rp, smem, sums);
-    for (int b = w0; b < w1; b += 2 * U) {
-      if (b + U < w1) fetch(hb, b + U);
-      compute(ha, b);
-      if (b + U >= w1) break;
-      if (b + 2 * U < w1) fetch(ha, b + 2 * U);
-      compute(hb, b + U);
+      for (int nt = 0; nt < NT; ++nt) w4_fetch_scales<ST, 8, true, false>(a, sw[nt], zw[nt], rows[nt], j * 32 + quad * 8);
+    }
+    bf16x8 t[NT][3];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      uint32_t w[3][4];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        uint32_t v[3];
+        w4_split(-w4_get(sw[nt], e, (const ST*)nullptr) * w4_shift(a, zw[nt], e), v);
+#pragma unroll
+        for (int p = 0; p < 3; ++p) w[p][e >> 1] = e & 1 ? w[p][e >> 1] | v[p] : v[p] >> 16;
+      }
+#pragma unroll
+      for (int p = 0; p < 3; ++p) t[nt][p] = __builtin_bit_cast(bf16x8, u32x4{w[p][0], w[p][1], w[p][2], w[p][3]});
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const char* xp = a.xsum + (((size_t)(rt * MT + m) * n32 + j) * 3) * 1024 + lane * 16;
+      bf16x8 x[3];
+#pragma unroll
+      for (int p = 0; p < 3; ++p) x[p] = *reinterpret_cast<const bf16x8*>(xp + p * 1024);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        f32x4 v = tot[m][nt];
+        v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[0], t[nt][2], v, 0, 0, 0);
+        v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[2], t[nt][0], v, 0, 0, 0);
+        v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[1], t[nt][1], v, 0, 0, 0);
+        v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[0], t[nt][1], v, 0, 0, 0);
+        v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[1], t[nt][0], v, 0, 0, 0);
+        v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[0], t[nt][0], v, 0, 0, 0);
+        tot[m][nt] = v;
+      }
     }
   }
 
-  if (a.KS > 1) {
-    // [wave][MT][NT][lane] partial sums over the staged rows; the first
-    // wavefront of a column tile adds them in order.
-    f32x4* red = reinterpret_cast<f32x4*>(smem);
-    __syncthreads();
+  stage_write(sr, 0);
+  __syncthreads();
+  const int nsteps = (nblk + U - 1) / U;
+  auto step = [&](const W4Ahead<ST, SUB, U> (&cur)[NT], W4Ahead<ST, SUB, U> (&nxt)[NT], int s) __attribute__((always_inline)) {
+    const int b = s * U, c = b / KC;
+    if (s + 1 < nsteps) fetch(nxt, b + U);
+    if (b % KC == 0 && c + 1 < chunks) stage_load(sr, c + 1);
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) red[((wave * MT + m) * NT + nt) * 64 + lane] = tot[m][nt];
-    __syncthreads();
-    if (ks != 0) return;
-    for (int o = 1; o < a.KS; ++o)
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) tot[m][nt] += red[(((wave + o) * MT + m) * NT + nt) * 64 + lane];
+    for (int u = 0; u < U; ++u)
+      if (b + u < nblk)
+        w4_block<XT, ST, SUB, MT, NT, U, false>(a, cur, u, xs[c & 1] + (b % KC + u) * 4 * P * 1024 + lane * 16, ROW, 1024,
+                                                nullptr, 0, tot);
+    if ((b + U) % KC == 0 && c + 1 < chunks) {
+      stage_write(sr, (c + 1) & 1);
+      __syncthreads();
+    }
+  };
+  for (int s = 0; s < nsteps; s += 2) {
+    step(ha, hb, s);
+    if (s + 1 < nsteps) step(hb, ha, s + 1);
   }
   w4_store<MT, NT>(a, rt, n0, tot);
 }
-
 }  // namespace sl

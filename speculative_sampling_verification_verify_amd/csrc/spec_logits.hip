@@ -25,12 +25,6 @@ static bool misaligned(const void* p, size_t n) { return (uintptr_t)p % n != 0; 
 // spec_logits_w4
 // ---------------------------------------------------------------------------
 
-// LDS bytes of a block of 128 k: its operands and the sums of its groups.
-template <typename XT>
-static int block_bytes(int sub, int mt, int rp) {
-  return 4 * W4Hidden<XT>::PARTS * mt * 64 * rp + sub * mt * 64;
-}
-
 constexpr int W4S_GRID = 256;   // one workgroup per CU
 
 template <typename XT, typename ST, int SUB, int MT>
@@ -41,66 +35,103 @@ static hipError_t launch_stream(W4Args a, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <typename XT, typename ST, int SUB, int MT, int NT, int U>
+template <typename XT, typename ST, int SUB, int MT, int NT, int U, int KC>
 static hipError_t launch_tile(W4Args a, hipStream_t st) {
-  const int nblk = (a.K + 127) / 128;
   a.row_tiles = (a.R + 16 * MT - 1) / (16 * MT);
-  const int per_block = block_bytes<XT>(SUB, MT, 16);
-  a.kc = W4_LDS / per_block;
-  if (a.kc > nblk) a.kc = nblk;
-  const int chunks = (nblk + a.kc - 1) / a.kc;
-  a.kc = (nblk + chunks - 1) / chunks;
-  // Few columns: wavefronts share them until there are about 2048.
-  a.KS = 1;
-  while (a.KS < W4_WAVES && 2 * a.KS * U <= a.kc &&
-         (long long)((a.N + 16 * NT - 1) / (16 * NT)) * a.row_tiles * a.KS * 2 <= 4096)
-    a.KS *= 2;
-  const int red = W4_WAVES * MT * NT * 1024;
-  int lds = a.kc * per_block;
-  if (a.KS > 1 && lds < red) lds = red;
-  const int cols = W4_WAVES / a.KS * NT * 16;
+  const int cols = W4_WAVES * NT * 16;
   const long long sets = (long long)((a.N + cols - 1) / cols) * a.row_tiles;
   if (sets > 0x7FFFFFF0LL) return hipErrorInvalidValue;
   a.per_xcd = (int)((sets + 7) / 8);
-  hipLaunchKernelGGL((w4_tile_kernel<XT, ST, SUB, MT, NT, U>), dim3((unsigned)a.per_xcd * 8), dim3(W4_NT), lds, st, a);
+  hipLaunchKernelGGL((w4_tile_kernel<XT, ST, SUB, MT, NT, U, KC>), dim3((unsigned)a.per_xcd * 8), dim3(W4_NT), 0, st, a);
   return hipGetLastError();
 }
 
+// The plan of a call, a function of its sizes and types alone.
+struct W4Plan {
+  int stream;        // row tiles of the streaming kernel (1, 2), 0: two launches
+  int rp;            // rows staged of a tile (streaming kernel)
+  int row_tiles16;   // row tiles of 16 in the workspace, whole workgroup tiles
+  size_t op_bytes, bytes;
+};
+
+// Row tiles of a workgroup of the two-launch form: four where the call has
+// more than 32 rows, but two with several groups to 128 k or fp32 hidden
+// states, whose registers four would spill.
+static int w4_tile_rows(int sub, int parts, int R) { return R > 32 && sub == 1 && parts == 1 ? 4 : 2; }
+
+static W4Plan w4_plan(int hidden_dtype, int group, int R, int K) {
+  W4Plan p;
+  memset(&p, 0, sizeof p);
+  const int sub = group == 32 ? 4 : group == 64 ? 2 : 1, nblk = (K + 127) / 128;
+  const int parts = hidden_dtype == SV_BF16 ? 1 : 3;
+  p.rp = 16;
+  while (p.rp / 2 >= R) p.rp /= 2;
+  const int mt = R <= 16 ? 1 : 2;
+  const long long lds = (long long)nblk * mt * (4 * parts * 64 * p.rp + sub * 64);
+  if (R <= 32 && lds <= W4S_LDS) {
+    p.stream = mt;
+    return p;
+  }
+  const int tile = w4_tile_rows(sub, parts, R);
+  p.row_tiles16 = (R + 16 * tile - 1) / (16 * tile) * tile;
+  p.op_bytes = (size_t)p.row_tiles16 * nblk * 4 * parts * 1024;
+  p.bytes = p.op_bytes + (size_t)p.row_tiles16 * ((nblk * sub + 31) / 32) * 3 * 1024;
+  return p;
+}
+
 template <typename XT, typename ST, int SUB>
-static hipError_t launch_w4(W4Args a, hipStream_t st) {
+static hipError_t launch_w4(W4Args a, const W4Plan& p, hipStream_t st) {
+  a.rp = p.rp;
+  if (p.stream == 1) return launch_stream<XT, ST, SUB, 1>(a, st);
+  if (p.stream == 2) return launch_stream<XT, ST, SUB, 2>(a, st);
   const int nblk = (a.K + 127) / 128;
-  a.rp = 16;
-  while (a.rp / 2 >= a.R) a.rp /= 2;
-  if (a.R <= 16 && (long long)nblk * block_bytes<XT>(SUB, 1, a.rp) <= W4S_LDS) return launch_stream<XT, ST, SUB, 1>(a, st);
-  if (a.R > 16 && a.R <= 32 && (long long)nblk * block_bytes<XT>(SUB, 2, 16) <= W4S_LDS)
-    return launch_stream<XT, ST, SUB, 2>(a, st);
-  if (a.R <= 16) return launch_tile<XT, ST, SUB, 1, 2, 2>(a, st);
-  if (a.R <= 32) return launch_tile<XT, ST, SUB, 2, 2, 2>(a, st);
-  return launch_tile<XT, ST, SUB, 4, 2, 1>(a, st);
+  hipLaunchKernelGGL((w4_order_kernel<XT, SUB>), dim3((unsigned)(p.row_tiles16 * nblk)), dim3(256), 0, st, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  // Wide column tiles where they still give every CU a workgroup.
+  constexpr int P = W4Hidden<XT>::PARTS, KC = P == 1 ? 2 : 1;   // blocks per chunk of x
+  const int mt = w4_tile_rows(SUB, P, a.R);
+  const bool wide = (long long)((a.N + 511) / 512) * (p.row_tiles16 / mt) >= 192;
+  if constexpr (SUB == 1 && P == 1)
+    if (mt == 4)
+      return wide ? launch_tile<XT, ST, SUB, 4, 4, 1, 1>(a, st) : launch_tile<XT, ST, SUB, 4, 1, KC, KC>(a, st);
+  return wide ? launch_tile<XT, ST, SUB, 2, 4, KC, KC>(a, st) : launch_tile<XT, ST, SUB, 2, 1, KC, KC>(a, st);
 }
 
 template <typename XT, typename ST>
-static hipError_t launch_w4(const W4Args& a, int group, hipStream_t st) {
-  return group == 32 ? launch_w4<XT, ST, 4>(a, st) : group == 64 ? launch_w4<XT, ST, 2>(a, st) : launch_w4<XT, ST, 1>(a, st);
+static hipError_t launch_w4(const W4Args& a, int group, const W4Plan& p, hipStream_t st) {
+  return group == 32 ? launch_w4<XT, ST, 4>(a, p, st) : group == 64 ? launch_w4<XT, ST, 2>(a, p, st) : launch_w4<XT, ST, 1>(a, p, st);
+}
+
+static int w4_sizes(int hidden_dtype, int group, int R, int K) {
+  if (!known(hidden_dtype) || R > SL_MAX_ROWS || K > SL_MAX_K) return SV_ERR_UNSUPPORTED;
+  if (R < 0 || K < 1 || group < 1) return SV_ERR_ARG;
+  if (group != 32 && group != 64 && group % 128 != 0) return SV_ERR_UNSUPPORTED;
+  return K % group != 0 ? SV_ERR_ARG : SV_OK;
 }
 
 }  // namespace sl
 
 using namespace sl;
 
+extern "C" size_t spec_logits_w4_workspace_bytes(int hidden_dtype, int group, int R, int K) {
+  return w4_sizes(hidden_dtype, group, R, K) == SV_OK && R > 0 ? w4_plan(hidden_dtype, group, R, K).bytes : 0;
+}
+
 extern "C" int spec_logits_w4(const void* hidden, int hidden_dtype, const uint8_t* weights, const void* scales,
                               int scale_dtype, const uint8_t* zeros, int group, int R, int K, int N, void* out,
-                              int out_dtype, void* stream) {
-  if (!known(hidden_dtype) || !known(scale_dtype) || !known(out_dtype)) return SV_ERR_UNSUPPORTED;
-  if (R > SL_MAX_ROWS || K > SL_MAX_K || N > SV_MAX_VOCAB) return SV_ERR_UNSUPPORTED;
-  if (R < 0 || K < 1 || N < 1 || group < 1) return SV_ERR_ARG;
-  if (group != 32 && group != 64 && group % 128 != 0) return SV_ERR_UNSUPPORTED;
-  if (K % group != 0) return SV_ERR_ARG;
+                              int out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!known(scale_dtype) || !known(out_dtype) || N > SV_MAX_VOCAB) return SV_ERR_UNSUPPORTED;
+  const int rc = w4_sizes(hidden_dtype, group, R, K);
+  if (rc != SV_OK) return rc;
+  if (N < 1) return SV_ERR_ARG;
   if (R == 0) return SV_OK;
   if (!hidden || !weights || !scales || !out) return SV_ERR_ARG;
   if (misaligned(hidden, 16) || misaligned(weights, 16) || misaligned(scales, size_of(scale_dtype)) ||
       misaligned(out, size_of(out_dtype)))
     return SV_ERR_ARG;
+  const W4Plan p = w4_plan(hidden_dtype, group, R, K);
+  if (p.bytes && (!workspace || workspace_bytes < p.bytes || misaligned(workspace, 256))) return SV_ERR_WORKSPACE;
   W4Args a;
   memset(&a, 0, sizeof a);
   a.x = hidden;
@@ -114,12 +145,14 @@ extern "C" int spec_logits_w4(const void* hidden, int hidden_dtype, const uint8_
   a.G = K / group;
   a.gb = group >= 128 ? group / 128 : 1;
   a.out_bf16 = out_dtype == SV_BF16;
+  a.xop = (char*)workspace;
+  a.xsum = (char*)workspace + p.op_bytes;
   hipStream_t st = (hipStream_t)stream;
   hipError_t e;
   if (hidden_dtype == SV_BF16)
-    e = scale_dtype == SV_BF16 ? launch_w4<uint16_t, uint16_t>(a, group, st) : launch_w4<uint16_t, float>(a, group, st);
+    e = scale_dtype == SV_BF16 ? launch_w4<uint16_t, uint16_t>(a, group, p, st) : launch_w4<uint16_t, float>(a, group, p, st);
   else
-    e = scale_dtype == SV_BF16 ? launch_w4<float, uint16_t>(a, group, st) : launch_w4<float, float>(a, group, st);
+    e = scale_dtype == SV_BF16 ? launch_w4<float, uint16_t>(a, group, p, st) : launch_w4<float, float>(a, group, p, st);
   return hip_status(e);
 }
 
@@ -245,6 +278,7 @@ extern "C" const char* spec_logits_strerror(int code) {
     case SV_OK: return "ok";
     case SV_ERR_ARG: return "invalid argument (null pointer, size out of range or misaligned pointer)";
     case SV_ERR_UNSUPPORTED: return "unsupported dtype, group or size";
+    case SV_ERR_WORKSPACE: return "workspace missing, too small or not 256-byte aligned";
     case SV_ERR_HIP: return g_errbuf[0] ? g_errbuf : "HIP error";
     default: return "unknown error code";
   }

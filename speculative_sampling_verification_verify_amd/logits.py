@@ -28,7 +28,7 @@ SL_MAX_DRAFT = 64
 SL_MAX_BIAS = 1024
 SL_MAX_MASKS = 1 << 20
 
-EXPORTED = ("spec_logits_w4", "spec_history_append", "spec_history_reset", "spec_process_logits",
+EXPORTED = ("spec_logits_w4", "spec_logits_w4_workspace_bytes", "spec_history_append", "spec_history_reset", "spec_process_logits",
             "spec_logits_strerror")
 
 _lib = None
@@ -47,8 +47,10 @@ def lib() -> ctypes.CDLL:
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(f"{LIB_PATH} is missing; build it with __graft_entry__.build()")
         L = ctypes.CDLL(LIB_PATH)
-        vp, i = ctypes.c_void_p, ctypes.c_int
-        L.spec_logits_w4.argtypes = [vp, i, vp, vp, i, vp, i, i, i, i, vp, i, vp]
+        vp, i, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+        L.spec_logits_w4_workspace_bytes.argtypes = [i, i, i, i]
+        L.spec_logits_w4_workspace_bytes.restype = sz
+        L.spec_logits_w4.argtypes = [vp, i, vp, vp, i, vp, i, i, i, i, vp, i, vp, sz, vp]
         L.spec_logits_w4.restype = i
         L.spec_history_append.argtypes = [vp, vp, vp, i, i, vp, vp, i, i, i, vp]
         L.spec_history_append.restype = i
@@ -106,7 +108,8 @@ def spec_logits_w4(hidden: torch.Tensor, weights: torch.Tensor, scales: torch.Te
 
     hidden [..., K] bf16 or fp32; weights [N, K / 2] uint8 (even k in the low
     four bits); scales [N, K / group] bf16 or fp32; zeros [N, K / group] uint8
-    or None (8).  `out` [..., N] or a new tensor of out_dtype (hidden's)."""
+    or None (8).  `out` [..., N] or a new tensor of out_dtype (hidden's).  The
+    workspace of many rows is torch's, allocated on the stream for the call."""
     if hidden.dim() < 1 or weights.dim() != 2 or scales.dim() != 2:
         raise ValueError("hidden must be [..., K], weights [N, K / 2] and scales [N, K / group]")
     dev = _gpu(hidden, "hidden")
@@ -125,8 +128,14 @@ def spec_logits_w4(hidden: torch.Tensor, weights: torch.Tensor, scales: torch.Te
     elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out: expected {out_dtype}, got {out.dtype}")
     _check(out, "out", out.dtype, (*hidden.shape[:-1], N), dev)
+    need = lib().spec_logits_w4_workspace_bytes(_dtype_code(hidden), K // G, R, K)
+    ws = None
+    if need:
+        with on_stream(stream):
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
     _call(lib().spec_logits_w4, "spec_logits_w4", dev, stream, _ptr(hidden), _dtype_code(hidden), _ptr(weights),
-          _ptr(scales), _dtype_code(scales), _ptr(zeros), K // G, R, K, N, _ptr(out), _dtype_code(out))
+          _ptr(scales), _dtype_code(scales), _ptr(zeros), K // G, R, K, N, _ptr(out), _dtype_code(out), _ptr(ws),
+          need)
     return out
 
 

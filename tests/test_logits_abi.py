@@ -11,8 +11,8 @@ import pytest
 import torch
 
 from speculative_sampling_verification_verify_amd import logits as L
-from speculative_sampling_verification_verify_amd.binding import (SV_BF16, SV_ERR_ARG, SV_ERR_UNSUPPORTED, SV_FP32,
-                                                                  SV_OK)
+from speculative_sampling_verification_verify_amd.binding import (SV_BF16, SV_ERR_ARG, SV_ERR_UNSUPPORTED, SV_ERR_WORKSPACE,
+                                                                  SV_FP32, SV_OK)
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 HEADER = os.path.join(ROOT, "include", "spec_logits.h")
@@ -40,8 +40,9 @@ def test_exports_every_declared_symbol():
         assert hasattr(_lib(), name), name
 
 
-def w4(x=FAKE, xt=SV_BF16, w=FAKE, s=FAKE, st=SV_BF16, z=None, group=64, R=2, K=128, N=10, out=FAKE, ot=SV_FP32):
-    return _lib().spec_logits_w4(x, xt, w, s, st, z, group, R, K, N, out, ot, None)
+def w4(x=FAKE, xt=SV_BF16, w=FAKE, s=FAKE, st=SV_BF16, z=None, group=64, R=2, K=128, N=10, out=FAKE, ot=SV_FP32,
+       ws=None, wsb=0):
+    return _lib().spec_logits_w4(x, xt, w, s, st, z, group, R, K, N, out, ot, ws, wsb, None)
 
 
 def test_w4_refusals():
@@ -56,6 +57,23 @@ def test_w4_refusals():
         assert w4(**{k: None}) == SV_ERR_ARG, k
     assert w4(x=FAKE + 8) == w4(w=FAKE + 4) == w4(s=FAKE + 1) == w4(out=FAKE + 2) == SV_ERR_ARG
     assert w4(s=FAKE + 2, st=SV_FP32) == w4(out=FAKE + 1, ot=SV_BF16) == SV_ERR_ARG
+
+
+def test_w4_workspace():
+    need = _lib().spec_logits_w4_workspace_bytes
+    assert need(SV_BF16, 128, 1, 4096) == need(SV_BF16, 128, 16, 4096) == need(SV_BF16, 128, 0, 4096) == 0
+    for bad in ((3, 128, 320, 4096), (SV_BF16, 16, 320, 4096), (SV_BF16, 128, -1, 4096), (SV_BF16, 128, 320, 100),
+                (SV_BF16, 128, 320, 1 << 20), (SV_BF16, 128, 1 << 21, 4096)):
+        assert need(*bad) == 0
+    for dt, size in ((SV_BF16, 2), (SV_FP32, 6)):       # an fp32 value takes three bf16 parts
+        for group in (32, 64, 128, 256):
+            for R in (17, 33, 320, 1000):
+                for K in (256, 4096, 65536):
+                    n = need(dt, group, R, K)
+                    assert n == 0 and R <= 32 or n >= R * K * size + R * K // min(group, 128) * 4, (dt, group, R, K)
+    n = need(SV_BF16, 64, 100, 128)
+    for ws, wsb in ((None, n), (FAKE, n - 1), (FAKE + 128, n)):
+        assert w4(R=100, ws=ws, wsb=wsb) == SV_ERR_WORKSPACE
 
 
 def test_history_refusals():
