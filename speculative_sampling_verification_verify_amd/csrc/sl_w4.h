@@ -43,12 +43,17 @@ struct W4Args {
 };
 
 // The eight weights of a word as bf16 numbers 16 + w, in the order 0 4 1 5 2 6 3 7.
+// The constants are kept in registers (one operand of an instruction may be a
+// constant), so that a pair takes a shift and a v_and_or_b32.
 __device__ __forceinline__ bf16x8 w4_expand(uint32_t w) {
-  uint4 v;
-  v.x = ((w << 3) & 0x00780078u) | 0x41804180u;
-  v.y = ((w >> 1) & 0x00780078u) | 0x41804180u;
-  v.z = ((w >> 5) & 0x00780078u) | 0x41804180u;
-  v.w = ((w >> 9) & 0x00780078u) | 0x41804180u;
+  uint32_t mask = 0x00780078u, base = 0x41804180u;
+  asm("" : "+s"(mask));
+  asm("" : "+v"(base));
+  u32x4 v;
+  v.x = ((w << 3) & mask) | base;
+  v.y = ((w >> 1) & mask) | base;
+  v.z = ((w >> 5) & mask) | base;
+  v.w = ((w >> 9) & mask) | base;
   return __builtin_bit_cast(bf16x8, v);
 }
 
@@ -470,6 +475,9 @@ __global__ __launch_bounds__(W4S_NT) void w4_stream_kernel(W4Args a) {
 // their own.
 // ---------------------------------------------------------------------------
 
+// Blocks of 128 k in the workspace: an even number.
+__host__ __device__ __forceinline__ int w4_blocks(int K) { return (K + 255) / 256 * 2; }
+
 __device__ __forceinline__ void w4_split(float v, uint32_t (&o)[3]) {
   o[0] = __float_as_uint(v) & 0xFFFF0000u;
   const float r = v - __uint_as_float(o[0]);
@@ -480,12 +488,13 @@ __device__ __forceinline__ void w4_split(float v, uint32_t (&o)[3]) {
 // One workgroup per 16 rows and 128 k.  xop: [row tile][block][i][part] of 1 KB
 // ([quad][row] 16 bytes), the rows' values; xsum: [row tile][32 entries][part]
 // of 1 KB ([quad][row] 8 entries), their sums over each 128 / SUB of k.  Rows
-// beyond R, k beyond K and entries beyond the last are zeros.
+// beyond R, k beyond K and entries beyond the last are zeros, so that the
+// product needs no checks: what it reads of the weights there meets zeros.
 template <typename XT, int SUB>
 __global__ __launch_bounds__(256) void w4_order_kernel(W4Args a) {
   constexpr int P = W4Hidden<XT>::PARTS;
   __shared__ float part[16][17];
-  const int nblk = (a.K + 127) / 128, n32 = (nblk * SUB + 31) / 32;
+  const int nblk = w4_blocks(a.K), n32 = (nblk * SUB + 31) / 32;
   const int rt = (int)(blockIdx.x / (unsigned)nblk), b = (int)(blockIdx.x % (unsigned)nblk);
   const int r = threadIdx.x >> 4, u = threadIdx.x & 15;   // u: 8 of the block's 128 k
   const int row = rt * 16 + r, k = b * 128 + u * 8;
@@ -542,7 +551,7 @@ __global__ __launch_bounds__(W4_NT) __attribute__((amdgpu_waves_per_eu(2))) void
   static_assert(OPS % (16 * W4_NT) == 0 && KC % U == 0, "chunk does not fit the workgroup");
   __shared__ __align__(16) char xs[2][OPS];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, l16 = lane & 15, quad = lane >> 4;
-  const int nblk = (a.K + 127) / 128, chunks = (nblk + KC - 1) / KC;
+  const int nblk = w4_blocks(a.K);
   const long long sets = (long long)((a.N + W4_WAVES * NT * 16 - 1) / (W4_WAVES * NT * 16)) * a.row_tiles;
   // The row tiles of a column tile run on one XCD, one after the other.
   const long long set = (long long)(blockIdx.x & 7) * a.per_xcd + (blockIdx.x >> 3);
@@ -556,14 +565,13 @@ __global__ __launch_bounds__(W4_NT) __attribute__((amdgpu_waves_per_eu(2))) void
   for (int nt = 0; nt < NT; ++nt) rows[nt] = w4_rows(a, n0 + nt * 16, l16);
 
   W4Stage<NL> sr;
-  // Chunk c's operands, ROW bytes of each row tile (what a last, partial chunk
-  // lacks is neither read nor used).
+  // Chunk c's operands, ROW bytes of each row tile (behind the last chunk, the first again).
   auto stage_load = [&](W4Stage<NL>& g, int c) __attribute__((always_inline)) {
 #pragma unroll
     for (int q = 0; q < NL; ++q) {
       const int o = (q * W4_NT + tid) * 16, m = o / ROW;
-      const uint32_t at = (uint32_t)c * ROW + o % ROW;
-      g.v[q] = *reinterpret_cast<const u32x4*>(xop + ((size_t)m * len + (at < len ? at : 0)));
+      const uint32_t at = (uint32_t)c * ROW < len ? (uint32_t)c * ROW : 0u;
+      g.v[q] = *reinterpret_cast<const u32x4*>(xop + at + ((uint32_t)m * len + o % ROW));
     }
   };
   auto stage_write = [&](const W4Stage<NL>& g, int buf) __attribute__((always_inline)) {
@@ -631,24 +639,25 @@ __global__ __launch_bounds__(W4_NT) __attribute__((amdgpu_waves_per_eu(2))) void
 
   stage_write(sr, 0);
   __syncthreads();
-  const int nsteps = (nblk + U - 1) / U;
+  const int nsteps = nblk / U;
   auto step = [&](const W4Ahead<ST, SUB, U> (&cur)[NT], W4Ahead<ST, SUB, U> (&nxt)[NT], int s) __attribute__((always_inline)) {
     const int b = s * U, c = b / KC;
-    if (s + 1 < nsteps) fetch(nxt, b + U);
-    if (b % KC == 0 && c + 1 < chunks) stage_load(sr, c + 1);
+    fetch(nxt, min(b + U, nblk - U));
+    if (b % KC == 0) stage_load(sr, c + 1);
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (b + u < nblk)
-        w4_block<XT, ST, SUB, MT, NT, U, false>(a, cur, u, xs[c & 1] + (b % KC + u) * 4 * P * 1024 + lane * 16, ROW, 1024,
-                                                nullptr, 0, tot);
-    if ((b + U) % KC == 0 && c + 1 < chunks) {
+      w4_block<XT, ST, SUB, MT, NT, U, false>(a, cur, u, xs[c & 1] + (b % KC + u) * 4 * P * 1024 + lane * 16, ROW, 1024, nullptr,
+                                              0, tot);
+    if ((b + U) % KC == 0) {
       stage_write(sr, (c + 1) & 1);
       __syncthreads();
     }
   };
-  for (int s = 0; s < nsteps; s += 2) {
+  for (int s = 0;;) {
     step(ha, hb, s);
-    if (s + 1 < nsteps) step(hb, ha, s + 1);
+    if (U == 2 && s + 1 == nsteps) break;
+    step(hb, ha, s + 1);
+    if ((s += 2) >= nsteps) break;
   }
   w4_store<MT, NT>(a, rt, n0, tot);
 }

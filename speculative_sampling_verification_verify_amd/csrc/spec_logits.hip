@@ -74,8 +74,9 @@ static W4Plan w4_plan(int hidden_dtype, int group, int R, int K) {
   }
   const int tile = w4_tile_rows(sub, parts, R);
   p.row_tiles16 = (R + 16 * tile - 1) / (16 * tile) * tile;
-  p.op_bytes = (size_t)p.row_tiles16 * nblk * 4 * parts * 1024;
-  p.bytes = p.op_bytes + (size_t)p.row_tiles16 * ((nblk * sub + 31) / 32) * 3 * 1024;
+  const int blocks = w4_blocks(K);
+  p.op_bytes = (size_t)p.row_tiles16 * blocks * 4 * parts * 1024;
+  p.bytes = p.op_bytes + (size_t)p.row_tiles16 * ((blocks * sub + 31) / 32) * 3 * 1024;
   return p;
 }
 
@@ -84,8 +85,7 @@ static hipError_t launch_w4(W4Args a, const W4Plan& p, hipStream_t st) {
   a.rp = p.rp;
   if (p.stream == 1) return launch_stream<XT, ST, SUB, 1>(a, st);
   if (p.stream == 2) return launch_stream<XT, ST, SUB, 2>(a, st);
-  const int nblk = (a.K + 127) / 128;
-  hipLaunchKernelGGL((w4_order_kernel<XT, SUB>), dim3((unsigned)(p.row_tiles16 * nblk)), dim3(256), 0, st, a);
+  hipLaunchKernelGGL((w4_order_kernel<XT, SUB>), dim3((unsigned)(p.row_tiles16 * w4_blocks(a.K))), dim3(256), 0, st, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   // Wide column tiles where they still give every CU a workgroup.
