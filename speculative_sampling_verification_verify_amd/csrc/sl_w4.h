@@ -23,6 +23,7 @@ namespace sl {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 struct W4Args {
@@ -471,7 +472,7 @@ __global__ __launch_bounds__(W4S_NT) void w4_stream_kernel(W4Args a) {
 // operation for each result and group.  So it is taken out by a product of its
 // own, tot = - sum_j t[n][j] * X[r][j] over the groups j, t = s * (16 + z): both
 // sides float32, split into three bf16 parts each, of whose products the six
-// above 2^-24 are formed -- 6 products for 32 groups, which have 32 to 128 of
+// above 2^-24 are formed -- 6 products for 16 groups, which have 32 to 128 of
 // their own.
 // ---------------------------------------------------------------------------
 
@@ -485,20 +486,44 @@ __device__ __forceinline__ void w4_split(float v, uint32_t (&o)[3]) {
   o[2] = __float_as_uint(r - __uint_as_float(o[1])) & 0xFFFF0000u;
 }
 
-// One workgroup per 16 rows and 128 k.  xop: [row tile][block][i][part] of 1 KB
-// ([quad][row] 16 bytes), the rows' values; xsum: [row tile][32 entries][part]
-// of 1 KB ([quad][row] 8 entries), their sums over each 128 / SUB of k.  Rows
-// beyond R, k beyond K and entries beyond the last are zeros, so that the
-// product needs no checks: what it reads of the weights there meets zeros.
+// The products here are v_mfma_f32_32x32x16_bf16 (lane l holds row / column
+// l % 32 of either operand at k = 8 * (l / 32) + 0..7, and rows 8 * (r / 4) +
+// 4 * (l / 32) + r % 4 of column l % 32 of the result): with two wavefronts on
+// a SIMD and two vector operations for each 16 x 16 x 32 of product between
+// them, they were measured at 2170 TFLOP/s over the chip, 16x16x32 at 1260.
+//
+// A block of 128 k is eight products t.  A lane's two 16-byte loads of a weight
+// row hold 32 consecutive k each, at 64 j + 32 h (h = l / 32); word i of load j
+// is product t = 4 j + i, at k = 64 j + 32 h + 8 i.  With groups of 32 the
+// halves of the wavefront exchange words, so that a product stays in one group:
+// t = 4 j + 2 g + q at k = 64 j + 32 g + 16 q + 8 h.
+
+template <int SUB>
+__device__ __forceinline__ void w4_place(int u, int& t, int& h) {   // of the block's k = 8 u
+  if (SUB == 4) {
+    t = (u >> 3) * 4 + ((u >> 2) & 1) * 2 + ((u >> 1) & 1);
+    h = u & 1;
+  } else {
+    t = (u >> 3) * 4 + (u & 3);
+    h = (u >> 2) & 1;
+  }
+}
+
+// One workgroup per 32 rows and 128 k.  xop: [row tile][block][t][part] of 1 KB
+// ([h][row] 16 bytes), the rows' values; xsum: [row tile][16 entries][part] of
+// 1 KB ([h][row] 8 entries), their sums over each 128 / SUB of k.  Rows beyond
+// R, k beyond K and entries beyond the last are zeros, so that the product
+// needs no checks: what it reads of the weights there meets zeros.
 template <typename XT, int SUB>
-__global__ __launch_bounds__(256) void w4_order_kernel(W4Args a) {
+__global__ __launch_bounds__(512) void w4_order_kernel(W4Args a) {
   constexpr int P = W4Hidden<XT>::PARTS;
-  __shared__ float part[16][17];
-  const int nblk = w4_blocks(a.K), n32 = (nblk * SUB + 31) / 32;
+  __shared__ float part[16][33];
+  const int nblk = w4_blocks(a.K), n16 = (nblk * SUB + 15) / 16;
   const int rt = (int)(blockIdx.x / (unsigned)nblk), b = (int)(blockIdx.x % (unsigned)nblk);
   const int r = threadIdx.x >> 4, u = threadIdx.x & 15;   // u: 8 of the block's 128 k
-  const int row = rt * 16 + r, k = b * 128 + u * 8;
-  const int i = SUB > 1 ? u >> 2 : u & 3, quad = SUB > 1 ? u & 3 : u >> 2;
+  const int row = rt * 32 + r, k = b * 128 + u * 8;
+  int t, h;
+  w4_place<SUB>(u, t, h);
   bf16x8 f[P];
   float sum = 0.0f;
   if (row < a.R && k < a.K) {
@@ -508,17 +533,17 @@ __global__ __launch_bounds__(256) void w4_order_kernel(W4Args a) {
     for (int e = 0; e < 8; ++e) sum += load_in(x + e);
   } else {
 #pragma unroll
-    for (int p = 0; p < P; ++p) f[p] = __builtin_bit_cast(bf16x8, make_uint4(0, 0, 0, 0));
+    for (int p = 0; p < P; ++p) f[p] = __builtin_bit_cast(bf16x8, u32x4{0, 0, 0, 0});
   }
-  char* o = a.xop + (((size_t)blockIdx.x * 4 + i) * P) * 1024 + (quad * 16 + r) * 16;
+  char* o = a.xop + (((size_t)blockIdx.x * 8 + t) * P) * 1024 + (h * 32 + r) * 16;
 #pragma unroll
   for (int p = 0; p < P; ++p) *reinterpret_cast<bf16x8*>(o + p * 1024) = f[p];
   part[u][r] = sum;
   __syncthreads();
-  // The block's entries, and behind the last block those up to the next 32.
-  const int j1 = b + 1 == nblk ? n32 * 32 : (b + 1) * SUB;
-  for (int q = threadIdx.x; q < (j1 - b * SUB) * 16; q += 256) {
-    const int sg = q >> 4, rr = q & 15, j = b * SUB + sg;
+  // The block's entries, and behind the last block those up to the next 16.
+  const int j1 = b + 1 == nblk ? n16 * 16 : (b + 1) * SUB;
+  for (int q = threadIdx.x; q < (j1 - b * SUB) * 32; q += 512) {
+    const int sg = q >> 5, rr = q & 31, j = b * SUB + sg;
     float t = 0.0f;
     if (sg < SUB) {
 #pragma unroll
@@ -528,17 +553,26 @@ __global__ __launch_bounds__(256) void w4_order_kernel(W4Args a) {
     w4_split(t, v);
 #pragma unroll
     for (int p = 0; p < 3; ++p)
-      *reinterpret_cast<uint16_t*>(a.xsum + (((size_t)rt * n32 + (j >> 5)) * 3 + p) * 1024 + (((j >> 3) & 3) * 16 + rr) * 16 +
+      *reinterpret_cast<uint16_t*>(a.xsum + (((size_t)rt * n16 + (j >> 4)) * 3 + p) * 1024 + (((j >> 3) & 1) * 32 + rr) * 16 +
                                    (j & 7) * 2) = (uint16_t)(v[p] >> 16);
   }
 }
 
 template <int NL> struct W4Stage { u32x4 v[NL]; };
 
+// What a wavefront fetches ahead of one column tile of 32: U blocks of 128 k.
+template <typename ST, int SUB, int U>
+struct W4Wide {
+  static constexpr int NS = U * SUB;
+  static constexpr int SW = (NS * (int)sizeof(ST) + 3) / 4;
+  u32x4 w[U][2];
+  uint32_t s[SW];
+};
+
 constexpr int W4_NT = 512;                 // threads per workgroup
 constexpr int W4_WAVES = W4_NT / 64;
 
-// MT * 16 rows by NT * 16 columns a wavefront, eight wavefronts side by side.
+// MT * 32 rows by NT * 32 columns a wavefront, eight wavefronts side by side.
 // Operands of x come KC blocks at a time through two LDS buffers: the next
 // chunk's are loaded into registers before this one is computed and written
 // after it, one barrier a chunk.  Weights go from memory to registers, U
@@ -546,23 +580,24 @@ constexpr int W4_WAVES = W4_NT / 64;
 template <typename XT, typename ST, int SUB, int MT, int NT, int U, int KC>
 __global__ __launch_bounds__(W4_NT) __attribute__((amdgpu_waves_per_eu(2))) void w4_tile_kernel(W4Args a) {
   constexpr int P = W4Hidden<XT>::PARTS;
-  constexpr int ROW = KC * 4 * P * 1024, OPS = MT * ROW;   // bytes of a chunk: one row tile's, all
+  constexpr int ROW = KC * 8 * P * 1024, OPS = MT * ROW;   // bytes of a chunk: one row tile's, all
   constexpr int NL = OPS / 16 / W4_NT;                     // 16-byte loads a thread
   static_assert(OPS % (16 * W4_NT) == 0 && KC % U == 0, "chunk does not fit the workgroup");
+  typedef W4Wide<ST, SUB, U> Wide;
   __shared__ __align__(16) char xs[2][OPS];
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, l16 = lane & 15, quad = lane >> 4;
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, l32 = lane & 31, half = lane >> 5;
   const int nblk = w4_blocks(a.K);
-  const long long sets = (long long)((a.N + W4_WAVES * NT * 16 - 1) / (W4_WAVES * NT * 16)) * a.row_tiles;
+  const long long sets = (long long)((a.N + W4_WAVES * NT * 32 - 1) / (W4_WAVES * NT * 32)) * a.row_tiles;
   // The row tiles of a column tile run on one XCD, one after the other.
   const long long set = (long long)(blockIdx.x & 7) * a.per_xcd + (blockIdx.x >> 3);
   if (set >= sets) return;
   const int rt = (int)(set % a.row_tiles);
-  const int n0 = ((int)(set / a.row_tiles) * W4_WAVES + __builtin_amdgcn_readfirstlane(wave)) * NT * 16;
-  const uint32_t len = (uint32_t)nblk * 4 * P * 1024;      // operands of a row tile
+  const int n0 = ((int)(set / a.row_tiles) * W4_WAVES + __builtin_amdgcn_readfirstlane(wave)) * NT * 32;
+  const uint32_t len = (uint32_t)nblk * 8 * P * 1024;      // operands of a row tile
   const char* xop = a.xop + (size_t)rt * MT * len;
   W4Rows rows[NT];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) rows[nt] = w4_rows(a, n0 + nt * 16, l16);
+  for (int nt = 0; nt < NT; ++nt) rows[nt] = w4_rows(a, n0 + nt * 32, l32);
 
   W4Stage<NL> sr;
   // Chunk c's operands, ROW bytes of each row tile (behind the last chunk, the first again).
@@ -578,30 +613,61 @@ __global__ __launch_bounds__(W4_NT) __attribute__((amdgpu_waves_per_eu(2))) void
 #pragma unroll
     for (int q = 0; q < NL; ++q) *reinterpret_cast<u32x4*>(xs[buf] + (q * W4_NT + tid) * 16) = g.v[q];
   };
-  auto fetch = [&](W4Ahead<ST, SUB, U> (&h)[NT], int b) __attribute__((always_inline)) {
-    w4_fetch<ST, SUB, U, NT, false>(a, h, rows, quad, b);
+  auto fetch = [&](Wide (&g)[NT], int b) __attribute__((always_inline)) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const uint8_t* w = a.w + rows[nt].first * (size_t)(a.K / 2);
+      const uint32_t row = rows[nt].local * (uint32_t)(a.K / 2);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          g[nt].w[u][j] =
+              *reinterpret_cast<const u32x4*>(w + (row + (uint32_t)min((b + u) * 64 + j * 32 + half * 16, a.K / 2 - 16)));
+    }
+    if (Wide::NS <= 2) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        uint32_t none[1];
+        w4_fetch_scales<ST, Wide::NS, false, false>(a, g[nt].s, none, rows[nt], b * SUB);
+      }
+    } else if (a.gb == 1 && (b + U) * SUB <= a.G) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        uint32_t none[1];
+        w4_fetch_scales<ST, Wide::NS, false, true>(a, g[nt].s, none, rows[nt], b * SUB);
+      }
+    } else {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        uint32_t none[1];
+        w4_fetch_scales<ST, Wide::NS, false, false>(a, g[nt].s, none, rows[nt], b * SUB);
+      }
+    }
   };
 
-  W4Ahead<ST, SUB, U> ha[NT], hb[NT];
+  Wide ha[NT], hb[NT];
   fetch(ha, 0);
   stage_load(sr, 0);
 
   // tot = - sum_j s * (16 + z) * X.
-  f32x4 tot[MT][NT];
+  f32x16 tot[MT][NT];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) tot[m][nt] = f32x4{0, 0, 0, 0};
-  const int n32 = (nblk * SUB + 31) / 32;
-  for (int j = 0; j < n32; ++j) {
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) tot[m][nt][r] = 0.0f;
+  const int n16 = (nblk * SUB + 15) / 16;
+  for (int j = 0; j < n16; ++j) {
     // The lane's eight entries of each column; behind the last they meet zeros.
     uint32_t sw[NT][8 * sizeof(ST) / 4], zw[NT][2];
-    if (a.gb == 1 && (j + 1) * 32 <= a.G) {
+    if (a.gb == 1 && (j + 1) * 16 <= a.G) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) w4_fetch_scales<ST, 8, true, true>(a, sw[nt], zw[nt], rows[nt], j * 32 + quad * 8);
+      for (int nt = 0; nt < NT; ++nt) w4_fetch_scales<ST, 8, true, true>(a, sw[nt], zw[nt], rows[nt], j * 16 + half * 8);
     } else {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) w4_fetch_scales<ST, 8, true, false>(a, sw[nt], zw[nt], rows[nt], j * 32 + quad * 8);
+      for (int nt = 0; nt < NT; ++nt) w4_fetch_scales<ST, 8, true, false>(a, sw[nt], zw[nt], rows[nt], j * 16 + half * 8);
     }
     bf16x8 t[NT][3];
 #pragma unroll
@@ -619,35 +685,84 @@ __global__ __launch_bounds__(W4_NT) __attribute__((amdgpu_waves_per_eu(2))) void
     }
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      const char* xp = a.xsum + (((size_t)(rt * MT + m) * n32 + j) * 3) * 1024 + lane * 16;
+      const char* xp = a.xsum + (((size_t)(rt * MT + m) * n16 + j) * 3) * 1024 + lane * 16;
       bf16x8 x[3];
 #pragma unroll
       for (int p = 0; p < 3; ++p) x[p] = *reinterpret_cast<const bf16x8*>(xp + p * 1024);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        f32x4 v = tot[m][nt];
-        v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[0], t[nt][2], v, 0, 0, 0);
-        v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[2], t[nt][0], v, 0, 0, 0);
-        v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[1], t[nt][1], v, 0, 0, 0);
-        v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[0], t[nt][1], v, 0, 0, 0);
-        v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[1], t[nt][0], v, 0, 0, 0);
-        v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[0], t[nt][0], v, 0, 0, 0);
+        f32x16 v = tot[m][nt];
+        v = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[0], t[nt][2], v, 0, 0, 0);
+        v = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[2], t[nt][0], v, 0, 0, 0);
+        v = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[1], t[nt][1], v, 0, 0, 0);
+        v = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[0], t[nt][1], v, 0, 0, 0);
+        v = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[1], t[nt][0], v, 0, 0, 0);
+        v = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[0], t[nt][0], v, 0, 0, 0);
         tot[m][nt] = v;
       }
     }
   }
 
+  // Block u of what was fetched, times its rows of x (this lane's in x), onto tot.
+  auto block = [&](const Wide (&g)[NT], int u, const char* x) __attribute__((always_inline)) {
+    constexpr int TG = 8 / SUB;   // products of a group
+#pragma unroll
+    for (int sg = 0; sg < SUB; ++sg) {
+      f32x16 blk[MT][NT];
+#pragma unroll
+      for (int q = 0; q < TG; ++q) {
+        const int t = sg * TG + q, j = t >> 2;
+        bf16x8 wv[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          uint32_t d;
+          if constexpr (SUB == 4) {
+            const auto pair = __builtin_amdgcn_permlane32_swap(g[nt].w[u][j][2 * q], g[nt].w[u][j][2 * q + 1], false, false);
+            d = pair[sg & 1];
+          } else {
+            d = g[nt].w[u][j][t & 3];
+          }
+          wv[nt] = w4_expand(d);
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+#pragma unroll
+          for (int p = P - 1; p >= 0; --p) {
+            const bf16x8 f = *reinterpret_cast<const bf16x8*>(x + m * ROW + (t * P + p) * 1024);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              if (q == 0 && p == P - 1) {
+                f32x16 zero;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) zero[r] = 0.0f;
+                blk[m][nt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, wv[nt], zero, 0, 0, 0);
+              } else {
+                blk[m][nt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, wv[nt], blk[m][nt], 0, 0, 0);
+              }
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float sc = w4_get(g[nt].s, u * SUB + sg, (const ST*)nullptr);
+#pragma unroll
+          for (int r = 0; r < 16; ++r) tot[m][nt][r] = __builtin_fmaf(sc, blk[m][nt][r], tot[m][nt][r]);
+        }
+    }
+  };
+
   stage_write(sr, 0);
   __syncthreads();
   const int nsteps = nblk / U;
-  auto step = [&](const W4Ahead<ST, SUB, U> (&cur)[NT], W4Ahead<ST, SUB, U> (&nxt)[NT], int s) __attribute__((always_inline)) {
+  auto step = [&](const Wide (&cur)[NT], Wide (&nxt)[NT], int s) __attribute__((always_inline)) {
     const int b = s * U, c = b / KC;
     fetch(nxt, min(b + U, nblk - U));
     if (b % KC == 0) stage_load(sr, c + 1);
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      w4_block<XT, ST, SUB, MT, NT, U, false>(a, cur, u, xs[c & 1] + (b % KC + u) * 4 * P * 1024 + lane * 16, ROW, 1024, nullptr,
-                                              0, tot);
+    for (int u = 0; u < U; ++u) block(cur, u, xs[c & 1] + (b % KC + u) * 8 * P * 1024 + lane * 16);
     if ((b + U) % KC == 0) {
       stage_write(sr, (c + 1) & 1);
       __syncthreads();
@@ -659,6 +774,23 @@ __global__ __launch_bounds__(W4_NT) __attribute__((amdgpu_waves_per_eu(2))) void
     step(hb, ha, s + 1);
     if ((s += 2) >= nsteps) break;
   }
-  w4_store<MT, NT>(a, rt, n0, tot);
+
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int n = n0 + nt * 32 + l32;
+    if (n >= a.N) continue;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int row = (rt * MT + m) * 32 + (r >> 2) * 8 + half * 4 + (r & 3);
+        if (row >= a.R) continue;
+        const size_t o = (size_t)row * a.N + n;
+        if (a.out_bf16) store_out(reinterpret_cast<uint16_t*>(a.out) + o, tot[m][nt][r]);
+        else store_out(reinterpret_cast<float*>(a.out) + o, tot[m][nt][r]);
+      }
+    }
+  }
 }
+
 }  // namespace sl

@@ -37,8 +37,8 @@ static hipError_t launch_stream(W4Args a, hipStream_t st) {
 
 template <typename XT, typename ST, int SUB, int MT, int NT, int U, int KC>
 static hipError_t launch_tile(W4Args a, hipStream_t st) {
-  a.row_tiles = (a.R + 16 * MT - 1) / (16 * MT);
-  const int cols = W4_WAVES * NT * 16;
+  a.row_tiles = (a.R + 32 * MT - 1) / (32 * MT);
+  const int cols = W4_WAVES * NT * 32;
   const long long sets = (long long)((a.N + cols - 1) / cols) * a.row_tiles;
   if (sets > 0x7FFFFFF0LL) return hipErrorInvalidValue;
   a.per_xcd = (int)((sets + 7) / 8);
@@ -50,14 +50,12 @@ static hipError_t launch_tile(W4Args a, hipStream_t st) {
 struct W4Plan {
   int stream;        // row tiles of the streaming kernel (1, 2), 0: two launches
   int rp;            // rows staged of a tile (streaming kernel)
-  int row_tiles16;   // row tiles of 16 in the workspace, whole workgroup tiles
+  int row_tiles;     // row tiles of 32 in the workspace, whole workgroup tiles
   size_t op_bytes, bytes;
 };
 
-// Row tiles of a workgroup of the two-launch form: four where the call has
-// more than 32 rows, but two with several groups to 128 k or fp32 hidden
-// states, whose registers four would spill.
-static int w4_tile_rows(int sub, int parts, int R) { return R > 32 && sub == 1 && parts == 1 ? 4 : 2; }
+// Row tiles of 32 of a workgroup in the two-launch form.
+static int w4_tile_rows(int R) { return R > 32 ? 2 : 1; }
 
 static W4Plan w4_plan(int hidden_dtype, int group, int R, int K) {
   W4Plan p;
@@ -72,11 +70,11 @@ static W4Plan w4_plan(int hidden_dtype, int group, int R, int K) {
     p.stream = mt;
     return p;
   }
-  const int tile = w4_tile_rows(sub, parts, R);
-  p.row_tiles16 = (R + 16 * tile - 1) / (16 * tile) * tile;
+  const int tile = w4_tile_rows(R);
+  p.row_tiles = (R + 32 * tile - 1) / (32 * tile) * tile;
   const int blocks = w4_blocks(K);
-  p.op_bytes = (size_t)p.row_tiles16 * blocks * 4 * parts * 1024;
-  p.bytes = p.op_bytes + (size_t)p.row_tiles16 * ((blocks * sub + 31) / 32) * 3 * 1024;
+  p.op_bytes = (size_t)p.row_tiles * blocks * 8 * parts * 1024;
+  p.bytes = p.op_bytes + (size_t)p.row_tiles * ((blocks * sub + 15) / 16) * 3 * 1024;
   return p;
 }
 
@@ -85,17 +83,17 @@ static hipError_t launch_w4(W4Args a, const W4Plan& p, hipStream_t st) {
   a.rp = p.rp;
   if (p.stream == 1) return launch_stream<XT, ST, SUB, 1>(a, st);
   if (p.stream == 2) return launch_stream<XT, ST, SUB, 2>(a, st);
-  hipLaunchKernelGGL((w4_order_kernel<XT, SUB>), dim3((unsigned)(p.row_tiles16 * w4_blocks(a.K))), dim3(256), 0, st, a);
+  hipLaunchKernelGGL((w4_order_kernel<XT, SUB>), dim3((unsigned)(p.row_tiles * w4_blocks(a.K))), dim3(512), 0, st, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   // Wide column tiles where they still give every CU a workgroup.
-  constexpr int P = W4Hidden<XT>::PARTS, KC = P == 1 ? 2 : 1;   // blocks per chunk of x
-  const int mt = w4_tile_rows(SUB, P, a.R);
-  const bool wide = (long long)((a.N + 511) / 512) * (p.row_tiles16 / mt) >= 192;
-  if constexpr (SUB == 1 && P == 1)
-    if (mt == 4)
-      return wide ? launch_tile<XT, ST, SUB, 4, 4, 1, 1>(a, st) : launch_tile<XT, ST, SUB, 4, 1, KC, KC>(a, st);
-  return wide ? launch_tile<XT, ST, SUB, 2, 4, KC, KC>(a, st) : launch_tile<XT, ST, SUB, 2, 1, KC, KC>(a, st);
+  const int mt = w4_tile_rows(a.R);
+  const bool wide = (long long)((a.N + 511) / 512) * (p.row_tiles / mt) >= 192;
+  if (mt == 1) return wide ? launch_tile<XT, ST, SUB, 1, 2, 2, 2>(a, st) : launch_tile<XT, ST, SUB, 1, 1, 2, 2>(a, st);
+  // (Groups of 32, or of 64 with fp32 hidden states, would spill registers there.)
+  if constexpr (SUB == 1 || (SUB == 2 && W4Hidden<XT>::PARTS == 1))
+    if (wide) return launch_tile<XT, ST, SUB, 2, 2, 1, 1>(a, st);
+  return launch_tile<XT, ST, SUB, 2, 1, 1, 1>(a, st);
 }
 
 template <typename XT, typename ST>
