@@ -88,8 +88,8 @@ static hipError_t launch_w4(W4Args a, const W4Plan& p, hipStream_t st) {
   if (e != hipSuccess) return e;
   // Wide column tiles where they still give every CU a workgroup.
   const int mt = w4_tile_rows(a.R);
+  if (mt == 1) return launch_tile<XT, ST, SUB, 1, 1, 2, 2>(a, st);
   const bool wide = (long long)((a.N + 511) / 512) * (p.row_tiles / mt) >= 192;
-  if (mt == 1) return wide ? launch_tile<XT, ST, SUB, 1, 2, 2, 2>(a, st) : launch_tile<XT, ST, SUB, 1, 1, 2, 2>(a, st);
   // (Groups of 32, or of 64 with fp32 hidden states, would spill registers there.)
   if constexpr (SUB == 1 || (SUB == 2 && W4Hidden<XT>::PARTS == 1))
     if (wide) return launch_tile<XT, ST, SUB, 2, 2, 1, 1>(a, st);

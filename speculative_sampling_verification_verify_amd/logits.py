@@ -15,7 +15,7 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from .binding import SV_OK, _check, _dtype_code, _ptr
+from .binding import SV_OK, _check, _dtype_code
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # The in-tree build; SL_LIBRARY names another build of the same source (the
@@ -70,18 +70,35 @@ def spec_logits_strerror(code: int) -> str:
 
 
 def _gpu(t: torch.Tensor, name: str) -> torch.device:
-    if t.device.type != "cuda":
+    dev = t.device
+    if dev.type != "cuda":
         raise ValueError(f"{name} must live in GPU memory")
-    return t.device
+    return dev
+
+
+def _arg(t: Optional[torch.Tensor], name: str, dtype, shape, dev) -> Optional[int]:
+    """The checked tensor's address (None for None); `shape` is a tuple.  These
+    checks are a good part of a small call's time, hence the one expression."""
+    if t is None:
+        return None
+    if not (t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous()):
+        _check(t, name, dtype, shape, dev)
+    return t.data_ptr()
+
+
+# torch.cuda.current_stream makes a Stream object; the handle is all that is needed.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _call(fn, where: str, dev: torch.device, stream, *args) -> None:
     """Enqueue on `stream` (None: the current stream of the tensors' device,
     which need not be the current device)."""
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    h = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if dev.index == torch.cuda.current_device():
+        h = _raw_stream(dev.index)
+    else:
+        h = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if torch.cuda.device_count() == 1 or dev.index == torch.cuda.current_device():
         rc = fn(*args, h or None)
     else:
         with torch.cuda.device(dev):
@@ -113,29 +130,29 @@ def spec_logits_w4(hidden: torch.Tensor, weights: torch.Tensor, scales: torch.Te
     if hidden.dim() < 1 or weights.dim() != 2 or scales.dim() != 2:
         raise ValueError("hidden must be [..., K], weights [N, K / 2] and scales [N, K / group]")
     dev = _gpu(hidden, "hidden")
-    K = hidden.shape[-1]
+    lead, K = hidden.shape[:-1], hidden.shape[-1]
     N, G = scales.shape
-    R = hidden.numel() // K if K else 0
-    _check(hidden, "hidden", hidden.dtype, hidden.shape, dev)
-    _check(weights, "weights", torch.uint8, (N, K // 2), dev)
-    _check(scales, "scales", scales.dtype, (N, G), dev)
-    _check(zeros, "zeros", torch.uint8, (N, G), dev)
+    R = lead.numel()
+    xt, st = _dtype_code(hidden), _dtype_code(scales)
+    x = _arg(hidden, "hidden", hidden.dtype, hidden.shape, dev)
+    w = _arg(weights, "weights", torch.uint8, (N, K // 2), dev)
+    s = _arg(scales, "scales", scales.dtype, (N, G), dev)
+    z = _arg(zeros, "zeros", torch.uint8, (N, G), dev)
     if K == 0 or G == 0 or N == 0 or K % G:
         raise ValueError(f"scales: {G} groups do not divide K = {K}")
     if out is None:
         with on_stream(stream):
-            out = torch.empty((*hidden.shape[:-1], N), dtype=out_dtype or hidden.dtype, device=dev)
+            out = torch.empty((*lead, N), dtype=out_dtype or hidden.dtype, device=dev)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out: expected {out_dtype}, got {out.dtype}")
-    _check(out, "out", out.dtype, (*hidden.shape[:-1], N), dev)
-    need = lib().spec_logits_w4_workspace_bytes(_dtype_code(hidden), K // G, R, K)
+    o = _arg(out, "out", out.dtype, (*lead, N), dev)
+    need = lib().spec_logits_w4_workspace_bytes(xt, K // G, R, K)
     ws = None
     if need:
         with on_stream(stream):
             ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    _call(lib().spec_logits_w4, "spec_logits_w4", dev, stream, _ptr(hidden), _dtype_code(hidden), _ptr(weights),
-          _ptr(scales), _dtype_code(scales), _ptr(zeros), K // G, R, K, N, _ptr(out), _dtype_code(out), _ptr(ws),
-          need)
+    _call(_lib.spec_logits_w4, "spec_logits_w4", dev, stream, x, xt, w, s, st, z, K // G, R, K, N, o, _dtype_code(out),
+          None if ws is None else ws.data_ptr(), need)
     return out
 
 
@@ -166,16 +183,16 @@ class History(NamedTuple):
         return cls(z(S, V), z(S, V), z(S))
 
 
-def _check_history(history: History):
+def _history_args(history: History):
+    """(counts, ids, num, S, V) as the C entry points take them, and the device."""
     counts, ids, num = history
     if counts.dim() != 2:
         raise ValueError("history.counts must be [S, V]")
     dev = _gpu(counts, "history.counts")
-    S, V = counts.shape
-    _check(counts, "history.counts", torch.int32, (S, V), dev)
-    _check(ids, "history.ids", torch.int32, (S, V), dev)
-    _check(num, "history.num", torch.int32, (S,), dev)
-    return S, V, dev
+    shape = counts.shape
+    S, V = shape
+    return (_arg(counts, "history.counts", torch.int32, shape, dev), _arg(ids, "history.ids", torch.int32, shape, dev),
+            _arg(num, "history.num", torch.int32, (S,), dev), S, V), dev
 
 
 def spec_history_append(history: History, tokens: torch.Tensor, slots: Optional[torch.Tensor] = None,
@@ -183,25 +200,22 @@ def spec_history_append(history: History, tokens: torch.Tensor, slots: Optional[
     """Add tokens [B, T] (int32; ids outside the vocabulary, such as the -1 that
     pads a verify's out_tokens, are skipped) to the history of slots [B]
     (None: 0..B-1), as output tokens or as prompt tokens."""
-    S, V, dev = _check_history(history)
+    h, dev = _history_args(history)
     if tokens.dim() != 2:
         raise ValueError("tokens must be [B, T]")
     B, T = tokens.shape
-    _check(tokens, "tokens", torch.int32, (B, T), dev)
-    _check(slots, "slots", torch.int32, (B,), dev)
+    t = _arg(tokens, "tokens", torch.int32, (B, T), dev)
+    s = _arg(slots, "slots", torch.int32, (B,), dev)
     if T == 0:
         return
-    _call(lib().spec_history_append, "spec_history_append", dev, stream, _ptr(history[0]), _ptr(history[1]),
-          _ptr(history[2]), S, V, _ptr(slots), _ptr(tokens), B, T, int(bool(prompt)))
+    _call(lib().spec_history_append, "spec_history_append", dev, stream, *h, s, t, B, T, 1 if prompt else 0)
 
 
 def spec_history_reset(history: History, slots: Optional[torch.Tensor] = None, stream=None) -> None:
     """Empty the given slots [B] (int32), or with None every slot."""
-    S, V, dev = _check_history(history)
-    B = S if slots is None else slots.numel()
-    _check(slots, "slots", torch.int32, (B,), dev)
-    _call(lib().spec_history_reset, "spec_history_reset", dev, stream, _ptr(history[0]), _ptr(history[1]),
-          _ptr(history[2]), S, V, _ptr(slots), B)
+    h, dev = _history_args(history)
+    B = h[3] if slots is None else slots.numel()
+    _call(lib().spec_history_reset, "spec_history_reset", dev, stream, *h, _arg(slots, "slots", torch.int32, (B,), dev), B)
 
 
 # ---------------------------------------------------------------------------
@@ -223,59 +237,60 @@ def spec_process_logits(logits: torch.Tensor, out: Optional[torch.Tensor] = None
     frequency [B] float32; bias_ids [B, NB] int32 with bias_values [B, NB]
     float32; masks [M, ceil(V / 32)] int32 bits with mask_rows [B, J] int32 (-1:
     no mask); rows [B] int32: rows j >= rows[b] are left alone."""
-    if logits.dim() not in (2, 3):
+    shape = logits.shape
+    if len(shape) not in (2, 3):
         raise ValueError("logits must be [B, J, V] or [B, V]")
     dev = _gpu(logits, "logits")
-    B, V = logits.shape[0], logits.shape[-1]
-    J = logits.shape[1] if logits.dim() == 3 else 1
+    B, V = shape[0], shape[-1]
+    J = shape[1] if len(shape) == 3 else 1
     dt = _dtype_code(logits)
-    out = logits if out is None else out
-    _check(logits, "logits", logits.dtype, logits.shape, dev)
-    _check(out, "out", logits.dtype, logits.shape, dev)
-    S, hist = 0, (None, None, None)
+    z = _arg(logits, "logits", logits.dtype, shape, dev)
+    if out is None:
+        out = logits
+    o = _arg(out, "out", logits.dtype, shape, dev)
+    h = (None, None, None, 0)
     if history is not None:
-        S, hv, hdev = _check_history(history)
-        if hv != V or hdev != dev:
-            raise ValueError(f"history is for V = {hv} on {hdev}, the logits have V = {V} on {dev}")
-        hist = history if S else hist
+        h, hdev = _history_args(history)
+        if h[4] != V or hdev != dev:
+            raise ValueError(f"history is for V = {h[4]} on {hdev}, the logits have V = {V} on {dev}")
+        h = h[:4] if h[3] else (None, None, None, 0)
     elif slots is not None:
         raise ValueError("slots without a history")
-    _check(slots, "slots", torch.int32, (B,), dev)
-    stride = 0
+    s = _arg(slots, "slots", torch.int32, (B,), dev)
+    d, stride = None, 0
     if draft_tokens is not None:
-        if draft_tokens.dim() != 2 or draft_tokens.shape[0] != B or draft_tokens.shape[1] < first + J - 1:
-            raise ValueError(f"draft_tokens: expected [{B}, >= {first + J - 1}], got {tuple(draft_tokens.shape)}")
+        n = first + J - 1
+        if draft_tokens.dim() != 2 or draft_tokens.shape[0] != B or draft_tokens.shape[1] < n:
+            raise ValueError(f"draft_tokens: expected [{B}, >= {n}], got {tuple(draft_tokens.shape)}")
         if draft_tokens.dtype != torch.int32:
             raise TypeError(f"draft_tokens: expected torch.int32, got {draft_tokens.dtype}")
         if draft_tokens.device != dev:
             raise ValueError(f"draft_tokens is on {draft_tokens.device}, expected {dev}")
-        if draft_tokens.shape[1] > 1 and draft_tokens.stride(1) != 1:
+        row, col = draft_tokens.stride()
+        if col != 1 and draft_tokens.shape[1] > 1:
             raise ValueError("draft_tokens must be contiguous along its rows")
-        stride = draft_tokens.stride(0) if B > 1 else max(draft_tokens.shape[1], first + J - 1)
-        if draft_tokens.shape[1] == 0:
-            draft_tokens = None
-    for t, name in ((repetition, "repetition"), (presence, "presence"), (frequency, "frequency")):
-        _check(t, name, torch.float32, (B,), dev)
+        if n > 0:
+            d, stride = draft_tokens.data_ptr(), row if B > 1 else n
+    f32, i32, per = torch.float32, torch.int32, (B,)
+    rep, pres, freq = _arg(repetition, "repetition", f32, per, dev), _arg(presence, "presence", f32, per, dev), \
+        _arg(frequency, "frequency", f32, per, dev)
     if (bias_ids is None) != (bias_values is None) or (masks is None) != (mask_rows is None):
         raise ValueError("bias_ids and bias_values, and masks and mask_rows, go together")
-    NB = M = 0
+    NB, bi, bv = 0, None, None
     if bias_ids is not None:
         NB = bias_ids.shape[-1]
-        _check(bias_ids, "bias_ids", torch.int32, (B, NB), dev)
-        _check(bias_values, "bias_values", torch.float32, (B, NB), dev)
+        bi, bv = _arg(bias_ids, "bias_ids", i32, (B, NB), dev), _arg(bias_values, "bias_values", f32, (B, NB), dev)
         if NB == 0:
-            bias_ids = bias_values = None
+            bi = bv = None
+    M, mt, mr = 0, None, None
     if masks is not None:
         M = masks.shape[0]
-        _check(masks, "masks", torch.int32, (M, (V + 31) // 32), dev)
-        _check(mask_rows, "mask_rows", torch.int32, (B, J) if logits.dim() == 3 or mask_rows.dim() == 2 else (B,), dev)
+        mt = _arg(masks, "masks", i32, (M, (V + 31) // 32), dev)
+        mr = _arg(mask_rows, "mask_rows", i32, (B, J) if len(shape) == 3 or mask_rows.dim() == 2 else per, dev)
         if M == 0:
             raise ValueError("masks is empty")
-    _check(rows, "rows", torch.int32, (B,), dev)
-    _call(lib().spec_process_logits, "spec_process_logits", dev, stream, _ptr(logits), _ptr(out), dt, _ptr(hist[0]),
-          _ptr(hist[1]), _ptr(hist[2]), S, _ptr(slots) if S else None, _ptr(draft_tokens), stride, int(first),
-          _ptr(repetition), _ptr(presence), _ptr(frequency), _ptr(bias_ids), _ptr(bias_values), NB, _ptr(masks), M,
-          _ptr(mask_rows), _ptr(rows), B, J, V)
+    _call(lib().spec_process_logits, "spec_process_logits", dev, stream, z, o, dt, *h, s if h[3] else None, d, stride,
+          int(first), rep, pres, freq, bi, bv, NB, mt, M, mr, _arg(rows, "rows", i32, per, dev), B, J, V)
     return out
 
 
