@@ -3,11 +3,19 @@
 // Of a row's V values a step touches few: the tokens that the sequence holds,
 // the drafts before the position and the biased ids.  Everything else is
 // copied, or left alone in place, or set to -inf where the mask forbids it.
-// So a workgroup first streams its piece of a row (copy and mask, 16 bytes a
-// lane, nothing in place where the mask allows all), and then walks the lists:
-// every touched token inside the piece is read again from the input and
-// written once.  In place, the stream leaves allowed values as they are, so
-// the second read still sees the input.
+//
+// Copying or masking (process_stream_kernel) is bound by the bytes of the
+// logits.  A workgroup has a piece of the vocabulary, all rows of a sequence:
+// it reads the history's list once and keeps the piece's touched ids, with
+// their counts, in LDS.  Out of place, a row's piece goes through an LDS tile in
+// which the touched values are adjusted between the load and the store, while
+// the next row is being loaded: the logits are read and written once, in whole
+// 16-byte units.  (Writing the touched values again after the copy cost as much
+// as the copy: at B=256, J=8, V=152064 with 2000 tokens held each, 210 us of
+// 471 us; adjusting them right behind a lane's own store cost 250 us.)  In
+// place, only units that the mask changes are written, and then the touched
+// values.  Without masks nothing is streamed: the lists are walked
+// (process_lists_kernel).
 #pragma once
 
 #include "sl_common.h"
@@ -15,8 +23,9 @@
 namespace sl {
 
 constexpr int PR_NT = 256;                                // threads per workgroup
-constexpr int PR_SPECIAL = SL_MAX_DRAFT + SL_MAX_BIAS;    // drafts and biased ids of a row
-constexpr int PR_HASH = 4096;                             // slots of their hash table
+constexpr int PR_UNITS = 4;                               // 16-byte units that a lane has in flight
+constexpr int PR_TILE = PR_NT * PR_UNITS;                 // units of the tile: one row's piece, or several rows'
+constexpr int PR_ENTRIES = 1024;                          // touched ids of a piece kept in LDS; beyond, its list is walked per row
 constexpr uint32_t IN_PROMPT = 0x80000000u;
 
 struct ProcessArgs {
@@ -37,9 +46,13 @@ struct ProcessArgs {
   const int32_t* rows;
   int S, draft_stride, first, NB, M, B, J, V;
   int W;        // words of a mask row
-  int chunks;   // pieces per row
+  int pieces;   // pieces of the vocabulary (stream), shares of the lists (lists)
   int piece;    // elements per piece, a multiple of 32
+  int groups;   // groups of rows of a sequence, each a workgroup's
   int wide;     // 1: the bases of in and out are 16-byte aligned
+  int tile_off; // the tile's place in LDS
+  int tile_rows; // rows that it holds
+  int hmask;    // slots of the ids' hash table - 1: at least twice as many as there are ids
 };
 
 struct Penalty {
@@ -100,151 +113,400 @@ template <typename ET> struct Raw;
 template <> struct Raw<uint16_t> { typedef uint16_t type; };
 template <> struct Raw<float> { typedef uint32_t type; };
 
-// One workgroup per (row, piece).  Pieces start at whole 16-byte units of the
-// row (after the `head` elements in front of its first one), so no two
-// workgroups write into one unit.  With nothing to stream (in place, no mask)
-// the pieces are shares of the lists instead.
-template <typename ET>
-__global__ __launch_bounds__(PR_NT) void process_kernel(ProcessArgs a) {
-  typedef typename Raw<ET>::type RT;
-  constexpr int VEC = Elem<ET>::VEC;
-  __shared__ int32_t s_hash[PR_HASH];         // ids, -1 free
-  __shared__ uint32_t s_twice[PR_HASH / 32];  // bit h: the id in slot h was listed more than once
-  __shared__ int32_t s_spec[PR_SPECIAL];      // slot << 16 | entry that took it
-  __shared__ int s_nspec;
-  const int tid = threadIdx.x;
-  const int c = (int)(blockIdx.x % (unsigned)a.chunks);
-  const int row = (int)(blockIdx.x / (unsigned)a.chunks);
-  const int b = row / a.J, j = row % a.J;
-  if (a.rows && j >= a.rows[b]) return;
-  const size_t base = (size_t)row * a.V;
-  const RT* in = reinterpret_cast<const RT*>(a.in) + base;
-  RT* out = reinterpret_cast<RT*>(a.out) + base;
-  const bool copy = a.in != a.out;
-  const bool shares = !copy && !a.mask_rows;
-  const int head = a.wide ? min(a.V, (int)((16 - (base * sizeof(RT)) % 16) % 16 / sizeof(RT))) : 0;
-  int lo = 0, hi = a.V;
-  if (!shares) {
-    if (c > 0) lo = min(a.V, head + c * a.piece);
-    if (c + 1 < a.chunks) hi = min(a.V, head + (c + 1) * a.piece);
+// An id that drafts or biases name: the positions of the drafts that are it,
+// and the sum of its biases.
+struct Special {
+  unsigned long long drafts;
+  float bias;
+  int biased;
+};
+
+// The ids that a sequence's drafts and biases name within [lo, hi), each once,
+// in LDS: a hash table from id to entry.
+struct Specials {
+  int32_t* slot;      // [hmask + 1] ids, -1 free
+  int32_t* entry;     // [hmask + 1] entry of the slot's id
+  uint32_t* twice;    // [(hmask + 32) / 32] bit h: the id in slot h was named more than once
+  Special* entries;
+  int32_t* source;    // per entry: slot << 16 | the name that took it
+  int n;              // names: drafts and biases
+  int hmask;
+
+  static __host__ __device__ int bytes(int names, int hmask) {
+    return names ? (hmask + 1) * 8 + (hmask + 32) / 32 * 4 + names * ((int)sizeof(Special) + 4) : 0;
   }
 
-  Penalty p;
-  p.rep = a.rep ? a.rep[b] : 1.0f;
-  p.pres = a.pres ? a.pres[b] : 0.0f;
-  p.freq = a.freq ? a.freq[b] : 0.0f;
-  const int mrow = a.mask_rows ? a.mask_rows[row] : -1;
-  if (!(p.rep > 0.0f) || !finite(p.rep) || !finite(p.pres) || !finite(p.freq) || mrow < -1 || mrow >= a.M) {
-    const int step = shares ? PR_NT * a.chunks : PR_NT;
-    for (int e = lo + (shares ? c * PR_NT : 0) + tid; e < hi; e += step) out[e] = Elem<ET>::QNAN;
-    return;
-  }
-  const uint32_t* mask = mrow >= 0 ? a.masks + (size_t)mrow * a.W : nullptr;
-  const bool penal = p.rep != 1.0f || p.pres != 0.0f || p.freq != 0.0f;
-  const int slot = a.counts && penal ? (a.slots ? a.slots[b] : b) : -1;
-  const bool held = slot >= 0 && slot < a.S;
-  const uint32_t* counts = held ? a.counts + (size_t)slot * a.V : nullptr;
-  const int nd = a.drafts && penal ? a.first + j : 0;
-  const int32_t* drafts = a.drafts + (size_t)b * a.draft_stride;
-  const int32_t* bias_ids = a.bias_ids + (size_t)b * a.NB;
-  const float* bias_vals = a.bias_vals + (size_t)b * a.NB;
-  const int nlist = nd + a.NB;
-
-  // The drafts and biased ids of this piece, each once.
-  int hmask = 63;
-  while (hmask + 1 < 2 * nlist) hmask = 2 * hmask + 1;
-  if (nlist) {
-    for (int i = tid; i <= hmask; i += PR_NT) s_hash[i] = -1;
-    for (int i = tid; i < PR_HASH / 32; i += PR_NT) s_twice[i] = 0;
-    if (tid == 0) s_nspec = 0;
+  // Builds the table; returns the number of entries.  Every thread calls it.
+  __device__ __forceinline__ int build(char* smem, int* count, const int32_t* drafts, int nd, const int32_t* bias_ids,
+                                       const float* bias_vals, int nb, int hm, int lo, int hi) {
+    n = nd + nb;
+    hmask = hm;
+    if (!n) return 0;
+    entries = reinterpret_cast<Special*>(smem);
+    slot = reinterpret_cast<int32_t*>(entries + n);
+    entry = slot + hmask + 1;
+    source = entry + hmask + 1;
+    twice = reinterpret_cast<uint32_t*>(source + n);
+    const int tid = threadIdx.x;
+    for (int i = tid; i <= hmask; i += PR_NT) slot[i] = -1;
+    for (int i = tid; i < (hmask + 32) / 32; i += PR_NT) twice[i] = 0;
+    if (tid == 0) *count = 0;
     __syncthreads();
-    for (int i = tid; i < nlist; i += PR_NT) {
+    for (int i = tid; i < n; i += PR_NT) {
       const int v = i < nd ? drafts[i] : bias_ids[i - nd];
       if (v < lo || v >= hi) continue;
       uint32_t h = hash_of(v) & hmask;
-      for (;;) {   // the table has twice as many slots as there are ids
-        const int old = atomicCAS(&s_hash[h], -1, v);
-        if (old == -1) s_spec[atomicAdd(&s_nspec, 1)] = (int)(h << 16) | i;
-        if (old == v) atomicOr(&s_twice[h >> 5], 1u << (h & 31));
+      for (;;) {
+        const int old = atomicCAS(&slot[h], -1, v);
+        if (old == -1) {
+          const int e = atomicAdd(count, 1);
+          entry[h] = e;
+          source[e] = (int)(h << 16) | i;
+        }
+        if (old == v) atomicOr(&twice[h >> 5], 1u << (h & 31));
         if (old == -1 || old == v) break;
         h = (h + 1) & hmask;
       }
     }
-  }
-
-  // Copy and mask.
-  if (copy || mask) {
-    const int start = c == 0 ? head : lo;
-    const int units = a.wide ? (hi - start) / VEC : 0;
-    constexpr uint32_t all = (1u << VEC) - 1u;
-    for (int u = tid; u < units; u += PR_NT) {
-      const int e = start + u * VEC;
-      const uint32_t bits = mask ? mask_word(mask, a.W, e) & all : all;
-      if (!copy && bits == all) continue;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (bits) v = *reinterpret_cast<const uint4*>(in + e);
-      *reinterpret_cast<uint4*>(out + e) = Elem<ET>::mask(v, bits);
-    }
-    const int rest = start + units * VEC;
-    const int before = c == 0 ? start : 0;   // elements in front of the row's first unit
-    for (int i = tid; i < before + (hi - rest); i += PR_NT) {
-      const int e = i < before ? i : rest + (i - before);
-      const bool ok = !mask || (mask[e >> 5] >> (e & 31) & 1u);
-      if (!ok || copy) out[e] = ok ? in[e] : (RT)Elem<ET>::NEG_INF;
-    }
-  }
-  __syncthreads();
-
-  // The listed ids.
-  if (nlist) {
-    const int ns = s_nspec;
-    for (int k = tid; k < ns; k += PR_NT) {
-      const int h = s_spec[k] >> 16, i = s_spec[k] & 0xFFFF;
-      const int v = s_hash[h];
-      if (shares && v % a.chunks != c) continue;
-      if (mask && !(mask[v >> 5] >> (v & 31) & 1u)) continue;
-      const uint32_t word = counts ? counts[v] : 0u;
-      uint32_t count = word & ~IN_PROMPT;
-      float bias = 0.0f;
-      bool biased = false;
-      if (s_twice[h >> 5] >> (h & 31) & 1u) {
-        for (int d = 0; d < nd; ++d) count += drafts[d] == v;
-        for (int d = 0; d < a.NB; ++d)
+    __syncthreads();
+    const int ne = *count;
+    for (int e = tid; e < ne; e += PR_NT) {
+      const int h = source[e] >> 16, i = source[e] & 0xFFFF, v = slot[h];
+      Special s = {0ull, 0.0f, 0};
+      if (twice[h >> 5] >> (h & 31) & 1u) {
+        for (int d = 0; d < nd; ++d)
+          if (drafts[d] == v) s.drafts |= 1ull << d;
+        for (int d = 0; d < nb; ++d)
           if (bias_ids[d] == v) {
-            bias = biased ? bias + bias_vals[d] : bias_vals[d];
-            biased = true;
+            s.bias = s.biased ? s.bias + bias_vals[d] : bias_vals[d];
+            s.biased = 1;
           }
       } else if (i < nd) {
-        ++count;
+        s.drafts = 1ull << i;
       } else {
-        bias = bias_vals[i - nd];
-        biased = true;
+        s.bias = bias_vals[i - nd];
+        s.biased = 1;
       }
-      store_out(reinterpret_cast<ET*>(out) + v,
-                adjust(load_in(reinterpret_cast<const ET*>(in) + v), (word & IN_PROMPT) || count, count, p, bias, biased));
+      entries[e] = s;
     }
+    __syncthreads();
+    return ne;
+  }
+  // The entry of id v, or -1.
+  __device__ __forceinline__ int find(int v) const {
+    uint32_t h = hash_of(v) & hmask;
+    int at;
+    while ((at = slot[h]) != -1 && at != v) h = (h + 1) & hmask;
+    return at == v ? entry[h] : -1;
+  }
+  __device__ __forceinline__ int id(int e) const { return slot[source[e] >> 16]; }
+};
+
+// Adjusts one value of row j in place of what out holds there; nothing where
+// the row does not touch it.
+template <typename ET>
+__device__ __forceinline__ void touch(const ET* in, ET* out, uint32_t word, const Special& s, int first, int j, const Penalty& p) {
+  const int sees = first + j;
+  const uint32_t count = (word & ~IN_PROMPT) + (uint32_t)__popcll(sees < 64 ? s.drafts & ((1ull << sees) - 1) : s.drafts);
+  const bool seen = (word & IN_PROMPT) || count;
+  if (!seen && !s.biased) return;
+  store_out(out, adjust(load_in(in), seen, count, p, s.bias, s.biased != 0));
+}
+
+// What the kernels know of a sequence.
+struct Sequence {
+  Penalty p;
+  bool bad;                // a penalty out of range: its rows become NaN
+  const uint32_t* counts;  // of its slot, or null
+  const int32_t* ids;
+  int held;                // ids listed
+  int nd;                  // drafts that its last row sees
+  int rows;                // rows used
+};
+__device__ __forceinline__ Sequence sequence(const ProcessArgs& a, int b) {
+  Sequence q;
+  q.p.rep = a.rep ? a.rep[b] : 1.0f;
+  q.p.pres = a.pres ? a.pres[b] : 0.0f;
+  q.p.freq = a.freq ? a.freq[b] : 0.0f;
+  q.bad = !(q.p.rep > 0.0f) || !finite(q.p.rep) || !finite(q.p.pres) || !finite(q.p.freq);
+  const bool penal = !q.bad && (q.p.rep != 1.0f || q.p.pres != 0.0f || q.p.freq != 0.0f);
+  const int slot = a.counts && penal ? (a.slots ? a.slots[b] : b) : -1;
+  const bool held = slot >= 0 && slot < a.S;
+  q.counts = held ? a.counts + (size_t)slot * a.V : nullptr;
+  q.ids = held ? a.ids + (size_t)slot * a.V : nullptr;
+  q.held = held ? min(a.num[slot], a.V) : 0;
+  q.nd = a.drafts && penal ? a.first + a.J - 1 : 0;
+  q.rows = a.rows ? min(a.rows[b], a.J) : a.J;
+  return q;
+}
+
+// One workgroup per (sequence, piece, group of rows).  Pieces start at whole
+// 16-byte units of the sequence's first row; where a row's units lie otherwise
+// (V odd), its `head` elements in front of its first unit move the piece, so
+// that no two workgroups write into one unit.
+template <typename ET>
+__global__ __launch_bounds__(PR_NT) void process_stream_kernel(ProcessArgs a) {
+  typedef typename Raw<ET>::type RT;
+  constexpr int VEC = Elem<ET>::VEC;
+  constexpr uint32_t ALL = (1u << VEC) - 1u;
+  extern __shared__ __align__(16) char smem[];
+  __shared__ int s_special, s_listed;
+  const int tid = threadIdx.x;
+  const int c = (int)(blockIdx.x % (unsigned)a.pieces);
+  const int rest = (int)(blockIdx.x / (unsigned)a.pieces);
+  const int grp = rest % a.groups, b = rest / a.groups;
+  const Sequence q = sequence(a, b);
+  const int per = (a.J + a.groups - 1) / a.groups;
+  const int j0 = grp * per, j1 = min(j0 + per, q.rows);
+  if (j0 >= j1) return;
+  const bool copy = a.in != a.out;
+  const size_t seq = (size_t)b * a.J * a.V;
+
+  const int lo = c * a.piece;
+
+  // Row j: where its piece lies, and its mask.
+  struct Row {
+    const RT* in;
+    RT* out;
+    int head, from, to, start, units;
+    const uint32_t* mask;
+    bool bad;
+  };
+  auto place = [&](int j) {
+    Row r;
+    const size_t base = seq + (size_t)j * a.V;
+    r.in = reinterpret_cast<const RT*>(a.in) + base;
+    r.out = reinterpret_cast<RT*>(a.out) + base;
+    r.head = a.wide ? min(a.V, (int)((16 - (base * sizeof(RT)) % 16) % 16 / sizeof(RT))) : 0;
+    r.from = c == 0 ? 0 : min(a.V, lo + r.head);
+    r.to = c + 1 == a.pieces ? a.V : min(a.V, lo + a.piece + r.head);
+    r.start = c == 0 ? r.head : r.from;   // the first unit; in front of it, elements of the row's head
+    r.units = a.wide ? (r.to - r.start) / VEC : 0;
+    return r;
+  };
+  auto row_of = [&](int j) {
+    Row r = place(j);
+    const int m = a.mask_rows ? a.mask_rows[(size_t)b * a.J + j] : -1;
+    r.bad = q.bad || m < -1 || m >= a.M;
+    r.mask = m >= 0 && m < a.M ? a.masks + (size_t)m * a.W : nullptr;
+    return r;
+  };
+
+  // Through the tile: `rows` rows a pass, each with VEC elements in front of its
+  // first unit (for its head) and as many behind its last.
+  const bool lists = q.held || q.nd || (a.NB && !q.bad);
+  const int upr = a.piece / VEC, rows = min(a.tile_rows, j1 - j0), stride = a.piece + 2 * VEC;
+  uint4 nv[PR_UNITS];
+  auto load = [&](int j) {
+#pragma unroll
+    for (int k = 0; k < PR_UNITS; ++k) {
+      const int f = tid + k * PR_NT, rr = rows > 1 ? f / upr : 0, u = f - rr * upr;
+      nv[k] = make_uint4(0, 0, 0, 0);
+      if (rr < rows && j + rr < j1) {
+        const Row r = place(j + rr);
+        if (u < r.units) nv[k] = *reinterpret_cast<const uint4*>(r.in + (r.start + u * VEC));
+      }
+    }
+  };
+  if (copy && lists) load(j0);   // while the lists are read
+
+  // Touched ids of [lo, hi): the piece, and the VEC elements behind it that a row's head may add.
+  const int hi = c + 1 == a.pieces ? a.V : min(a.V, lo + a.piece + VEC);
+  int2* entries = reinterpret_cast<int2*>(smem);   // (id, count word), other than the specials
+  Specials sp;
+  int ne = 0, listed = 0;
+  bool kept = true;
+  if (lists) {
+    int v[PR_UNITS];
+#pragma unroll
+    for (int k = 0; k < PR_UNITS; ++k) v[k] = tid + k * PR_NT < q.held ? q.ids[tid + k * PR_NT] : -1;
+    if (tid == 0) s_listed = 0;
+    ne = sp.build(smem + PR_ENTRIES * sizeof(int2), &s_special, a.drafts + (size_t)b * a.draft_stride, q.nd,
+                  a.bias_ids + (size_t)b * a.NB, a.bias_vals + (size_t)b * a.NB, a.NB, a.hmask, lo, hi);
+    __syncthreads();
+    for (int i = tid;;) {
+#pragma unroll
+      for (int k = 0; k < PR_UNITS; ++k) {
+        if (v[k] < lo || v[k] >= hi || (ne && sp.find(v[k]) >= 0)) continue;
+        const int at = atomicAdd(&s_listed, 1);
+        if (at < PR_ENTRIES) entries[at] = make_int2(v[k], (int)q.counts[v[k]]);
+      }
+      if ((i += PR_TILE) >= q.held) break;
+#pragma unroll
+      for (int k = 0; k < PR_UNITS; ++k) v[k] = i + k * PR_NT < q.held ? q.ids[i + k * PR_NT] : -1;
+    }
+    __syncthreads();
+    kept = s_listed <= PR_ENTRIES;
+    listed = kept ? s_listed : q.held;
+  }
+  const bool tile = copy && (ne || listed);
+
+  auto allowed = [&](const uint32_t* mask, int v) { return !mask || (mask[v >> 5] >> (v & 31) & 1u); };
+  // The i-th touched id (i < ne + listed) in [from, to), its count word and its names; or -1.
+  auto touched = [&](int i, int from, int to, uint32_t& word, Special& s) {
+    int v;
+    s = Special{0ull, 0.0f, 0};
+    if (i < ne) {
+      v = sp.id(i);
+      if (v < from || v >= to) return -1;
+      s = sp.entries[i];
+      word = q.counts ? q.counts[v] : 0u;
+    } else if (kept) {
+      v = entries[i - ne].x;
+      if (v < from || v >= to) return -1;
+      word = (uint32_t)entries[i - ne].y;
+    } else {
+      v = q.ids[i - ne];
+      if (v < from || v >= to || (ne && sp.find(v) >= 0)) return -1;
+      word = q.counts[v];
+    }
+    return v;
+  };
+  auto fill_nan = [&](const Row& r) {
+    for (int e = r.from + tid; e < r.to; e += PR_NT) r.out[e] = Elem<ET>::QNAN;
+  };
+
+  if (!tile) {
+    for (int j = j0; j < j1; ++j) {
+      const Row r = row_of(j);
+      if (r.bad) {
+        fill_nan(r);
+        continue;
+      }
+      if (copy || r.mask) {
+        for (int u = tid; u < r.units; u += PR_TILE) {
+          uint4 v[PR_UNITS];
+          uint32_t ok[PR_UNITS];
+#pragma unroll
+          for (int k = 0; k < PR_UNITS; ++k) {
+            const int e = r.start + (u + k * PR_NT) * VEC;
+            ok[k] = u + k * PR_NT < r.units ? r.mask ? mask_word(r.mask, a.W, e) & ALL : ALL : 0u;
+            v[k] = make_uint4(0, 0, 0, 0);
+            if (ok[k] && (copy || ok[k] != ALL)) v[k] = *reinterpret_cast<const uint4*>(r.in + e);
+          }
+#pragma unroll
+          for (int k = 0; k < PR_UNITS; ++k)
+            if (u + k * PR_NT < r.units && (copy || ok[k] != ALL))
+              *reinterpret_cast<uint4*>(r.out + (r.start + (u + k * PR_NT) * VEC)) = Elem<ET>::mask(v[k], ok[k]);
+        }
+        const int tail = r.start + r.units * VEC, before = r.start - r.from;
+        for (int i = tid; i < before + (r.to - tail); i += PR_NT) {
+          const int e = i < before ? r.from + i : tail + (i - before);
+          const bool ok = allowed(r.mask, e);
+          if (!ok || copy) r.out[e] = ok ? r.in[e] : (RT)Elem<ET>::NEG_INF;
+        }
+      }
+    }
+    if (copy || !(ne || listed)) return;
+    __syncthreads();   // in place: the touched values, which the masks left as they were
+    for (int j = j0; j < j1; ++j) {
+      const Row r = row_of(j);
+      if (r.bad) continue;
+      for (int i = tid; i < ne + listed; i += PR_NT) {
+        uint32_t word;
+        Special s;
+        const int v = touched(i, r.from, r.to, word, s);
+        if (v >= 0 && allowed(r.mask, v))
+          touch(reinterpret_cast<const ET*>(r.in) + v, reinterpret_cast<ET*>(r.out) + v, word, s, a.first, j, q.p);
+      }
+    }
+    return;
   }
 
-  // The tokens that the slot holds, other than those.
-  if (held) {
-    const int32_t* ids = a.ids + (size_t)slot * a.V;
-    const int n = min(a.num[slot], a.V);
-    const int step = shares ? PR_NT * a.chunks : PR_NT;
-    for (int i = (shares ? c * PR_NT : 0) + tid; i < n; i += step) {
-      const int v = ids[i];
-      if (v < lo || v >= hi) continue;
-      if (mask && !(mask[v >> 5] >> (v & 31) & 1u)) continue;
-      if (nlist) {
-        uint32_t h = hash_of(v) & hmask;
-        int at;
-        while ((at = s_hash[h]) != -1 && at != v) h = (h + 1) & hmask;
-        if (at == v) continue;
+  ET* buf = reinterpret_cast<ET*>(smem + a.tile_off);
+  for (int j = j0; j < j1; j += rows) {
+    const int n = min(rows, j1 - j);
+#pragma unroll
+    for (int k = 0; k < PR_UNITS; ++k) {
+      const int f = tid + k * PR_NT, rr = rows > 1 ? f / upr : 0, u = f - rr * upr;
+      if (rr < n && u < upr) *reinterpret_cast<uint4*>(buf + (rr * stride + VEC + u * VEC)) = nv[k];
+    }
+    for (int rr = 0; rr < n; ++rr) {
+      const Row r = row_of(j + rr);
+      if (r.bad) continue;
+      const int tail = r.start + r.units * VEC, before = r.start - r.from;
+      for (int i = tid; i < before + (r.to - tail); i += PR_NT) {
+        const int e = i < before ? r.from + i : tail + (i - before);
+        reinterpret_cast<RT*>(buf)[rr * stride + VEC + (e - r.start)] = r.in[e];
       }
-      const uint32_t word = counts[v];
-      if (!word) continue;
-      const uint32_t count = word & ~IN_PROMPT;
-      store_out(reinterpret_cast<ET*>(out) + v,
-                adjust(load_in(reinterpret_cast<const ET*>(in) + v), true, count, p, 0.0f, false));
+    }
+    __syncthreads();
+    if (j + rows < j1) load(j + rows);
+    for (int rr = 0; rr < n; ++rr) {
+      const Row r = row_of(j + rr);
+      for (int i = tid; i < ne + listed; i += PR_NT) {
+        uint32_t word;
+        Special s;
+        const int v = touched(i, r.from, r.to, word, s);
+        ET* z = buf + (rr * stride + VEC + (v - r.start));
+        if (v >= 0) touch(z, z, word, s, a.first, j + rr, q.p);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < PR_UNITS; ++k) {
+      const int f = tid + k * PR_NT, rr = rows > 1 ? f / upr : 0, u = f - rr * upr;
+      if (rr >= n) continue;
+      const Row r = row_of(j + rr);
+      if (r.bad || u >= r.units) continue;
+      const int e = r.start + u * VEC;
+      const uint4 v = *reinterpret_cast<const uint4*>(buf + (rr * stride + VEC + u * VEC));
+      *reinterpret_cast<uint4*>(r.out + e) = Elem<ET>::mask(v, r.mask ? mask_word(r.mask, a.W, e) & ALL : ALL);
+    }
+    for (int rr = 0; rr < n; ++rr) {
+      const Row r = row_of(j + rr);
+      if (r.bad) {
+        fill_nan(r);
+        continue;
+      }
+      const int tail = r.start + r.units * VEC, before = r.start - r.from;
+      for (int i = tid; i < before + (r.to - tail); i += PR_NT) {
+        const int e = i < before ? r.from + i : tail + (i - before);
+        r.out[e] = allowed(r.mask, e) ? reinterpret_cast<const RT*>(buf)[rr * stride + VEC + (e - r.start)] : (RT)Elem<ET>::NEG_INF;
+      }
+    }
+  }
+}
+
+// In place, without masks: one workgroup per (sequence, share of the lists,
+// group of rows); a lane takes a listed id of a row.
+template <typename ET>
+__global__ __launch_bounds__(PR_NT) void process_lists_kernel(ProcessArgs a) {
+  typedef typename Raw<ET>::type RT;
+  extern __shared__ __align__(16) char smem[];
+  __shared__ int s_count;
+  const int tid = threadIdx.x;
+  const int c = (int)(blockIdx.x % (unsigned)a.pieces);
+  const int rest = (int)(blockIdx.x / (unsigned)a.pieces);
+  const int grp = rest % a.groups, b = rest / a.groups;
+  const Sequence q = sequence(a, b);
+  const int per = (a.J + a.groups - 1) / a.groups;
+  const int j0 = grp * per, nj = min(j0 + per, q.rows) - j0;
+  if (nj <= 0) return;
+  ET* z = reinterpret_cast<ET*>(a.out) + ((size_t)b * a.J + j0) * a.V;
+  if (q.bad) {
+    RT* o = reinterpret_cast<RT*>(z);
+    for (size_t e = (size_t)c * PR_NT + tid; e < (size_t)nj * a.V; e += (size_t)PR_NT * a.pieces) o[e] = Elem<ET>::QNAN;
+    return;
+  }
+  Specials sp;
+  const int ne = sp.build(smem, &s_count, a.drafts + (size_t)b * a.draft_stride, q.nd, a.bias_ids + (size_t)b * a.NB,
+                          a.bias_vals + (size_t)b * a.NB, a.NB, a.hmask, 0, a.V);
+  const Special none = {0ull, 0.0f, 0};
+  for (int r0 = 0; r0 < nj; r0 += 16) {   // 16 rows at a time: the items fit 32 bits
+    const unsigned m = (unsigned)min(16, nj - r0);
+    // (The table's order differs between workgroups: they share its ids out by their values.)
+    for (unsigned i = tid; i < ne * m; i += PR_NT) {
+      const int e = (int)(i / m), j = r0 + (int)(i % m), v = sp.id(e);
+      if (v % a.pieces != c) continue;
+      ET* at = z + (size_t)j * a.V + v;
+      touch(at, at, q.counts ? q.counts[v] : 0u, sp.entries[e], a.first, j0 + j, q.p);
+    }
+    for (unsigned i = c * PR_NT + tid; i < q.held * m; i += PR_NT * a.pieces) {
+      const int j = r0 + (int)(i % m), v = q.ids[i / m];
+      if (v < 0 || v >= a.V || (ne && sp.find(v) >= 0)) continue;
+      ET* at = z + (size_t)j * a.V + v;
+      touch(at, at, q.counts[v], none, a.first, j0 + j, q.p);
     }
   }
 }

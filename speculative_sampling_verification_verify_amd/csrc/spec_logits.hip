@@ -202,9 +202,53 @@ extern "C" int spec_history_reset(int32_t* counts, const int32_t* ids, int32_t* 
 // spec_process_logits
 // ---------------------------------------------------------------------------
 
-// Workgroups to spread a call of few rows over, and the least elements worth one.
+// Workgroups to spread a call over where each reads lists first, and where it
+// only streams; and the least elements of a piece worth one.
 constexpr int PR_TARGET = 1024;
+constexpr int PR_TARGET_PLAIN = 4096;
 constexpr int PR_MIN_PIECE = 4096;
+
+template <typename ET>
+static hipError_t launch_process(ProcessArgs a, hipStream_t st) {
+  constexpr int VEC = Elem<ET>::VEC, TILE = PR_TILE * VEC;
+  const int names = a.NB + (a.drafts ? a.first + a.J - 1 : 0);
+  a.hmask = 63;
+  while (a.hmask + 1 < names + names / 2) a.hmask = 2 * a.hmask + 1;
+  int lds = Specials::bytes(names, a.hmask);
+  const bool stream = a.in != a.out || a.mask_rows, lists = names || a.counts;
+  const int target = lists ? PR_TARGET : PR_TARGET_PLAIN;
+  const int most = (a.V + PR_MIN_PIECE - 1) / PR_MIN_PIECE, least = (a.V + TILE - 1) / TILE;
+  // Pieces of the vocabulary (shares of the lists), then groups of rows; with
+  // no lists to read, every row by itself.
+  a.groups = stream && !lists ? a.J : 1;
+  const long long per = (long long)a.B * a.groups;
+  const long long want = (target + per - 1) / per;
+  a.pieces = (int)(want < 1 ? 1 : want);
+  if (stream) {
+    if (a.pieces > most) a.pieces = most;
+    if (lists && a.pieces < least) a.pieces = least;
+    a.piece = ((a.V + a.pieces - 1) / a.pieces + 31) / 32 * 32;
+    a.pieces = (a.V + a.piece - 1) / a.piece;
+    if (lists) {
+      a.tile_off = (PR_ENTRIES * (int)sizeof(int2) + lds + 15) / 16 * 16;
+      a.tile_rows = TILE / (a.piece + 2 * VEC);
+      if (a.tile_rows > a.J) a.tile_rows = a.J;
+      if (a.tile_rows < 1) a.tile_rows = 1;
+      lds = a.tile_off + a.tile_rows * (a.piece + 2 * VEC) * (int)sizeof(ET);
+    }
+  } else if (a.pieces > 8) {
+    a.pieces = 8;
+  }
+  if (a.groups < a.J) {
+    const long long g = (target + (long long)a.B * a.pieces - 1) / ((long long)a.B * a.pieces);
+    a.groups = (int)(g > a.J ? a.J : g);
+  }
+  const long long grid = (long long)a.B * a.pieces * a.groups;
+  if (grid > 0x7FFFFFFFLL) return hipErrorInvalidValue;
+  if (stream) hipLaunchKernelGGL((process_stream_kernel<ET>), dim3((unsigned)grid), dim3(PR_NT), lds, st, a);
+  else hipLaunchKernelGGL((process_lists_kernel<ET>), dim3((unsigned)grid), dim3(PR_NT), lds, st, a);
+  return hipGetLastError();
+}
 
 extern "C" int spec_process_logits(const void* logits, void* out, int dtype, const int32_t* counts, const int32_t* ids,
                                    const int32_t* num, int S, const int32_t* slots, const int32_t* draft_tokens,
@@ -258,17 +302,8 @@ extern "C" int spec_process_logits(const void* logits, void* out, int dtype, con
   a.V = V;
   a.W = (V + 31) / 32;
   a.wide = !misaligned(logits, 16) && !misaligned(out, 16);
-  const int nrows = B * J;
-  int chunks = (PR_TARGET + nrows - 1) / nrows;
-  const int most = (V + PR_MIN_PIECE - 1) / PR_MIN_PIECE;
-  if (chunks > most) chunks = most;
-  a.piece = ((V + chunks - 1) / chunks + 31) / 32 * 32;
-  a.chunks = (V + a.piece - 1) / a.piece;
-  const dim3 grid((unsigned)((long long)nrows * a.chunks));
   hipStream_t st = (hipStream_t)stream;
-  if (dtype == SV_BF16) hipLaunchKernelGGL((process_kernel<uint16_t>), grid, dim3(PR_NT), 0, st, a);
-  else hipLaunchKernelGGL((process_kernel<float>), grid, dim3(PR_NT), 0, st, a);
-  return hip_status(hipGetLastError());
+  return hip_status(dtype == SV_BF16 ? launch_process<uint16_t>(a, st) : launch_process<float>(a, st));
 }
 
 extern "C" const char* spec_logits_strerror(int code) {
