@@ -23,7 +23,7 @@
 namespace sl {
 
 constexpr int PR_NT = 256;                                // threads per workgroup
-constexpr int PR_UNITS = 4;                               // 16-byte units that a lane has in flight
+constexpr int PR_UNITS = 2;                               // 16-byte units that a lane has in flight
 constexpr int PR_TILE = PR_NT * PR_UNITS;                 // units of the tile: one row's piece, or several rows'
 constexpr int PR_ENTRIES = 1024;                          // touched ids of a piece kept in LDS; beyond, its list is walked per row
 constexpr uint32_t IN_PROMPT = 0x80000000u;
@@ -47,7 +47,7 @@ struct ProcessArgs {
   int S, draft_stride, first, NB, M, B, J, V;
   int W;        // words of a mask row
   int pieces;   // pieces of the vocabulary (stream), shares of the lists (lists)
-  int piece;    // elements per piece, a multiple of 32
+  int piece;    // elements per piece, whole 16-byte units
   int groups;   // groups of rows of a sequence, each a workgroup's
   int wide;     // 1: the bases of in and out are 16-byte aligned
   int tile_off; // the tile's place in LDS
@@ -112,6 +112,13 @@ template <> struct Elem<float> {
 template <typename ET> struct Raw;
 template <> struct Raw<uint16_t> { typedef uint16_t type; };
 template <> struct Raw<float> { typedef uint32_t type; };
+
+// A unit that this call does not read again: past the cache (B=128, J=9,
+// V=128256 with masks, penalties and biases: 126 -> 101 us).
+__device__ __forceinline__ void store_stream(void* p, uint4 v) {
+  typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+  __builtin_nontemporal_store(u32x4{v.x, v.y, v.z, v.w}, reinterpret_cast<u32x4*>(p));
+}
 
 // An id that drafts or biases name: the positions of the drafts that are it,
 // and the sum of its biases.
@@ -244,7 +251,8 @@ __device__ __forceinline__ Sequence sequence(const ProcessArgs& a, int b) {
 // 16-byte units of the sequence's first row; where a row's units lie otherwise
 // (V odd), its `head` elements in front of its first unit move the piece, so
 // that no two workgroups write into one unit.
-template <typename ET>
+// LISTS: the call has a history, drafts or biases.
+template <typename ET, bool LISTS>
 __global__ __launch_bounds__(PR_NT) void process_stream_kernel(ProcessArgs a) {
   typedef typename Raw<ET>::type RT;
   constexpr int VEC = Elem<ET>::VEC;
@@ -294,7 +302,7 @@ __global__ __launch_bounds__(PR_NT) void process_stream_kernel(ProcessArgs a) {
 
   // Through the tile: `rows` rows a pass, each with VEC elements in front of its
   // first unit (for its head) and as many behind its last.
-  const bool lists = q.held || q.nd || (a.NB && !q.bad);
+  const bool lists = LISTS && (q.held || q.nd || (a.NB && !q.bad));
   const int upr = a.piece / VEC, rows = min(a.tile_rows, j1 - j0), stride = a.piece + 2 * VEC;
   uint4 nv[PR_UNITS];
   auto load = [&](int j) {
@@ -339,7 +347,7 @@ __global__ __launch_bounds__(PR_NT) void process_stream_kernel(ProcessArgs a) {
     kept = s_listed <= PR_ENTRIES;
     listed = kept ? s_listed : q.held;
   }
-  const bool tile = copy && (ne || listed);
+  const bool tile = LISTS && copy && (ne || listed);
 
   auto allowed = [&](const uint32_t* mask, int v) { return !mask || (mask[v >> 5] >> (v & 31) & 1u); };
   // The i-th touched id (i < ne + listed) in [from, to), its count word and its names; or -1.
@@ -385,9 +393,12 @@ __global__ __launch_bounds__(PR_NT) void process_stream_kernel(ProcessArgs a) {
             if (ok[k] && (copy || ok[k] != ALL)) v[k] = *reinterpret_cast<const uint4*>(r.in + e);
           }
 #pragma unroll
-          for (int k = 0; k < PR_UNITS; ++k)
-            if (u + k * PR_NT < r.units && (copy || ok[k] != ALL))
-              *reinterpret_cast<uint4*>(r.out + (r.start + (u + k * PR_NT) * VEC)) = Elem<ET>::mask(v[k], ok[k]);
+          for (int k = 0; k < PR_UNITS; ++k) {
+            RT* o = r.out + (r.start + (u + k * PR_NT) * VEC);
+            if (u + k * PR_NT >= r.units || !(copy || ok[k] != ALL)) continue;
+            if (copy) store_stream(o, Elem<ET>::mask(v[k], ok[k]));
+            else *reinterpret_cast<uint4*>(o) = Elem<ET>::mask(v[k], ok[k]);
+          }
         }
         const int tail = r.start + r.units * VEC, before = r.start - r.from;
         for (int i = tid; i < before + (r.to - tail); i += PR_NT) {
@@ -397,7 +408,7 @@ __global__ __launch_bounds__(PR_NT) void process_stream_kernel(ProcessArgs a) {
         }
       }
     }
-    if (copy || !(ne || listed)) return;
+    if (!LISTS || copy || !(ne || listed)) return;
     __syncthreads();   // in place: the touched values, which the masks left as they were
     for (int j = j0; j < j1; ++j) {
       const Row r = row_of(j);
@@ -451,7 +462,7 @@ __global__ __launch_bounds__(PR_NT) void process_stream_kernel(ProcessArgs a) {
       if (r.bad || u >= r.units) continue;
       const int e = r.start + u * VEC;
       const uint4 v = *reinterpret_cast<const uint4*>(buf + (rr * stride + VEC + u * VEC));
-      *reinterpret_cast<uint4*>(r.out + e) = Elem<ET>::mask(v, r.mask ? mask_word(r.mask, a.W, e) & ALL : ALL);
+      store_stream(r.out + e, Elem<ET>::mask(v, r.mask ? mask_word(r.mask, a.W, e) & ALL : ALL));
     }
     for (int rr = 0; rr < n; ++rr) {
       const Row r = row_of(j + rr);

@@ -202,10 +202,12 @@ extern "C" int spec_history_reset(int32_t* counts, const int32_t* ids, int32_t* 
 // spec_process_logits
 // ---------------------------------------------------------------------------
 
-// Workgroups to spread a call over where each reads lists first, and where it
-// only streams; and the least elements of a piece worth one.
-constexpr int PR_TARGET = 1024;
+// Workgroups to spread a call over where each reads lists and streams, where
+// it only streams, and where it only walks lists; and the least elements of a
+// piece worth one.
+constexpr int PR_TARGET = 512;
 constexpr int PR_TARGET_PLAIN = 4096;
+constexpr int PR_TARGET_LISTS = 2048;
 constexpr int PR_MIN_PIECE = 4096;
 
 template <typename ET>
@@ -216,7 +218,7 @@ static hipError_t launch_process(ProcessArgs a, hipStream_t st) {
   while (a.hmask + 1 < names + names / 2) a.hmask = 2 * a.hmask + 1;
   int lds = Specials::bytes(names, a.hmask);
   const bool stream = a.in != a.out || a.mask_rows, lists = names || a.counts;
-  const int target = lists ? PR_TARGET : PR_TARGET_PLAIN;
+  const int target = !stream ? PR_TARGET_LISTS : lists ? PR_TARGET : PR_TARGET_PLAIN;
   const int most = (a.V + PR_MIN_PIECE - 1) / PR_MIN_PIECE, least = (a.V + TILE - 1) / TILE;
   // Pieces of the vocabulary (shares of the lists), then groups of rows; with
   // no lists to read, every row by itself.
@@ -227,7 +229,9 @@ static hipError_t launch_process(ProcessArgs a, hipStream_t st) {
   if (stream) {
     if (a.pieces > most) a.pieces = most;
     if (lists && a.pieces < least) a.pieces = least;
-    a.piece = ((a.V + a.pieces - 1) / a.pieces + 31) / 32 * 32;
+    // Whole 128-byte lines, or a whole row in whole units.
+    const int round = a.pieces > 1 ? 128 / (int)sizeof(ET) : VEC;
+    a.piece = ((a.V + a.pieces - 1) / a.pieces + round - 1) / round * round;
     a.pieces = (a.V + a.piece - 1) / a.piece;
     if (lists) {
       a.tile_off = (PR_ENTRIES * (int)sizeof(int2) + lds + 15) / 16 * 16;
@@ -245,7 +249,8 @@ static hipError_t launch_process(ProcessArgs a, hipStream_t st) {
   }
   const long long grid = (long long)a.B * a.pieces * a.groups;
   if (grid > 0x7FFFFFFFLL) return hipErrorInvalidValue;
-  if (stream) hipLaunchKernelGGL((process_stream_kernel<ET>), dim3((unsigned)grid), dim3(PR_NT), lds, st, a);
+  if (stream && lists) hipLaunchKernelGGL((process_stream_kernel<ET, true>), dim3((unsigned)grid), dim3(PR_NT), lds, st, a);
+  else if (stream) hipLaunchKernelGGL((process_stream_kernel<ET, false>), dim3((unsigned)grid), dim3(PR_NT), 0, st, a);
   else hipLaunchKernelGGL((process_lists_kernel<ET>), dim3((unsigned)grid), dim3(PR_NT), lds, st, a);
   return hipGetLastError();
 }
