@@ -47,10 +47,11 @@ extern "C" {
  *  hidden   [R][K] bf16 or fp32 (hidden_dtype), 16-byte aligned.
  *  weights  [N][K/2] bytes, 16-byte aligned: byte j of row n holds w[n][2j] in its low and
  *           w[n][2j+1] in its high four bits, each 0..15.
- *  scales   [N][K/group] bf16 or fp32 (scale_dtype), aligned to its element.
+ *  scales   [N][K/group] bf16 or fp32 (scale_dtype), aligned to its element; finite.
  *  zeros    [N][K/group] bytes, each 0..15 (the low four bits are used), or NULL: 8 everywhere.
  *  group    values of k that share a scale: 32, 64 or a multiple of 128; K is a multiple of it.
  *  R, K, N  R >= 0 and <= SL_MAX_ROWS (R == 0 is a no-op), 32 <= K <= SL_MAX_K, 1 <= N <= SV_MAX_VOCAB.
+ *           R * N and R * K below 2^34 (SV_ERR_UNSUPPORTED beyond).
  *  out      [R][N] bf16 or fp32 (out_dtype), aligned to its element; overlaps no input.
  *
  *  workspace  device buffer of spec_logits_w4_workspace_bytes(hidden_dtype, group, R, K) bytes,

@@ -409,10 +409,13 @@ class Sampler:
     def from_hidden(self, hidden, head, uniforms, temperature, out=None, stream=None, **kw):
         """The same from the drafter's hidden states [R, K] and its 4-bit head
         (logits.W4Head).  The logits, which the verify needs as its q rows, go to
-        `out` [R, V] (None: self.logits, overwritten by the next call)."""
+        `out` [R, V] (None: a buffer of the sampler's, overwritten by the next
+        such call) and stay reachable as self.logits."""
         if out is None:
-            out = getattr(self, "logits", None)
-        self.logits = head(hidden, out, _torch_dtype(self.dtype), stream)
+            out = self._buffer = head(hidden, getattr(self, "_buffer", None), _torch_dtype(self.dtype), stream)
+        else:
+            head(hidden, out, _torch_dtype(self.dtype), stream)
+        self.logits = out
         return self(self.logits, uniforms, temperature, stream=stream, **kw)
 
 

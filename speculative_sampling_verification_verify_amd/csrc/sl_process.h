@@ -241,7 +241,7 @@ __device__ __forceinline__ Sequence sequence(const ProcessArgs& a, int b) {
   const bool held = slot >= 0 && slot < a.S;
   q.counts = held ? a.counts + (size_t)slot * a.V : nullptr;
   q.ids = held ? a.ids + (size_t)slot * a.V : nullptr;
-  q.held = held ? min(a.num[slot], a.V) : 0;
+  q.held = held ? max(0, min(a.num[slot], a.V)) : 0;
   q.nd = a.drafts && penal ? a.first + a.J - 1 : 0;
   q.rows = a.rows ? min(a.rows[b], a.J) : a.J;
   return q;

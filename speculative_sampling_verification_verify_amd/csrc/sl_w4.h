@@ -11,10 +11,12 @@
 // into three bf16 parts (8 + 8 + 8 significand bits, truncated, so the parts
 // add up to the value exactly) that take three products.
 //
-// v_mfma_f32_16x16x32_bf16: lane l holds row / column l % 16 of either operand
-// at k = 8 * (l / 16) + 0..7, and rows 4 * (l / 16) + 0..3 of column l % 16 of
-// the result.  Rows are rows of x, columns are rows of the weight matrix: a
-// lane's results share one weight row, hence one scale.
+// Two forms.  Up to 16 rows (32 where K is short) the weight bytes bound: the
+// rows of x stay in LDS and the weights are streamed (w4_stream_kernel).  With
+// more rows the products count too: tiles over rows and columns, x brought into
+// operand order first (w4_order_kernel, w4_tile_kernel).  Rows of x are the
+// products' rows, rows of the weight matrix their columns: the results that a
+// lane holds share one weight row, hence one scale.
 #pragma once
 
 #include "sl_common.h"
@@ -37,7 +39,7 @@ struct W4Args {
   int gb;             // 128-k blocks per group (1 where the group is 32 or 64)
   int out_bf16;
   int rp;             // few rows: rows staged of a tile (a power of two, 16 unless R is smaller)
-  int row_tiles;      // more rows: tiles of MT * 16 rows
+  int row_tiles;      // more rows: tiles of MT * 32 rows
   int per_xcd;        // workgroups of one XCD
   char* xop;          // x in operand order and its sums per group (workspace)
   char* xsum;
@@ -187,146 +189,84 @@ __device__ __forceinline__ void w4_fetch_scales(const W4Args& a, uint32_t (&sw)[
   }
 }
 
-// Blocks b .. b + U - 1 of NT column tiles.  What lies beyond K repeats the
+// Blocks b .. b + U - 1 of a column tile.  What lies beyond K repeats the
 // row's end: it meets zeros of x.
-template <typename ST, int SUB, int U, int NT, bool ZEROS>
-__device__ __forceinline__ void w4_fetch(const W4Args& a, W4Ahead<ST, SUB, U> (&h)[NT], const W4Rows (&r)[NT], int quad, int b) {
+template <typename ST, int SUB, int U>
+__device__ __forceinline__ void w4_fetch(const W4Args& a, W4Ahead<ST, SUB, U>& h, const W4Rows& r, int quad, int b) {
   constexpr int NS = W4Ahead<ST, SUB, U>::NS;
+  const uint8_t* w = a.w + r.first * (size_t)(a.K / 2);
+  const uint32_t row = r.local * (uint32_t)(a.K / 2);
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const uint8_t* w = a.w + r[nt].first * (size_t)(a.K / 2);
-    const uint32_t row = r[nt].local * (uint32_t)(a.K / 2);
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      h[nt].w[u] = *reinterpret_cast<const u32x4*>(w + (row + (uint32_t)min((b + u) * 64 + quad * 16, a.K / 2 - 16)));
-  }
-  if (NS <= 2 && !ZEROS) {
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) w4_fetch_scales<ST, NS, ZEROS, false>(a, h[nt].s, h[nt].z, r[nt], b * SUB);
-  } else if (a.gb == 1 && (b + U) * SUB <= a.G) {
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) w4_fetch_scales<ST, NS, ZEROS, true>(a, h[nt].s, h[nt].z, r[nt], b * SUB);
-  } else {
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) w4_fetch_scales<ST, NS, ZEROS, false>(a, h[nt].s, h[nt].z, r[nt], b * SUB);
-  }
+  for (int u = 0; u < U; ++u)
+    h.w[u] = *reinterpret_cast<const u32x4*>(w + (row + (uint32_t)min((b + u) * 64 + quad * 16, a.K / 2 - 16)));
+  if (a.gb == 1 && (b + U) * SUB <= a.G) w4_fetch_scales<ST, NS, true, true>(a, h.s, h.z, r, b * SUB);
+  else w4_fetch_scales<ST, NS, true, false>(a, h.s, h.z, r, b * SUB);
 }
 
 // Block u of what was fetched, times the rows of x in LDS, onto tot.  x: the
 // operands of this block and lane, `mx` bytes from one row tile to the next,
-// `frag` from one operand to the next.  With SHIFT, 16 + z is taken out here:
-// xsum: the sums of this block and lane, `ms` bytes from one row tile to the
-// next.
-template <typename XT, typename ST, int SUB, int MT, int NT, int U, bool SHIFT>
-__device__ __forceinline__ void w4_block(const W4Args& a, const W4Ahead<ST, SUB, U> (&h)[NT], int u, const char* x, int mx,
-                                         int frag, const char* xsum, int ms, f32x4 (&tot)[MT][NT]) {
-  constexpr int P = W4Hidden<XT>::PARTS;
-  uint32_t d[NT][4];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    d[nt][0] = h[nt].w[u].x;
-    d[nt][1] = h[nt].w[u].y;
-    d[nt][2] = h[nt].w[u].z;
-    d[nt][3] = h[nt].w[u].w;
-    if (SUB > 1) w4_transpose(d[nt]);
-  }
-  // The block's groups, IG operands of 32 k each.
-  constexpr int IG = 4 / SUB;
+// `frag` from one operand to the next; xsum: the sums of this block and lane,
+// `ms` bytes from one row tile to the next.
+template <typename XT, typename ST, int SUB, int MT, int U>
+__device__ __forceinline__ void w4_block(const W4Args& a, const W4Ahead<ST, SUB, U>& h, int u, const char* x, int mx, int frag,
+                                         const char* xsum, int ms, f32x4 (&tot)[MT]) {
+  constexpr int P = W4Hidden<XT>::PARTS, IG = 4 / SUB;   // operands of 32 k in a group
+  uint32_t d[4] = {h.w[u].x, h.w[u].y, h.w[u].z, h.w[u].w};
+  if (SUB > 1) w4_transpose(d);
 #pragma unroll
   for (int sg = 0; sg < SUB; ++sg) {
-    f32x4 blk[MT][NT];
-    if constexpr (SUB == 1) {
-      // Four operands a group: one after the other, over all tiles.
+    f32x4 blk[MT];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        bf16x8 wv[NT];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) wv[nt] = w4_expand(d[nt][i]);
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-#pragma unroll
-          for (int p = P - 1; p >= 0; --p) {
-            const bf16x8 f = *reinterpret_cast<const bf16x8*>(x + m * mx + (i * P + p) * frag);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              blk[m][nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                  f, wv[nt], i == 0 && p == P - 1 ? f32x4{0, 0, 0, 0} : blk[m][nt], 0, 0, 0);
-          }
-        }
-        if (MT * NT >= 16) __builtin_amdgcn_sched_barrier(0);   // no operand is loaded far ahead: registers are full
-      }
-    } else {
-      // One or two: a row tile after the other, whose results are used up at once.
-      bf16x8 wv[IG][NT];
-#pragma unroll
-      for (int i = 0; i < IG; ++i)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) wv[i][nt] = w4_expand(d[nt][sg * IG + i]);
+    for (int i = 0; i < IG; ++i) {
+      const bf16x8 wv = w4_expand(d[sg * IG + i]);
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
 #pragma unroll
-        for (int i = 0; i < IG; ++i) {
-#pragma unroll
-          for (int p = P - 1; p >= 0; --p) {
-            const bf16x8 f = *reinterpret_cast<const bf16x8*>(x + m * mx + ((sg * IG + i) * P + p) * frag);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              blk[m][nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                  f, wv[i][nt], i == 0 && p == P - 1 ? f32x4{0, 0, 0, 0} : blk[m][nt], 0, 0, 0);
-          }
+        for (int p = P - 1; p >= 0; --p) {
+          const bf16x8 f = *reinterpret_cast<const bf16x8*>(x + m * mx + ((sg * IG + i) * P + p) * frag);
+          blk[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, wv, i == 0 && p == P - 1 ? f32x4{0, 0, 0, 0} : blk[m], 0, 0, 0);
         }
       }
     }
+    const float sc = w4_get(h.s, u * SUB + sg, (const ST*)nullptr), zz = w4_shift(a, h.z, u * SUB + sg);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      f32x4 x4 = {0, 0, 0, 0};
-      if (SHIFT) x4 = *reinterpret_cast<const f32x4*>(xsum + m * ms + sg * 64);
+      const f32x4 x4 = *reinterpret_cast<const f32x4*>(xsum + m * ms + sg * 64);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int e = u * SUB + sg;
-        const float sc = w4_get(h[nt].s, e, (const ST*)nullptr);
-        const float zz = SHIFT ? w4_shift(a, h[nt].z, e) : 0.0f;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float v = SHIFT ? __builtin_fmaf(-zz, x4[r], blk[m][nt][r]) : blk[m][nt][r];
-          tot[m][nt][r] = __builtin_fmaf(sc, v, tot[m][nt][r]);
-        }
-      }
+      for (int r = 0; r < 4; ++r) tot[m][r] = __builtin_fmaf(sc, __builtin_fmaf(-zz, x4[r], blk[m][r]), tot[m][r]);
     }
-    if (SUB > 1 && MT * NT >= 16) __builtin_amdgcn_sched_barrier(0);
   }
 }
 
-// Rows rt * MT * 16 .. of x, blocks b0 .. b1 - 1, into LDS as the products'
-// operands: [MT][block][i][part][quad][rp] 16 bytes, and their sums per group
-// (products with ones): [MT][block][SUB][16].  The caller has synchronised;
-// the rows are ready when this returns.
+// The rows of x into LDS as the products' operands: [MT][block][i][part][quad][rp] 16 bytes, and their sums per group
+// (products with ones): [MT][block][SUB][16].  The rows
+// are ready when this returns.
 template <typename XT, int SUB, int MT, int NTHR>
-__device__ __forceinline__ void w4_stage(const W4Args& a, int rt, int b0, int b1, int rp, char* xs, float* sums) {
+__device__ __forceinline__ void w4_stage(const W4Args& a, int nblk, int rp, char* xs, float* sums) {
   constexpr int P = W4Hidden<XT>::PARTS;
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, l16 = lane & 15, quad = lane >> 4;
   const int frag = 64 * rp, loff = (quad * rp + min(l16, rp - 1)) * 16;
-  const bf16x8 ones = __builtin_bit_cast(bf16x8, make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u));
+  const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
   const XT* x = reinterpret_cast<const XT*>(a.x);
-  const int units = (b1 - b0) * 4 * MT * 4 * rp;
+  const int units = nblk * 4 * MT * 4 * rp;
   for (int q = tid; q < units; q += NTHR) {
     const int r = q & (rp - 1), rest0 = q / rp, qd = rest0 & 3, rest = rest0 >> 2;
     const int m = rest % MT, i = rest / MT & 3, lb = rest / MT >> 2;
-    const int k = (b0 + lb) * 128 + (SUB > 1 ? i * 32 + qd * 8 : qd * 32 + i * 8);
-    const int row = min((rt * MT + m) * 16 + r, a.R - 1);
+    const int k = lb * 128 + (SUB > 1 ? i * 32 + qd * 8 : qd * 32 + i * 8);
+    const int row = min(m * 16 + r, a.R - 1);
     bf16x8 f[P];
     if (k < a.K) {
       W4Hidden<XT>::load(x + (size_t)row * a.K + k, f);
     } else {
 #pragma unroll
-      for (int p = 0; p < P; ++p) f[p] = __builtin_bit_cast(bf16x8, make_uint4(0, 0, 0, 0));
+      for (int p = 0; p < P; ++p) f[p] = __builtin_bit_cast(bf16x8, u32x4{0, 0, 0, 0});
     }
 #pragma unroll
     for (int p = 0; p < P; ++p)
-      *reinterpret_cast<bf16x8*>(xs + (((m * (b1 - b0) + lb) * 4 + i) * P + p) * frag + (qd * rp + r) * 16) = f[p];
+      *reinterpret_cast<bf16x8*>(xs + (((m * nblk + lb) * 4 + i) * P + p) * frag + (qd * rp + r) * 16) = f[p];
   }
   __syncthreads();
-  for (int q = wave; q < (b1 - b0) * MT; q += NTHR / 64) {
+  for (int q = wave; q < nblk * MT; q += NTHR / 64) {
     const int m = q % MT, lb = q / MT;
     f32x4 sum = {0, 0, 0, 0};
 #pragma unroll
@@ -334,10 +274,10 @@ __device__ __forceinline__ void w4_stage(const W4Args& a, int rt, int b0, int b1
 #pragma unroll
       for (int p = P - 1; p >= 0; --p)
         sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-            *reinterpret_cast<const bf16x8*>(xs + (((m * (b1 - b0) + lb) * 4 + i) * P + p) * frag + loff), ones, sum, 0, 0, 0);
+            *reinterpret_cast<const bf16x8*>(xs + (((m * nblk + lb) * 4 + i) * P + p) * frag + loff), ones, sum, 0, 0, 0);
       if (SUB == 4 || (SUB == 2 && (i & 1)) || i == 3) {
         const int sg = SUB == 4 ? i : SUB == 2 ? i >> 1 : 0;
-        if (l16 == 0) *reinterpret_cast<f32x4*>(sums + ((m * (b1 - b0) + lb) * SUB + sg) * 16 + quad * 4) = sum;
+        if (l16 == 0) *reinterpret_cast<f32x4*>(sums + ((m * nblk + lb) * SUB + sg) * 16 + quad * 4) = sum;
         sum = f32x4{0, 0, 0, 0};
       }
     }
@@ -345,23 +285,19 @@ __device__ __forceinline__ void w4_stage(const W4Args& a, int rt, int b0, int b1
   __syncthreads();
 }
 
-template <int MT, int NT>
-__device__ __forceinline__ void w4_store(const W4Args& a, int rt, int n0, const f32x4 (&tot)[MT][NT]) {
-  const int l16 = threadIdx.x & 15, quad = (threadIdx.x >> 4) & 3;
+template <int MT>
+__device__ __forceinline__ void w4_store(const W4Args& a, int n0, const f32x4 (&tot)[MT]) {
+  const int n = n0 + (threadIdx.x & 15), quad = (threadIdx.x >> 4) & 3;
+  if (n >= a.N) return;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int n = n0 + nt * 16 + l16;
-    if (n >= a.N) continue;
+  for (int m = 0; m < MT; ++m) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = (rt * MT + m) * 16 + quad * 4 + r;
-        if (row >= a.R) continue;
-        const size_t o = (size_t)row * a.N + n;
-        if (a.out_bf16) store_out(reinterpret_cast<uint16_t*>(a.out) + o, tot[m][nt][r]);
-        else store_out(reinterpret_cast<float*>(a.out) + o, tot[m][nt][r]);
-      }
+    for (int r = 0; r < 4; ++r) {
+      const int row = m * 16 + quad * 4 + r;
+      if (row >= a.R) continue;
+      const size_t o = (size_t)row * a.N + n;
+      if (a.out_bf16) store_out(reinterpret_cast<uint16_t*>(a.out) + o, tot[m][r]);
+      else store_out(reinterpret_cast<float*>(a.out) + o, tot[m][r]);
     }
   }
 }
@@ -372,6 +308,17 @@ __device__ __forceinline__ void w4_store(const W4Args& a, int rt, int n0, const 
 // time.  A wavefront streams its share without a barrier, fetching one step
 // ahead across tile borders; a tile that lies in several shares is added up at
 // the end, in the order of the wavefronts.
+//
+// v_mfma_f32_16x16x32_bf16: lane l holds row / column l % 16 of either operand
+// at k = 8 * (l / 16) + 0..7, and rows 4 * (l / 16) + 0..3 of column l % 16 of
+// the result.
+//
+// Bound by the weight bytes.  R=1, K=4096, N=152064, groups of 128 with zeros:
+// 65 us, 5.0 TB/s (a 1 GiB copy moves 5.1 TB/s), 12% of the matrix cores; R=16:
+// 78 us.  A first form, one wavefront to 16 columns with x from the cache, took
+// 187 us; one with x in LDS, a barrier for each set of columns and no even
+// shares, 129 us.  R=1, K=2048, N=32000, groups of 64: 11.6 us for 34.9 MB, of
+// which filling the 256 CUs' pipelines once is about half.
 // ---------------------------------------------------------------------------
 constexpr int W4S_NT = 1024;
 constexpr int W4S_WAVES = W4S_NT / 64;
@@ -394,47 +341,46 @@ __global__ __launch_bounds__(W4S_NT) void w4_stream_kernel(W4Args a) {
   int tile = t0 + first / steps, step = first % steps;             // of what is computed
   int ftile = tile, fstep = step;                                  // of what is fetched
 
-  auto fetch = [&](W4Ahead<ST, SUB, U> (&h)[1]) {
-    const W4Rows rows[1] = {w4_rows(a, ftile * 16, l16)};
-    w4_fetch<ST, SUB, U, 1, true>(a, h, rows, quad, fstep * U);
+  auto fetch = [&](W4Ahead<ST, SUB, U>& h) {
+    w4_fetch<ST, SUB, U>(a, h, w4_rows(a, ftile * 16, l16), quad, fstep * U);
     if (++fstep == steps) {
       fstep = 0;
       ++ftile;
     }
   };
-  f32x4 tot[MT][1], head[MT][1];
+  f32x4 tot[MT], head[MT];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) tot[m][0] = head[m][0] = f32x4{0, 0, 0, 0};
+  for (int m = 0; m < MT; ++m) tot[m] = head[m] = f32x4{0, 0, 0, 0};
   bool begun = step == 0;   // the current tile's first block is this wavefront's
-  auto compute = [&](const W4Ahead<ST, SUB, U> (&h)[1]) {
+  auto compute = [&](const W4Ahead<ST, SUB, U>& h) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (step * U + u < nblk) {
         const int b = step * U + u;
-        w4_block<XT, ST, SUB, MT, 1, U, true>(a, h, u, smem + b * 4 * P * frag + loff, nblk * 4 * P * frag, frag,
-                                        reinterpret_cast<const char*>(sums + b * SUB * 16 + quad * 4), nblk * SUB * 64, tot);
+        w4_block<XT, ST, SUB, MT, U>(a, h, u, smem + b * 4 * P * frag + loff, nblk * 4 * P * frag, frag,
+                                     reinterpret_cast<const char*>(sums + b * SUB * 16 + quad * 4), nblk * SUB * 64, tot);
       }
-      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_sched_barrier(0);   // no block's operands are loaded ahead: 128 registers for 16 wavefronts
     }
     if (++step == steps) {
       if (begun) {
-        w4_store<MT, 1>(a, 0, tile * 16, tot);
+        w4_store<MT>(a, tile * 16, tot);
       } else {
 #pragma unroll
-        for (int m = 0; m < MT; ++m) head[m][0] = tot[m][0];
+        for (int m = 0; m < MT; ++m) head[m] = tot[m];
       }
 #pragma unroll
-      for (int m = 0; m < MT; ++m) tot[m][0] = f32x4{0, 0, 0, 0};
+      for (int m = 0; m < MT; ++m) tot[m] = f32x4{0, 0, 0, 0};
       step = 0;
       ++tile;
       begun = true;
     }
   };
 
-  W4Ahead<ST, SUB, U> ha[1], hb[1];
+  W4Ahead<ST, SUB, U> ha, hb;
   const int n = last - first;
   if (n > 0) fetch(ha);
-  w4_stage<XT, SUB, MT, W4S_NT>(a, 0, 0, nblk, rp, smem, sums);
+  w4_stage<XT, SUB, MT, W4S_NT>(a, nblk, rp, smem, sums);
   for (int i = 0; i < n; i += 2) {
     if (i + 1 < n) fetch(hb);
     compute(ha);
@@ -447,19 +393,19 @@ __global__ __launch_bounds__(W4S_NT) void w4_stream_kernel(W4Args a) {
   // here, or all of this share is inside a tile.
   if (n > 0 && step > 0 && !begun) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m) head[m][0] = tot[m][0];
+    for (int m = 0; m < MT; ++m) head[m] = tot[m];
   }
   f32x4* part = reinterpret_cast<f32x4*>(smem);   // [wave][MT][lane], over the staged rows
   __syncthreads();
 #pragma unroll
-  for (int m = 0; m < MT; ++m) part[(wave * MT + m) * 64 + lane] = head[m][0];
+  for (int m = 0; m < MT; ++m) part[(wave * MT + m) * 64 + lane] = head[m];
   __syncthreads();
   if (n > 0 && step > 0 && begun) {
     const long long end = (long long)(tile - t0 + 1) * steps;
     for (int w = wave + 1; w < W4S_WAVES && all * w / W4S_WAVES < end; ++w)
 #pragma unroll
-      for (int m = 0; m < MT; ++m) tot[m][0] += part[(w * MT + m) * 64 + lane];
-    w4_store<MT, 1>(a, 0, tile * 16, tot);
+      for (int m = 0; m < MT; ++m) tot[m] += part[(w * MT + m) * 64 + lane];
+    w4_store<MT>(a, tile * 16, tot);
   }
 }
 
@@ -474,6 +420,19 @@ __global__ __launch_bounds__(W4S_NT) void w4_stream_kernel(W4Args a) {
 // sides float32, split into three bf16 parts each, of whose products the six
 // above 2^-24 are formed -- 6 products for 16 groups, which have 32 to 128 of
 // their own.
+//
+// R=320, K=4096, N=128256, groups of 128 with zeros: 390 us, 860 TFLOP/s, where
+// the library's bf16 product of the same shape, with 4 times the weight bytes,
+// takes 470 us (715) and its best on 8192^3 is 1198.  On the way: 16x16x32
+// products with a shift of each group, 942 us; with the product above, 566; the
+// checks out of the loop and the weights' pairs by two operations, 433; 32x32x16
+// products, 390.  Leaving out, one at a time, the fetch of the weights, the LDS
+// reads, the expansion or the scaling changes it by less than 6%, and half as
+// many workgroups on half the CUs take half the time: what bounds it is shared
+// by the CUs.  Chunks of two blocks, two blocks ahead and workgroups of four
+// wavefronts were the same or slower.  Groups of 32: 576 us (one column tile a
+// wavefront: two would spill registers).  R=32: 83 us, 3.4 TB/s, of which the
+// first launch is 5.
 // ---------------------------------------------------------------------------
 
 // Blocks of 128 k in the workspace: an even number.

@@ -21,6 +21,9 @@ static bool known(int dtype) { return dtype == SV_BF16 || dtype == SV_FP32; }
 static size_t size_of(int dtype) { return dtype == SV_BF16 ? 2 : 4; }
 static bool misaligned(const void* p, size_t n) { return (uintptr_t)p % n != 0; }
 
+// A launch holds fewer than 2^32 threads.
+static bool fits(long long groups, int threads) { return groups * threads < (1LL << 32); }
+
 // ---------------------------------------------------------------------------
 // spec_logits_w4
 // ---------------------------------------------------------------------------
@@ -40,7 +43,6 @@ static hipError_t launch_tile(W4Args a, hipStream_t st) {
   a.row_tiles = (a.R + 32 * MT - 1) / (32 * MT);
   const int cols = W4_WAVES * NT * 32;
   const long long sets = (long long)((a.N + cols - 1) / cols) * a.row_tiles;
-  if (sets > 0x7FFFFFF0LL) return hipErrorInvalidValue;
   a.per_xcd = (int)((sets + 7) / 8);
   hipLaunchKernelGGL((w4_tile_kernel<XT, ST, SUB, MT, NT, U, KC>), dim3((unsigned)a.per_xcd * 8), dim3(W4_NT), 0, st, a);
   return hipGetLastError();
@@ -98,7 +100,8 @@ static hipError_t launch_w4(W4Args a, const W4Plan& p, hipStream_t st) {
 
 template <typename XT, typename ST>
 static hipError_t launch_w4(const W4Args& a, int group, const W4Plan& p, hipStream_t st) {
-  return group == 32 ? launch_w4<XT, ST, 4>(a, p, st) : group == 64 ? launch_w4<XT, ST, 2>(a, p, st) : launch_w4<XT, ST, 1>(a, p, st);
+  if (group == 32) return launch_w4<XT, ST, 4>(a, p, st);
+  return group == 64 ? launch_w4<XT, ST, 2>(a, p, st) : launch_w4<XT, ST, 1>(a, p, st);
 }
 
 static int w4_sizes(int hidden_dtype, int group, int R, int K) {
@@ -129,6 +132,9 @@ extern "C" int spec_logits_w4(const void* hidden, int hidden_dtype, const uint8_
       misaligned(out, size_of(out_dtype)))
     return SV_ERR_ARG;
   const W4Plan p = w4_plan(hidden_dtype, group, R, K);
+  if (!p.stream && (!fits((long long)p.row_tiles * w4_blocks(K), 512) ||
+                    !fits(((long long)(N + 255) / 256 + 8) * p.row_tiles, W4_NT)))
+    return SV_ERR_UNSUPPORTED;
   if (p.bytes && (!workspace || workspace_bytes < p.bytes || misaligned(workspace, 256))) return SV_ERR_WORKSPACE;
   W4Args a;
   memset(&a, 0, sizeof a);
@@ -182,7 +188,7 @@ extern "C" int spec_history_append(int32_t* counts, int32_t* ids, int32_t* num, 
   if (!tokens || misaligned(tokens, 4)) return SV_ERR_ARG;
   const int chunks = (T + HA_NT - 1) / HA_NT;
   const long long grid = (long long)B * chunks;
-  if (grid > 0x7FFFFFFFLL) return SV_ERR_UNSUPPORTED;
+  if (!fits(grid, HA_NT)) return SV_ERR_UNSUPPORTED;
   const HistoryArgs a = {(uint32_t*)counts, ids, num, slots, tokens, S, V, B, T, prompt != 0, chunks};
   hipLaunchKernelGGL(history_append_kernel, dim3((unsigned)grid), dim3(HA_NT), 0, (hipStream_t)stream, a);
   return hip_status(hipGetLastError());
@@ -211,7 +217,7 @@ constexpr int PR_TARGET_LISTS = 2048;
 constexpr int PR_MIN_PIECE = 4096;
 
 template <typename ET>
-static hipError_t launch_process(ProcessArgs a, hipStream_t st) {
+static int launch_process(ProcessArgs a, hipStream_t st) {
   constexpr int VEC = Elem<ET>::VEC, TILE = PR_TILE * VEC;
   const int names = a.NB + (a.drafts ? a.first + a.J - 1 : 0);
   a.hmask = 63;
@@ -248,11 +254,11 @@ static hipError_t launch_process(ProcessArgs a, hipStream_t st) {
     a.groups = (int)(g > a.J ? a.J : g);
   }
   const long long grid = (long long)a.B * a.pieces * a.groups;
-  if (grid > 0x7FFFFFFFLL) return hipErrorInvalidValue;
+  if (!fits(grid, PR_NT)) return SV_ERR_UNSUPPORTED;
   if (stream && lists) hipLaunchKernelGGL((process_stream_kernel<ET, true>), dim3((unsigned)grid), dim3(PR_NT), lds, st, a);
   else if (stream) hipLaunchKernelGGL((process_stream_kernel<ET, false>), dim3((unsigned)grid), dim3(PR_NT), 0, st, a);
   else hipLaunchKernelGGL((process_lists_kernel<ET>), dim3((unsigned)grid), dim3(PR_NT), lds, st, a);
-  return hipGetLastError();
+  return hip_status(hipGetLastError());
 }
 
 extern "C" int spec_process_logits(const void* logits, void* out, int dtype, const int32_t* counts, const int32_t* ids,
@@ -308,7 +314,7 @@ extern "C" int spec_process_logits(const void* logits, void* out, int dtype, con
   a.W = (V + 31) / 32;
   a.wide = !misaligned(logits, 16) && !misaligned(out, 16);
   hipStream_t st = (hipStream_t)stream;
-  return hip_status(dtype == SV_BF16 ? launch_process<uint16_t>(a, st) : launch_process<float>(a, st));
+  return dtype == SV_BF16 ? launch_process<uint16_t>(a, st) : launch_process<float>(a, st);
 }
 
 extern "C" const char* spec_logits_strerror(int code) {

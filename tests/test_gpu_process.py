@@ -101,6 +101,8 @@ CASES = [
     dict(B=2, J=2, V=8190, hist=30, penalties=False, bias=5, masks=5), dict(B=3, J=2, V=12345, hist=0, masks=5, penalties=False),
     dict(B=2, J=60, V=300, hist=50, first=5), dict(B=2, J=1, V=3001, hist=500, bias=1024, masks=2),
     dict(B=1200, J=1, V=600, hist=20, masks=3, first=2), dict(B=1, J=3, V=131071, hist=2500, bias=17),
+    # more touched ids in a piece than a workgroup keeps
+    dict(B=2, J=3, V=5000, hist=6000, masks=2, bias=3, first=1), dict(B=1, J=2, V=4096, hist=9000, first=1),
 ]
 
 
@@ -314,6 +316,68 @@ def test_history_same_slot_many_times():
     L.spec_history_reset(h, dev(slots))
     ref.reset(slots)
     same_history(h, ref)
+
+
+def test_damaged_history_stays_inside():
+    """num and ids that no append made: nothing outside the arrays is read or
+    written, and slots with a sound state are not affected."""
+    V, S = 3000, 5
+    c = Case(41, 4, 3, V, S=S, hist=50, bias=4, masks=2, first=1)
+    c.slots = np.array([0, 1, 2, 3], dtype=np.int32)
+    h = c.gpu_hist
+    room = torch.full((3, V), 7, dtype=torch.int32, device="cuda")     # the next allocation, for what it is worth
+    h.num[0], h.num[1], h.num[2] = -5, V + 1000, -2147483648
+    h.ids[1] = torch.randint(-2147483648, 2147483647, (V,), dtype=torch.int64).int().cuda()
+    args = c.gpu_args()
+    x = c.logits.cuda()
+    out = torch.zeros_like(x)
+    L.spec_process_logits(x, out=out, **args)
+    y = x.clone()
+    L.spec_process_logits(y, **args)
+    plain = {k: v for k, v in args.items() if k not in ("masks", "mask_rows")}
+    z = x.clone()
+    L.spec_process_logits(z, **plain)
+    f32 = oracle.logits.process_rows_f32(c.logits.float().numpy(), **c.host_args())
+    want = torch.from_numpy(f32).bfloat16()[3]
+    assert torch.equal(out[3].cpu(), want) and torch.equal(y[3].cpu(), want)
+    L.spec_history_append(h, dev(np.array([[1, 2], [3, 4], [5, 6]], dtype=np.int32)))
+    L.spec_history_reset(h, dev(np.array([0, 1, 2], dtype=np.int32)))
+    torch.cuda.synchronize()
+    assert (h.num[:3] == 0).all() and (room == 7).all()
+    assert (h.counts[3:].cpu().numpy().view(np.uint32) == c.hist.counts()[3:]).all()
+
+
+def test_python_refusals():
+    """What the binding checks before a call: types, shapes, layout, pairs."""
+    B, J, V = 2, 3, 64
+    x = torch.zeros((B, J, V), device="cuda")
+    i = lambda *shape: torch.zeros(shape, dtype=torch.int32, device="cuda")
+    f = lambda *shape: torch.ones(shape, device="cuda")
+    h = L.History.new(B, V)
+    ok = dict(history=h, slots=i(B), draft_tokens=i(B, 2), repetition=f(B), bias_ids=i(B, 4), bias_values=f(B, 4),
+              masks=i(1, 2), mask_rows=i(B, J), rows=i(B))
+    L.spec_process_logits(x, **ok)
+    for bad in (dict(slots=i(B + 1)), dict(draft_tokens=i(B, 1)), dict(draft_tokens=i(B, 4)[:, ::2]),
+                dict(repetition=f(B, 1)), dict(bias_values=None), dict(bias_values=f(B, 3)), dict(masks=i(1, 3)),
+                dict(masks=i(0, 2)), dict(mask_rows=None), dict(mask_rows=i(B, J + 1)), dict(rows=i(1)),
+                dict(history=None), dict(history=L.History.new(B, V + 1)), dict(rows=i(B).cpu()),
+                dict(out=torch.zeros((B, J, V + 1), device="cuda")), dict(out=x.transpose(0, 1))):
+        with pytest.raises(ValueError):
+            L.spec_process_logits(x, **{**ok, **bad})
+    for bad in (dict(slots=i(B).long()), dict(draft_tokens=i(B, 2).long()), dict(presence=f(B).half()),
+                dict(out=x.bfloat16()), dict(bias_ids=i(B, 4).float())):
+        with pytest.raises(TypeError):
+            L.spec_process_logits(x, **{**ok, **bad})
+    with pytest.raises(TypeError):
+        L.spec_process_logits(x.half())
+    with pytest.raises(L.SpecLogitsError):      # more sequences than slots
+        L.spec_process_logits(x, history=L.History.new(1, V))
+    with pytest.raises(L.SpecLogitsError):
+        L.spec_history_append(h, i(3, 2))
+    with pytest.raises(ValueError):
+        L.spec_history_append(h, i(4))
+    with pytest.raises(TypeError):
+        L.spec_history_append(h, i(2, 2).long())
 
 
 def test_history_past_32_bits():

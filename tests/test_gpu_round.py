@@ -79,3 +79,43 @@ def test_rounds(dtype, V):
         assert (proc.history.counts.cpu().numpy().view(np.uint32) == ref.counts()).all()
         assert (proc.history.num.cpu().numpy() == ref.num()).all()
     assert seen >= 9          # most of the 18 verified sequences were compared
+
+
+def test_sampler_buffers():
+    """Logits given a place of their own stay there; the sampler's own buffer is
+    used again by the next call without one."""
+    rng = np.random.default_rng(0)
+    R, K, V = 3, 64, 130
+    head, sam = L.W4Head(*make_head(rng, V, K, 32)), binding.Sampler(R, V)
+    u, T = dev(rng.random(R).astype(np.float32)), torch.ones(R, device="cuda")
+    h = [dev(rng.standard_normal((R, K)), torch.bfloat16) for _ in range(3)]
+    mine = torch.empty((R, V), dtype=torch.bfloat16, device="cuda")
+    sam.from_hidden(h[0], head, u, T, out=mine)
+    assert sam.logits is mine
+    sam.from_hidden(h[1], head, u, T)
+    first = sam.logits
+    assert torch.equal(mine, head(h[0])) and torch.equal(first, head(h[1]))
+    sam.from_hidden(h[2], head, u, T)
+    assert sam.logits is first and torch.equal(first, head(h[2])) and torch.equal(mine, head(h[0]))
+    with pytest.raises(ValueError):
+        sam.from_hidden(h[0][:2].contiguous(), head, u, T)
+
+
+def test_candidates_of_a_tree():
+    """The K candidates of a sequence for the multi-candidate verify: each its own
+    drafts, one slot, one set of penalties."""
+    rng = np.random.default_rng(1)
+    B, K, n, V = 3, 4, 5, 500
+    ref = oracle.logits.TokenHistory(B, V)
+    hist = L.History.new(B, V)
+    prompt = zipf(rng, (B, 30), V)
+    L.spec_history_append(hist, dev(prompt))
+    ref.append(prompt)
+    slots = np.repeat(np.arange(B, dtype=np.int32), K)
+    cand = zipf(rng, (B, K, n), V)
+    rep = np.repeat(np.array([1.1, 1.0, 1.3], dtype=np.float32), K)
+    z = torch.randn((B, K, n + 1, V))
+    got = L.LogitProcessor(hist, dev(slots), dev(rep))(z.cuda().view(B * K, n + 1, V), dev(cand).view(B * K, n))
+    want = oracle.logits.process_rows_f32(z.numpy().reshape(B * K, n + 1, V), history=ref, slots=slots,
+                                          drafts=cand.reshape(B * K, n), repetition=rep)
+    assert torch.equal(got.cpu(), torch.from_numpy(want))

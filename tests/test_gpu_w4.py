@@ -116,6 +116,24 @@ def test_leading_dimensions_alignment_and_out():
         assert (room[0] == 123) and (room[1 + B * J * N:] == 123).all()
 
 
+def test_python_refusals():
+    w, s, z = make_head(np.random.default_rng(0), 8, 64, 32)
+    x = torch.zeros((3, 64), device="cuda", dtype=torch.bfloat16)
+    for bad in (dict(weights=w[:, :16]), dict(scales=s[:4]), dict(zeros=z[:, :1].contiguous()), dict(hidden=x.t()),
+                dict(hidden=x[:, :60].contiguous()), dict(out=torch.empty((3, 9), device="cuda")), dict(hidden=x.cpu()),
+                dict(weights=w.cpu()), dict(out=torch.empty((8, 3), device="cuda").t())):
+        with pytest.raises(ValueError):
+            L.spec_logits_w4(**{**dict(hidden=x, weights=w, scales=s, zeros=z), **bad})
+    for bad in (dict(hidden=x.half()), dict(weights=w.int()), dict(scales=s.half()), dict(zeros=z.int()),
+                dict(out=torch.empty((3, 8), device="cuda"), out_dtype=torch.bfloat16)):
+        with pytest.raises(TypeError):
+            L.spec_logits_w4(**{**dict(hidden=x, weights=w, scales=s, zeros=z), **bad})
+    with pytest.raises(L.SpecLogitsError):       # groups of 16
+        L.spec_logits_w4(x, w, torch.ones((8, 4), device="cuda"))
+    with pytest.raises(L.SpecLogitsError):       # rows that are not 16-byte aligned
+        L.spec_logits_w4(torch.zeros(65, device="cuda", dtype=torch.bfloat16)[1:].view(1, 64), w, s)
+
+
 def test_empty_call():
     w, s, z = make_head(np.random.default_rng(0), 8, 64, 32)
     assert L.spec_logits_w4(torch.empty((0, 64), device="cuda", dtype=torch.bfloat16), w, s, z).shape == (0, 8)

@@ -71,6 +71,7 @@ def test_w4_workspace():
                 for K in (256, 4096, 65536):
                     n = need(dt, group, R, K)
                     assert n == 0 and R <= 32 or n >= R * K * size + R * K // min(group, 128) * 4, (dt, group, R, K)
+    assert w4(R=1 << 20, N=1 << 20) == w4(R=1 << 20, K=65536, N=32) == SV_ERR_UNSUPPORTED   # more threads than a launch
     n = need(SV_BF16, 64, 100, 128)
     for ws, wsb in ((None, n), (FAKE, n - 1), (FAKE + 128, n)):
         assert w4(R=100, ws=ws, wsb=wsb) == SV_ERR_WORKSPACE
@@ -111,6 +112,7 @@ def test_process_refusals():
     assert call(M=L.SL_MAX_MASKS + 1) == call(B=1 << 19, J=4) == SV_ERR_UNSUPPORTED
     assert call(draft_stride=100, J=65, first=1) == SV_ERR_UNSUPPORTED
     assert call(draft_stride=1 << 30, J=2, first=(1 << 31) - 1) == SV_ERR_ARG
+    assert call(B=1 << 20, J=1, V=1 << 20) == SV_ERR_UNSUPPORTED      # more threads than a launch
     for k in ("B", "S", "NB", "M", "first"):
         assert call(**{k: -1}) == SV_ERR_ARG, k
     assert call(J=0) == call(V=0) == SV_ERR_ARG
