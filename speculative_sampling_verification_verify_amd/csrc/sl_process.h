@@ -135,7 +135,7 @@ struct Specials {
   int32_t* entry;     // [hmask + 1] entry of the slot's id
   uint32_t* twice;    // [(hmask + 32) / 32] bit h: the id in slot h was named more than once
   Special* entries;
-  int32_t* source;    // per entry: slot << 16 | the name that took it
+  int32_t* source;    // per entry: its slot
   int n;              // names: drafts and biases
   int hmask;
 
@@ -155,45 +155,57 @@ struct Specials {
     source = entry + hmask + 1;
     twice = reinterpret_cast<uint32_t*>(source + n);
     const int tid = threadIdx.x;
+    // The first names are loaded before the table is cleared.
+    int v[PR_UNITS];
+    float val[PR_UNITS];
+    auto names = [&](int i0) {
+#pragma unroll
+      for (int k = 0; k < PR_UNITS; ++k) {
+        const int i = i0 + k * PR_NT;
+        v[k] = i < n ? i < nd ? drafts[i] : bias_ids[i - nd] : -1;
+        val[k] = i >= nd && i < n ? bias_vals[i - nd] : 0.0f;
+      }
+    };
+    names(tid);
     for (int i = tid; i <= hmask; i += PR_NT) slot[i] = -1;
     for (int i = tid; i < (hmask + 32) / 32; i += PR_NT) twice[i] = 0;
     if (tid == 0) *count = 0;
     __syncthreads();
-    for (int i = tid; i < n; i += PR_NT) {
-      const int v = i < nd ? drafts[i] : bias_ids[i - nd];
-      if (v < lo || v >= hi) continue;
-      uint32_t h = hash_of(v) & hmask;
-      for (;;) {
-        const int old = atomicCAS(&slot[h], -1, v);
-        if (old == -1) {
-          const int e = atomicAdd(count, 1);
-          entry[h] = e;
-          source[e] = (int)(h << 16) | i;
+    for (int i0 = tid;;) {
+#pragma unroll
+      for (int k = 0; k < PR_UNITS; ++k) {
+        const int i = i0 + k * PR_NT;
+        if (v[k] < lo || v[k] >= hi) continue;
+        uint32_t h = hash_of(v[k]) & hmask;
+        for (;;) {
+          const int old = atomicCAS(&slot[h], -1, v[k]);
+          if (old == -1) {
+            const int e = atomicAdd(count, 1);
+            entry[h] = e;
+            source[e] = (int)h;
+            entries[e] = i < nd ? Special{1ull << i, 0.0f, 0} : Special{0ull, val[k], 1};
+          }
+          if (old == v[k]) atomicOr(&twice[h >> 5], 1u << (h & 31));
+          if (old == -1 || old == v[k]) break;
+          h = (h + 1) & hmask;
         }
-        if (old == v) atomicOr(&twice[h >> 5], 1u << (h & 31));
-        if (old == -1 || old == v) break;
-        h = (h + 1) & hmask;
       }
+      if ((i0 += PR_UNITS * PR_NT) >= n) break;
+      names(i0);
     }
     __syncthreads();
     const int ne = *count;
-    for (int e = tid; e < ne; e += PR_NT) {
-      const int h = source[e] >> 16, i = source[e] & 0xFFFF, v = slot[h];
+    for (int e = tid; e < ne; e += PR_NT) {   // those named more than once, in the order of their names
+      const int h = source[e];
+      if (!(twice[h >> 5] >> (h & 31) & 1u)) continue;
       Special s = {0ull, 0.0f, 0};
-      if (twice[h >> 5] >> (h & 31) & 1u) {
-        for (int d = 0; d < nd; ++d)
-          if (drafts[d] == v) s.drafts |= 1ull << d;
-        for (int d = 0; d < nb; ++d)
-          if (bias_ids[d] == v) {
-            s.bias = s.biased ? s.bias + bias_vals[d] : bias_vals[d];
-            s.biased = 1;
-          }
-      } else if (i < nd) {
-        s.drafts = 1ull << i;
-      } else {
-        s.bias = bias_vals[i - nd];
-        s.biased = 1;
-      }
+      for (int d = 0; d < nd; ++d)
+        if (drafts[d] == slot[h]) s.drafts |= 1ull << d;
+      for (int d = 0; d < nb; ++d)
+        if (bias_ids[d] == slot[h]) {
+          s.bias = s.biased ? s.bias + bias_vals[d] : bias_vals[d];
+          s.biased = 1;
+        }
       entries[e] = s;
     }
     __syncthreads();
@@ -206,7 +218,7 @@ struct Specials {
     while ((at = slot[h]) != -1 && at != v) h = (h + 1) & hmask;
     return at == v ? entry[h] : -1;
   }
-  __device__ __forceinline__ int id(int e) const { return slot[source[e] >> 16]; }
+  __device__ __forceinline__ int id(int e) const { return slot[source[e]]; }
 };
 
 // Adjusts one value of row j in place of what out holds there; nothing where
@@ -325,9 +337,16 @@ __global__ __launch_bounds__(PR_NT) void process_stream_kernel(ProcessArgs a) {
   int ne = 0, listed = 0;
   bool kept = true;
   if (lists) {
+    // The first ids and their counts are under way while the names are sorted out.
     int v[PR_UNITS];
+    uint32_t word[PR_UNITS];
+    auto ids = [&](int i0) {
 #pragma unroll
-    for (int k = 0; k < PR_UNITS; ++k) v[k] = tid + k * PR_NT < q.held ? q.ids[tid + k * PR_NT] : -1;
+      for (int k = 0; k < PR_UNITS; ++k) v[k] = i0 + k * PR_NT < q.held ? q.ids[i0 + k * PR_NT] : -1;
+#pragma unroll
+      for (int k = 0; k < PR_UNITS; ++k) word[k] = v[k] >= lo && v[k] < hi ? q.counts[v[k]] : 0u;
+    };
+    ids(tid);
     if (tid == 0) s_listed = 0;
     ne = sp.build(smem + PR_ENTRIES * sizeof(int2), &s_special, a.drafts + (size_t)b * a.draft_stride, q.nd,
                   a.bias_ids + (size_t)b * a.NB, a.bias_vals + (size_t)b * a.NB, a.NB, a.hmask, lo, hi);
@@ -337,11 +356,10 @@ __global__ __launch_bounds__(PR_NT) void process_stream_kernel(ProcessArgs a) {
       for (int k = 0; k < PR_UNITS; ++k) {
         if (v[k] < lo || v[k] >= hi || (ne && sp.find(v[k]) >= 0)) continue;
         const int at = atomicAdd(&s_listed, 1);
-        if (at < PR_ENTRIES) entries[at] = make_int2(v[k], (int)q.counts[v[k]]);
+        if (at < PR_ENTRIES) entries[at] = make_int2(v[k], (int)word[k]);
       }
       if ((i += PR_TILE) >= q.held) break;
-#pragma unroll
-      for (int k = 0; k < PR_UNITS; ++k) v[k] = i + k * PR_NT < q.held ? q.ids[i + k * PR_NT] : -1;
+      ids(i);
     }
     __syncthreads();
     kept = s_listed <= PR_ENTRIES;
