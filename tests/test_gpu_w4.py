@@ -20,7 +20,9 @@ pytestmark = pytest.mark.gpu
 SHAPES = [(1, 32, 1, 32), (1, 128, 16, 128), (3, 96, 17, 32), (2, 160, 33, 32), (16, 256, 33, 64), (17, 320, 50, 64),
           (33, 512, 100, 128), (5, 1024, 1000, 256), (2, 384, 7, 384), (64, 160, 130, 32), (100, 128, 300, 32),
           (130, 640, 257, 128), (15, 2048, 515, 64), (32, 4096, 271, 128), (65, 192, 64, 64), (257, 256, 385, 128),
-          (1, 8192, 130, 128), (9, 4128, 90, 32), (4, 1088, 2049, 64), (1, 512, 32000, 128), (48, 96, 31, 32)]
+          (1, 8192, 130, 128), (9, 4128, 90, 32), (4, 1088, 2049, 64), (1, 512, 32000, 128), (48, 96, 31, 32),
+          # groups of several blocks in tiles, and enough tiles for the widest ones
+          (40, 768, 100, 384), (20, 8192, 70, 1024), (2100, 256, 3001, 128), (2100, 128, 3001, 64), (2100, 64, 3001, 32)]
 
 
 def small_ints(rng, R, K, x):
