@@ -421,18 +421,20 @@ __global__ __launch_bounds__(W4S_NT) void w4_stream_kernel(W4Args a) {
 // above 2^-24 are formed -- 6 products for 16 groups, which have 32 to 128 of
 // their own.
 //
-// R=320, K=4096, N=128256, groups of 128 with zeros: 390 us, 860 TFLOP/s, where
+// R=320, K=4096, N=128256, groups of 128 with zeros: 380-389 us, 870 TFLOP/s, where
 // the library's bf16 product of the same shape, with 4 times the weight bytes,
 // takes 470 us (715) and its best on 8192^3 is 1198.  On the way: 16x16x32
 // products with a shift of each group, 942 us; with the product above, 566; the
 // checks out of the loop and the weights' pairs by two operations, 433; 32x32x16
-// products, 390.  Leaving out, one at a time, the fetch of the weights, the LDS
-// reads, the expansion or the scaling changes it by less than 6%, and half as
-// many workgroups on half the CUs take half the time: what bounds it is shared
-// by the CUs.  Chunks of two blocks, two blocks ahead and workgroups of four
-// wavefronts were the same or slower.  Groups of 32: 576 us (one column tile a
-// wavefront: two would spill registers).  R=32: 83 us, 3.4 TB/s, of which the
-// first launch is 5.
+// products, two column tiles a wavefront, 390; one column tile, which two
+// workgroups of a CU then share, 380 (at N=32000 153 -> 117).  Leaving out, one
+// at a time, the fetch of the weights, the LDS reads, the expansion or the
+// scaling changed the 390 by less than 6%, and half as many workgroups on half
+// the CUs took half the time: what bounds it is shared by the CUs.  Chunks of
+// two blocks (403 us), two blocks ahead (451) and workgroups of four wavefronts
+// (413) were slower.  Groups of 32: 573 us (16 scalings for 4 products).  R=64:
+// 107 us, R=32: 83 us (3.4 TB/s, of which the first launch is 5 us): there a
+// chunk's barrier and its wait for the weights.
 // ---------------------------------------------------------------------------
 
 // Blocks of 128 k in the workspace: an even number.
@@ -531,14 +533,15 @@ struct W4Wide {
 constexpr int W4_NT = 512;                 // threads per workgroup
 constexpr int W4_WAVES = W4_NT / 64;
 
-// MT * 32 rows by NT * 32 columns a wavefront, eight wavefronts side by side.
+// MT * 32 rows by 32 columns a wavefront, eight wavefronts side by side.
 // Operands of x come KC blocks at a time through two LDS buffers: the next
 // chunk's are loaded into registers before this one is computed and written
 // after it, one barrier a chunk.  Weights go from memory to registers, U
 // blocks ahead.
-template <typename XT, typename ST, int SUB, int MT, int NT, int U, int KC>
+template <typename XT, typename ST, int SUB, int MT, int U, int KC>
 __global__ __launch_bounds__(W4_NT) __attribute__((amdgpu_waves_per_eu(2))) void w4_tile_kernel(W4Args a) {
   constexpr int P = W4Hidden<XT>::PARTS;
+  constexpr int NT = 1;   // column tiles of 32 a wavefront; two take twice the registers, half the wavefronts
   constexpr int ROW = KC * 8 * P * 1024, OPS = MT * ROW;   // bytes of a chunk: one row tile's, all
   constexpr int NL = OPS / 16 / W4_NT;                     // 16-byte loads a thread
   static_assert(OPS % (16 * W4_NT) == 0 && KC % U == 0, "chunk does not fit the workgroup");

@@ -38,17 +38,19 @@ static hipError_t launch_stream(W4Args a, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <typename XT, typename ST, int SUB, int MT, int NT, int U, int KC>
+template <typename XT, typename ST, int SUB, int MT, int U, int KC>
 static hipError_t launch_tile(W4Args a, hipStream_t st) {
   a.row_tiles = (a.R + 32 * MT - 1) / (32 * MT);
-  const int cols = W4_WAVES * NT * 32;
+  const int cols = W4_WAVES * 32;
   const long long sets = (long long)((a.N + cols - 1) / cols) * a.row_tiles;
   a.per_xcd = (int)((sets + 7) / 8);
-  hipLaunchKernelGGL((w4_tile_kernel<XT, ST, SUB, MT, NT, U, KC>), dim3((unsigned)a.per_xcd * 8), dim3(W4_NT), 0, st, a);
+  hipLaunchKernelGGL((w4_tile_kernel<XT, ST, SUB, MT, U, KC>), dim3((unsigned)a.per_xcd * 8), dim3(W4_NT), 0, st, a);
   return hipGetLastError();
 }
 
-// The plan of a call, a function of its sizes and types alone.
+// The plan of a call, a function of its sizes and types alone.  The rows of x
+// stay in LDS where they fit it: at R=16, K=4096, N=152064 that takes 82 us and
+// the tiles 118, at R=32, K=2048, N=128256 43.5 and 46.5, K=1024 26 and 30.
 struct W4Plan {
   int stream;        // row tiles of the streaming kernel (1, 2), 0: two launches
   int rp;            // rows staged of a tile (streaming kernel)
@@ -56,7 +58,8 @@ struct W4Plan {
   size_t op_bytes, bytes;
 };
 
-// Row tiles of 32 of a workgroup in the two-launch form.
+// Row tiles of 32 of a workgroup in the two-launch form: two above 32 rows (one
+// takes 148 us instead of 110 at R=64, K=4096, N=128256).
 static int w4_tile_rows(int R) { return R > 32 ? 2 : 1; }
 
 static W4Plan w4_plan(int hidden_dtype, int group, int R, int K) {
@@ -88,14 +91,8 @@ static hipError_t launch_w4(W4Args a, const W4Plan& p, hipStream_t st) {
   hipLaunchKernelGGL((w4_order_kernel<XT, SUB>), dim3((unsigned)(p.row_tiles * w4_blocks(a.K))), dim3(512), 0, st, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  // Wide column tiles where they still give every CU a workgroup.
-  const int mt = w4_tile_rows(a.R);
-  if (mt == 1) return launch_tile<XT, ST, SUB, 1, 1, 2, 2>(a, st);
-  const bool wide = (long long)((a.N + 511) / 512) * (p.row_tiles / mt) >= 192;
-  // (Groups of 32, or of 64 with fp32 hidden states, would spill registers there.)
-  if constexpr (SUB == 1 || (SUB == 2 && W4Hidden<XT>::PARTS == 1))
-    if (wide) return launch_tile<XT, ST, SUB, 2, 2, 1, 1>(a, st);
-  return launch_tile<XT, ST, SUB, 2, 1, 1, 1>(a, st);
+  if (w4_tile_rows(a.R) == 1) return launch_tile<XT, ST, SUB, 1, 2, 2>(a, st);
+  return launch_tile<XT, ST, SUB, 2, 1, 1>(a, st);
 }
 
 template <typename XT, typename ST>
@@ -208,12 +205,16 @@ extern "C" int spec_history_reset(int32_t* counts, const int32_t* ids, int32_t* 
 // spec_process_logits
 // ---------------------------------------------------------------------------
 
-// Workgroups to spread a call over where each reads lists and streams, where
-// it only streams, and where it only walks lists; and the least elements of a
-// piece worth one.
+// Workgroups to spread a call over.  Where each reads lists and streams, few:
+// with 1024 instead of 512, B=1000, J=5, V=1000 in fp32 takes two groups of rows
+// to a sequence and 25 us, not 21.  Where it only streams, many: 2048, 4096 and
+// 8192 give 142, 121 and 114 us for a masked copy (B=128, J=9, V=128256), and 27,
+// 24 and 24.5 in place (B=64, J=5).  Where it only walks lists: 512 and 2048 give
+// 106 and 97 us (B=256, J=8, V=152064, 2000 tokens held).
 constexpr int PR_TARGET = 512;
 constexpr int PR_TARGET_PLAIN = 4096;
 constexpr int PR_TARGET_LISTS = 2048;
+// The least elements of a piece worth a workgroup (2048: the same).
 constexpr int PR_MIN_PIECE = 4096;
 
 template <typename ET>
@@ -225,6 +226,8 @@ static int launch_process(ProcessArgs a, hipStream_t st) {
   int lds = Specials::bytes(names, a.hmask);
   const bool stream = a.in != a.out || a.mask_rows, lists = names || a.counts;
   const int target = !stream ? PR_TARGET_LISTS : lists ? PR_TARGET : PR_TARGET_PLAIN;
+  // With lists, a piece goes through a tile (half a tile: 390 us instead of 294 at B=256, J=8, V=152064; two to
+  // four tiles a workgroup: 338).
   const int most = (a.V + PR_MIN_PIECE - 1) / PR_MIN_PIECE, least = (a.V + TILE - 1) / TILE;
   // Pieces of the vocabulary (shares of the lists), then groups of rows; with
   // no lists to read, every row by itself.
