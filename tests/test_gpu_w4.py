@@ -195,3 +195,28 @@ def test_repeatable_and_on_another_stream(R, N):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(c, L.spec_logits_w4(h, w, s, z)), k
+
+
+def test_two_graphs_at_once():
+    """Two captured calls that need a workspace, replayed at the same time."""
+    rng = np.random.default_rng(9)
+    K, N = 1024, 3000
+    w, s, z = make_head(rng, N, K, 128)
+    h = [dev(rng.standard_normal((R, K)), torch.bfloat16) for R in (40, 130)]
+    out = [torch.empty((len(x), N), dtype=torch.bfloat16, device="cuda") for x in h]
+    graphs, streams = [torch.cuda.CUDAGraph() for _ in h], [torch.cuda.Stream() for _ in h]
+    for g, x, o in zip(graphs, h, out):
+        with torch.cuda.graph(g):
+            for _ in range(5):
+                L.spec_logits_w4(x, w, s, z, out=o)
+    for k in range(3):
+        for x, o in zip(h, out):
+            x.copy_(dev(rng.standard_normal(tuple(x.shape)), torch.bfloat16))
+            o.zero_()
+        torch.cuda.synchronize()
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+        torch.cuda.synchronize()
+        for x, o in zip(h, out):
+            assert torch.equal(o, L.spec_logits_w4(x, w, s, z)), k
