@@ -460,7 +460,8 @@ __global__ __launch_bounds__(PR_NT) void process_stream_kernel(ProcessArgs a) {
 #pragma unroll
     for (int k = 0; k < PR_UNITS; ++k) {
       const int f = tid + k * PR_NT, rr = rows > 1 ? f / upr : 0, u = f - rr * upr;
-      if (rr < n && u < upr) *reinterpret_cast<uint4*>(buf + (rr * stride + VEC + u * VEC)) = nv[k];
+      // (Only the row's units: what lies behind them in the tile are elements that other lanes write below.)
+      if (rr < n && u < place(j + rr).units) *reinterpret_cast<uint4*>(buf + (rr * stride + VEC + u * VEC)) = nv[k];
     }
     for (int rr = 0; rr < n; ++rr) {
       const Row r = row_of(j + rr);
@@ -506,6 +507,8 @@ __global__ __launch_bounds__(PR_NT) void process_stream_kernel(ProcessArgs a) {
         r.out[e] = allowed(r.mask, e) ? reinterpret_cast<const RT*>(buf)[rr * stride + VEC + (e - r.start)] : (RT)Elem<ET>::NEG_INF;
       }
     }
+    // The next rows' units lie otherwise: nobody may fill the tile while another lane still reads these.
+    if (j + rows < j1) __syncthreads();
   }
 }
 
