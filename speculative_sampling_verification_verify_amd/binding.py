@@ -169,15 +169,9 @@ def _check(t: Optional[torch.Tensor], name: str, dtype, shape, device):
         raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
-def spec_verify(p_logits: torch.Tensor, q_logits: torch.Tensor, draft_tokens: torch.Tensor,
-                gamma_len: Optional[torch.Tensor], uniforms: torch.Tensor, temperature: torch.Tensor,
-                top_k: Optional[torch.Tensor], top_p: Optional[torch.Tensor],
-                out_tokens: torch.Tensor, out_n_accepted: torch.Tensor, out_alpha: torch.Tensor,
-                out_pq: Optional[torch.Tensor], workspace: torch.Tensor, stream=None,
-                lenience: Optional[torch.Tensor] = None, hints: int = 0) -> None:
-    """Enqueue one verify call (see include/spec_verify.h for the contract);
-    with `lenience` ([B] float32) or `hints` (SV_HINT_* flags) the call goes
-    to spec_verify_ex."""
+def _check_verify(p_logits, q_logits, draft_tokens, gamma_len, uniforms, temperature, top_k, top_p, out_tokens,
+                  out_n_accepted, out_alpha, out_pq, lenience):
+    """The checks of spec_verify's arguments; returns (B, gamma_max, V, dtype code)."""
     if p_logits.dim() != 3 or q_logits.dim() != 3:
         raise ValueError("p_logits must be [B, gamma_max+1, V] and q_logits [B, gamma_max, V]")
     B, G1, V = p_logits.shape
@@ -199,6 +193,32 @@ def spec_verify(p_logits: torch.Tensor, q_logits: torch.Tensor, draft_tokens: to
     _check(out_alpha, "out_alpha", torch.float32, (B, G), dev)
     _check(out_pq, "out_pq", torch.float32, (B, G, 2), dev)
     _check(lenience, "lenience", torch.float32, (B,), dev)
+    return B, G, V, dt
+
+
+def _require(**tensors) -> None:
+    for name, t in tensors.items():
+        if t is None:
+            raise ValueError(f"{name} is missing")
+
+
+def spec_verify(p_logits: torch.Tensor, q_logits: torch.Tensor, draft_tokens: torch.Tensor,
+                gamma_len: Optional[torch.Tensor], uniforms: torch.Tensor, temperature: torch.Tensor,
+                top_k: Optional[torch.Tensor], top_p: Optional[torch.Tensor],
+                out_tokens: torch.Tensor, out_n_accepted: torch.Tensor, out_alpha: torch.Tensor,
+                out_pq: Optional[torch.Tensor], workspace: torch.Tensor, stream=None,
+                lenience: Optional[torch.Tensor] = None, hints: int = 0) -> None:
+    """Enqueue one verify call (see include/spec_verify.h for the contract);
+    with `lenience` ([B] float32) or `hints` (SV_HINT_* flags) the call goes
+    to spec_verify_ex."""
+    B, G, V, dt = _check_verify(p_logits, q_logits, draft_tokens, gamma_len, uniforms, temperature, top_k, top_p,
+                                out_tokens, out_n_accepted, out_alpha, out_pq, lenience)
+    _enqueue_verify(p_logits, q_logits, draft_tokens, gamma_len, uniforms, temperature, top_k, top_p, out_tokens,
+                    out_n_accepted, out_alpha, out_pq, workspace, stream, lenience, hints, B, G, V, dt)
+
+
+def _enqueue_verify(p_logits, q_logits, draft_tokens, gamma_len, uniforms, temperature, top_k, top_p, out_tokens,
+                    out_n_accepted, out_alpha, out_pq, workspace, stream, lenience, hints, B, G, V, dt) -> None:
     wsb = workspace.numel() * workspace.element_size()
     if lenience is None and not hints:
         rc = lib().spec_verify(_ptr(p_logits), _ptr(q_logits), dt, _ptr(draft_tokens), _ptr(gamma_len),
@@ -275,15 +295,24 @@ class Verifier:
         [B, gamma_max+1] picks its grammar masks.  q_logits must be what the
         drafts were sampled from: a Sampler given the same processor leaves
         them so."""
+        args = (p_logits, q_logits, draft_tokens, gamma_len, uniforms, temperature, top_k, top_p,
+                self.tokens, self.n_accepted, self.alpha, self.pq)
+        sizes = _check_verify(*args, lenience)
         if processor is not None:
+            # A call that is refused leaves the logits as they were: what the verify would refuse, here first.
+            _require(draft_tokens=draft_tokens, uniforms=uniforms, temperature=temperature)
+            need = spec_verify_workspace_bytes(*sizes)
+            both = SV_HINT_NO_DENSE | SV_HINT_ALL_DENSE
+            if need == 0 or need > self.workspace.numel() or self.hints & ~(both | SV_HINT_UNFILTERED) or \
+                    self.hints & both == both:
+                raise ValueError("the verifier's workspace or hints do not fit these logits")
             rows = None
             if gamma_len is not None:   # target rows beyond gamma_b stay as they are
                 from .logits import on_stream
                 with on_stream(stream):
                     rows = gamma_len + 1
             processor(p_logits, draft_tokens, 0, mask_rows, rows, stream=stream)
-        spec_verify(p_logits, q_logits, draft_tokens, gamma_len, uniforms, temperature, top_k, top_p,
-                    self.tokens, self.n_accepted, self.alpha, self.pq, self.workspace, stream, lenience, self.hints)
+        _enqueue_verify(*args, self.workspace, stream, lenience, self.hints, *sizes)
         return self.tokens, self.n_accepted, self.alpha, self.pq
 
     def from_hidden(self, hidden, head, q_logits, draft_tokens, uniforms, temperature, stream=None, **kw):
@@ -389,9 +418,6 @@ class Sampler:
         if logits.dim() != 2:
             raise ValueError("logits must be [R, V]")
         R, V = logits.shape
-        if processor is not None:
-            processor(logits, draft_tokens, 0 if draft_tokens is None else draft_tokens.shape[1], mask_rows,
-                      stream=stream)
         dev = logits.device
         dt = _dtype_code(logits)
         _check(logits, "logits", logits.dtype, (self.R, self.V), dev)
@@ -399,6 +425,12 @@ class Sampler:
         _check(temperature, "temperature", torch.float32, (R,), dev)
         _check(top_k, "top_k", torch.int32, (R,), dev)
         _check(top_p, "top_p", torch.float32, (R,), dev)
+        if processor is not None:   # after every check: a call that is refused leaves the logits as they were
+            _require(uniforms=uniforms, temperature=temperature)
+            if spec_sample_workspace_bytes(R, V, dt) > self.workspace.numel():
+                raise ValueError("the sampler's workspace does not fit these logits")
+            processor(logits, draft_tokens, 0 if draft_tokens is None else draft_tokens.shape[1], mask_rows,
+                      stream=stream)
         rc = lib().spec_sample(_ptr(logits), dt, _ptr(uniforms), _ptr(temperature), _ptr(top_k), _ptr(top_p), R, V,
                                _ptr(self.tokens), _ptr(self.workspace),
                                self.workspace.numel() * self.workspace.element_size(), _stream_handle(stream))
