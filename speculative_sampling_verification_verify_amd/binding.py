@@ -271,6 +271,19 @@ def spec_verify_noalloc(p_logits: torch.Tensor, q_logits: torch.Tensor, draft_to
         raise SpecVerifyError(rc, "spec_verify_noalloc")
 
 
+def _logits_buffer(head, hidden, buffer, shape, dtype, dev, stream):
+    """The head's logits of `hidden` in `buffer`, or, where that is None, in a new
+    tensor that is kept as the buffer: hence the checks before one is made."""
+    if tuple(hidden.shape[:-1]) != shape[:-1]:
+        raise ValueError(f"hidden: expected {list(shape[:-1])} rows, got {list(hidden.shape[:-1])}")
+    if hidden.device != dev:
+        raise ValueError(f"hidden is on {hidden.device}, expected {dev}")
+    out = head(hidden, buffer, _torch_dtype(dtype), stream)
+    if tuple(out.shape) != shape:
+        raise ValueError(f"the head gives logits of {tuple(out.shape)}, expected {shape}")
+    return out
+
+
 class Verifier:
     """Owns a workspace and output buffers for calls of one shape."""
 
@@ -318,7 +331,8 @@ class Verifier:
     def from_hidden(self, hidden, head, q_logits, draft_tokens, uniforms, temperature, stream=None, **kw):
         """The same from the target's hidden states [B, gamma_max+1, K] and its
         4-bit head (logits.W4Head); the logits stay in self.p_logits."""
-        self.p_logits = head(hidden, getattr(self, "p_logits", None), _torch_dtype(self.dtype), stream)
+        self.p_logits = _logits_buffer(head, hidden, getattr(self, "p_logits", None), (self.B, self.G + 1, self.V),
+                                       self.dtype, self.tokens.device, stream)
         return self(self.p_logits, q_logits, draft_tokens, uniforms, temperature, stream=stream, **kw)
 
 
@@ -444,7 +458,8 @@ class Sampler:
         `out` [R, V] (None: a buffer of the sampler's, overwritten by the next
         such call) and stay reachable as self.logits."""
         if out is None:
-            out = self._buffer = head(hidden, getattr(self, "_buffer", None), _torch_dtype(self.dtype), stream)
+            out = self._buffer = _logits_buffer(head, hidden, getattr(self, "_buffer", None), (self.R, self.V),
+                                                self.dtype, self.tokens.device, stream)
         else:
             head(hidden, out, _torch_dtype(self.dtype), stream)
         self.logits = out

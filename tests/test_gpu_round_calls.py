@@ -77,3 +77,27 @@ def test_a_refused_call_leaves_the_logits():
     assert torch.equal(z, before)
     sam(z, r.u1, r.T, processor=r.proc)
     assert torch.equal(z, r.proc(before.clone())) and not torch.equal(z, before)
+
+
+def test_a_wrong_first_call_keeps_no_buffer():
+    """Hidden states with a wrong number of rows, or a head of another
+    vocabulary, in the first call: refused, and the next call is served."""
+    r = Round()
+    head = L.W4Head(*make_head(r.rng, V, K, 32))
+    other = L.W4Head(*make_head(r.rng, V + 4, K, 32))
+    h = lambda *s: dev(r.rng.standard_normal((*s, K)), torch.bfloat16)
+    ver, sam = binding.Verifier(B, G, V), binding.Sampler(B, V)
+    args = (r.q, r.x, r.u, r.T)
+    for bad, by in ((h(B, G), head), (h(B + 1, G + 1), head), (h(B * (G + 1)), head), (h(B, G + 1), other),
+                    (h(B, G + 1).cpu(), head)):
+        with pytest.raises((ValueError, binding.SpecVerifyError)):
+            ver.from_hidden(bad, by, *args)
+    good = h(B, G + 1)
+    ver.from_hidden(good, head, *args)
+    assert torch.equal(ver.p_logits, head(good))
+    for bad, by in ((h(B + 1), head), (h(B, 1), head), (h(B), other)):
+        with pytest.raises((ValueError, binding.SpecVerifyError)):
+            sam.from_hidden(bad, by, r.u1, r.T)
+    good = h(B)
+    sam.from_hidden(good, head, r.u1, r.T)
+    assert torch.equal(sam.logits, head(good))
