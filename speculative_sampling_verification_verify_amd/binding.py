@@ -305,9 +305,11 @@ class Verifier:
                  gamma_len=None, stream=None, lenience=None, processor=None, mask_rows=None):
         """With `processor` (logits.LogitProcessor), p_logits are adjusted in
         place before the verify, position by position of the drafts; mask_rows
-        [B, gamma_max+1] picks its grammar masks.  q_logits must be what the
+        [B, gamma_max+1] picks its grammar masks (needed where it has any).  q_logits must be what the
         drafts were sampled from: a Sampler given the same processor leaves
         them so."""
+        if processor is None and mask_rows is not None:
+            raise ValueError("mask_rows without a processor")
         args = (p_logits, q_logits, draft_tokens, gamma_len, uniforms, temperature, top_k, top_p,
                 self.tokens, self.n_accepted, self.alpha, self.pq)
         sizes = _check_verify(*args, lenience)
@@ -428,7 +430,10 @@ class Sampler:
                  draft_tokens=None, mask_rows=None):
         """With `processor` (logits.LogitProcessor), the logits are adjusted in
         place before the draw: they follow the history and draft_tokens [R, n],
-        the sequence's drafts so far; mask_rows [R] picks grammar masks."""
+        the sequence's drafts so far; mask_rows [R] picks its grammar masks
+        (needed where it has any)."""
+        if processor is None and mask_rows is not None:
+            raise ValueError("mask_rows without a processor")
         if logits.dim() != 2:
             raise ValueError("logits must be [R, V]")
         R, V = logits.shape

@@ -297,7 +297,8 @@ def spec_process_logits(logits: torch.Tensor, out: Optional[torch.Tensor] = None
 class LogitProcessor:
     """What B sequences ask of their logits: their history and slots, their
     penalties and biases, and the table of grammar masks.  Called with logits,
-    adjusts them in place (or into `out`)."""
+    adjusts them in place (or into `out`).  With masks, every call says by
+    mask_rows which of them a row takes (-1: none)."""
 
     def __init__(self, history: Optional[History] = None, slots: Optional[torch.Tensor] = None,
                  repetition: Optional[torch.Tensor] = None, presence: Optional[torch.Tensor] = None,
@@ -310,7 +311,7 @@ class LogitProcessor:
     def __call__(self, logits, draft_tokens=None, first=0, mask_rows=None, rows=None, out=None, stream=None):
         return spec_process_logits(logits, out, self.history, self.slots, draft_tokens, first, self.repetition,
                                    self.presence, self.frequency, self.bias_ids, self.bias_values,
-                                   None if mask_rows is None else self.masks, mask_rows, rows, stream)
+                                   self.masks, mask_rows, rows, stream)
 
     def append(self, tokens, stream=None):
         """Add a verify's out_tokens [B, T] (or a prompt's, with history calls of

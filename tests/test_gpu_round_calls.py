@@ -101,3 +101,31 @@ def test_a_wrong_first_call_keeps_no_buffer():
     good = h(B)
     sam.from_hidden(good, head, r.u1, r.T)
     assert torch.equal(sam.logits, head(good))
+
+
+def test_a_grammar_is_never_dropped():
+    """A processor with masks refuses a call that does not say which, before it
+    writes anything; so do calls that pick masks where there are none."""
+    r = Round()
+    allowed = np.zeros((1, V), dtype=bool)
+    allowed[0, 5] = True
+    proc = L.LogitProcessor(r.history, masks=dev(pack_masks(allowed)))
+    ver, sam = binding.Verifier(B, G, V), binding.Sampler(B, V)
+    p, z = r.p.clone(), r.p[:, 0].contiguous()
+    z0 = z.clone()
+    for call in (lambda: proc(p, r.x), lambda: ver(p, r.q, r.x, r.u, r.T, processor=proc), lambda: proc(z),
+                 lambda: sam(z, r.u1, r.T, processor=proc)):
+        with pytest.raises(ValueError):
+            call()
+    at = torch.zeros((B, G + 1), dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        r.proc(p, r.x, mask_rows=at)         # a processor without masks
+    with pytest.raises(ValueError):
+        ver(p, r.q, r.x, r.u, r.T, mask_rows=at)
+    with pytest.raises(ValueError):
+        sam(z, r.u1, r.T, mask_rows=at[:, 0].contiguous())
+    torch.cuda.synchronize()
+    assert torch.equal(p, r.p) and torch.equal(z, z0)
+    assert (sam(z, r.u1, r.T, processor=proc, mask_rows=at[:, 0].contiguous()) == 5).all()
+    proc(p, r.x, mask_rows=at - 1)           # -1: no mask
+    assert torch.equal(p, r.p)
