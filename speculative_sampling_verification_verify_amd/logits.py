@@ -316,4 +316,6 @@ class LogitProcessor:
     def append(self, tokens, stream=None):
         """Add a verify's out_tokens [B, T] (or a prompt's, with history calls of
         one's own) to the sequences' history."""
+        if self.history is None:
+            raise ValueError("the processor has no history")
         spec_history_append(self.history, tokens, self.slots, stream=stream)

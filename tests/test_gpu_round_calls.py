@@ -129,3 +129,9 @@ def test_a_grammar_is_never_dropped():
     assert (sam(z, r.u1, r.T, processor=proc, mask_rows=at[:, 0].contiguous()) == 5).all()
     proc(p, r.x, mask_rows=at - 1)           # -1: no mask
     assert torch.equal(p, r.p)
+
+
+def test_append_without_a_history():
+    with pytest.raises(ValueError, match="no history"):
+        L.LogitProcessor(bias_ids=torch.zeros((1, 1), dtype=torch.int32), bias_values=torch.zeros((1, 1))).append(
+            torch.zeros((1, 1), dtype=torch.int32))
