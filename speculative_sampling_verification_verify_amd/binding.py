@@ -324,7 +324,7 @@ class Verifier:
             rows = None
             if gamma_len is not None:   # target rows beyond gamma_b stay as they are
                 from .logits import on_stream
-                with on_stream(stream):
+                with on_stream(stream, p_logits.device):
                     rows = gamma_len + 1
             processor(p_logits, draft_tokens, 0, mask_rows, rows, stream=stream)
         _enqueue_verify(*args, self.workspace, stream, lenience, self.hints, *sizes)

@@ -107,12 +107,18 @@ def _call(fn, where: str, dev: torch.device, stream, *args) -> None:
         raise SpecLogitsError(rc, where)
 
 
-def on_stream(stream):
+def on_stream(stream, dev: Optional[torch.device] = None):
     """A context in which torch allocates and computes on `stream` (a torch
-    stream, a handle, or None: the current one)."""
+    stream, a handle of one of `dev`, or None: the current one).  Handle 0 is the
+    default stream, which ExternalStream does not give; a handle names no device
+    (dev None: the current one), and memory must come from the stream that uses
+    it."""
     if stream is None:
         return contextlib.nullcontext()
-    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+    if not hasattr(stream, "cuda_stream"):
+        h = int(stream)
+        stream = torch.cuda.ExternalStream(h, device=dev) if h else torch.cuda.default_stream(dev)
+    return torch.cuda.stream(stream)
 
 
 # ---------------------------------------------------------------------------
@@ -141,7 +147,7 @@ def spec_logits_w4(hidden: torch.Tensor, weights: torch.Tensor, scales: torch.Te
     if K == 0 or G == 0 or N == 0 or K % G:
         raise ValueError(f"scales: {G} groups do not divide K = {K}")
     if out is None:
-        with on_stream(stream):
+        with on_stream(stream, dev):
             out = torch.empty((*lead, N), dtype=out_dtype or hidden.dtype, device=dev)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out: expected {out_dtype}, got {out.dtype}")
@@ -149,7 +155,7 @@ def spec_logits_w4(hidden: torch.Tensor, weights: torch.Tensor, scales: torch.Te
     need = lib().spec_logits_w4_workspace_bytes(xt, K // G, R, K)
     ws = None
     if need:
-        with on_stream(stream):
+        with on_stream(stream, dev):
             ws = torch.empty(need, dtype=torch.uint8, device=dev)
     _call(_lib.spec_logits_w4, "spec_logits_w4", dev, stream, x, xt, w, s, st, z, K // G, R, K, N, o, _dtype_code(out),
           None if ws is None else ws.data_ptr(), need)

@@ -135,3 +135,48 @@ def test_append_without_a_history():
     with pytest.raises(ValueError, match="no history"):
         L.LogitProcessor(bias_ids=torch.zeros((1, 1), dtype=torch.int32), bias_values=torch.zeros((1, 1))).append(
             torch.zeros((1, 1), dtype=torch.int32))
+
+
+def test_streams_given_as_handles():
+    """Inside on_stream torch works on the stream that the handle names, the
+    default stream (handle 0) included, whatever stream is current."""
+    gpu, side, other = torch.device("cuda", 0), torch.cuda.Stream(), torch.cuda.Stream()
+    for current in (torch.cuda.default_stream(), other):
+        with torch.cuda.stream(current):
+            for s, h in ((0, 0), (side.cuda_stream, side.cuda_stream), (side, side.cuda_stream), (None, current.cuda_stream),
+                         (torch.cuda.default_stream(), 0)):
+                with L.on_stream(s, gpu):
+                    assert torch.cuda.current_stream().cuda_stream == h
+            assert torch.cuda.current_stream() == current
+
+
+def test_handles_name_no_device(monkeypatch):
+    """The stream made of a handle is one of the tensors' device, which need not
+    be the current one."""
+    made = []
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h, device=None: made.append((h, device)) or torch.cuda.Stream())
+    with L.on_stream(77, torch.device("cuda", 0)):
+        pass
+    assert made == [(77, torch.device("cuda", 0))]
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_rounds_on_the_default_stream(handle):
+    """From a side stream, calls that name the default stream: workspaces and
+    row limits are made where they are used."""
+    r = Round()
+    head = L.W4Head(*make_head(r.rng, V, K, 32))
+    h = dev(r.rng.standard_normal((40, K)), torch.bfloat16)      # rows that need a workspace
+    hb = dev(r.rng.standard_normal((B, G + 1, K)), torch.bfloat16)
+    ver = binding.Verifier(B, G, V)
+    gamma = torch.tensor([G, 1, G], dtype=torch.int32, device="cuda")
+    want, full = head(h), head(hb)
+    r.proc(full, r.x, rows=gamma + 1)
+    stream = 0 if handle else torch.cuda.default_stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        got = [head(h, stream=stream) for _ in range(20)]
+        ver.from_hidden(hb, head, r.q, r.x, r.u, r.T, gamma_len=gamma, processor=r.proc, stream=stream)
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want) for g in got)
+    assert torch.equal(ver.p_logits, full)
