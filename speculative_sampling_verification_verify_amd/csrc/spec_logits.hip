@@ -101,11 +101,16 @@ static hipError_t launch_w4(const W4Args& a, int group, const W4Plan& p, hipStre
   return group == 64 ? launch_w4<XT, ST, 2>(a, p, st) : launch_w4<XT, ST, 1>(a, p, st);
 }
 
+// R * K and R * N stay below it, so that both launches hold fewer than 2^32
+// threads: one for 8 values of x, 512 for 32 rows and 256 columns.
+constexpr long long W4_MOST = 1LL << 34;
+
 static int w4_sizes(int hidden_dtype, int group, int R, int K) {
   if (!known(hidden_dtype) || R > SL_MAX_ROWS || K > SL_MAX_K) return SV_ERR_UNSUPPORTED;
   if (R < 0 || K < 1 || group < 1) return SV_ERR_ARG;
   if (group != 32 && group != 64 && group % 128 != 0) return SV_ERR_UNSUPPORTED;
-  return K % group != 0 ? SV_ERR_ARG : SV_OK;
+  if (K % group != 0) return SV_ERR_ARG;
+  return (long long)R * K < W4_MOST ? SV_OK : SV_ERR_UNSUPPORTED;
 }
 
 }  // namespace sl
@@ -123,15 +128,13 @@ extern "C" int spec_logits_w4(const void* hidden, int hidden_dtype, const uint8_
   const int rc = w4_sizes(hidden_dtype, group, R, K);
   if (rc != SV_OK) return rc;
   if (N < 1) return SV_ERR_ARG;
+  if ((long long)R * N >= W4_MOST) return SV_ERR_UNSUPPORTED;
   if (R == 0) return SV_OK;
   if (!hidden || !weights || !scales || !out) return SV_ERR_ARG;
   if (misaligned(hidden, 16) || misaligned(weights, 16) || misaligned(scales, size_of(scale_dtype)) ||
       misaligned(out, size_of(out_dtype)))
     return SV_ERR_ARG;
   const W4Plan p = w4_plan(hidden_dtype, group, R, K);
-  if (!p.stream && (!fits((long long)p.row_tiles * w4_blocks(K), 512) ||
-                    !fits(((long long)(N + 255) / 256 + 8) * p.row_tiles, W4_NT)))
-    return SV_ERR_UNSUPPORTED;
   if (p.bytes && (!workspace || workspace_bytes < p.bytes || misaligned(workspace, 256))) return SV_ERR_WORKSPACE;
   W4Args a;
   memset(&a, 0, sizeof a);

@@ -77,6 +77,18 @@ def test_w4_workspace():
         assert w4(R=100, ws=ws, wsb=wsb) == SV_ERR_WORKSPACE
 
 
+def test_w4_largest_sizes():
+    """R * K and R * N: below 2^34 the call goes on to ask for its workspace, from
+    there on it is refused, and no workspace is asked for."""
+    need = _lib().spec_logits_w4_workspace_bytes
+    assert w4(R=1 << 18, K=65472, N=32) == SV_ERR_WORKSPACE and need(SV_BF16, 64, 1 << 18, 65472) >= (1 << 18) * 65472 * 2
+    assert w4(R=1 << 18, K=65536, N=32) == SV_ERR_UNSUPPORTED and need(SV_BF16, 64, 1 << 18, 65536) == 0
+    for R, N in ((1 << 20, (1 << 14) - 1), ((1 << 14) - 1, 1 << 20), (131071, 131072)):
+        assert R * N < 1 << 34 and w4(R=R, N=N) == SV_ERR_WORKSPACE, (R, N)
+    for R, N in ((1 << 20, 1 << 14), (1 << 14, 1 << 20), (131072, 131073)):
+        assert R * N >= 1 << 34 and w4(R=R, N=N) == SV_ERR_UNSUPPORTED, (R, N)
+
+
 def test_history_refusals():
     def append(c=FAKE, i=FAKE, n=FAKE, S=4, V=100, slots=FAKE, t=FAKE, B=3, T=5):
         return _lib().spec_history_append(c, i, n, S, V, slots, t, B, T, 0, None)
