@@ -116,8 +116,8 @@ int spec_history_reset(int32_t* counts, const int32_t* ids, int32_t* num, int S,
  *
  *  logits      [B][J][V] bf16 or fp32, aligned to its element (16-byte alignment takes the
  *              wide path).
- *  out         [B][J][V], same type: `logits` itself (in place) or no overlap with it.  In place,
- *              only what changes is written.
+ *  out         [B][J][V], same type: `logits` itself (in place) or no overlap with it
+ *              (SV_ERR_ARG).  In place, only what changes is written.
  *  counts, ids, num, S: a history as above, or NULL, NULL, NULL, 0: no history.
  *  slots       [B] int32 or NULL (slot b; then B <= S).  A slot outside [0, S) has no history.
  *              Slots may repeat (the candidates of one sequence share its history).

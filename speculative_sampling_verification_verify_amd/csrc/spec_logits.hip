@@ -21,6 +21,10 @@ static bool known(int dtype) { return dtype == SV_BF16 || dtype == SV_FP32; }
 static size_t size_of(int dtype) { return dtype == SV_BF16 ? 2 : 4; }
 static bool misaligned(const void* p, size_t n) { return (uintptr_t)p % n != 0; }
 
+static bool overlap(const void* p, size_t np, const void* q, size_t nq) {
+  return (uintptr_t)p < (uintptr_t)q + nq && (uintptr_t)q < (uintptr_t)p + np;
+}
+
 // A launch holds fewer than 2^32 threads.
 static bool fits(long long groups, int threads) { return groups * threads < (1LL << 32); }
 
@@ -291,6 +295,8 @@ extern "C" int spec_process_logits(const void* logits, void* out, int dtype, con
   for (const void* p : words)
     if (misaligned(p, 4)) return SV_ERR_ARG;
   if (misaligned(logits, size_of(dtype)) || misaligned(out, size_of(dtype))) return SV_ERR_ARG;
+  const size_t bytes = (size_t)B * J * V * size_of(dtype);
+  if (out != logits && overlap(logits, bytes, out, bytes)) return SV_ERR_ARG;
 
   ProcessArgs a;
   memset(&a, 0, sizeof a);

@@ -141,6 +141,20 @@ def test_process_refusals():
     assert call(logits=FAKE + 1) == call(out=FAKE + 1) == call(out=FAKE + 2, dtype=SV_FP32) == SV_ERR_ARG
 
 
+def test_process_refuses_a_partial_overlap():
+    """`out` is the logits or lies apart from them.  (Sizes that are refused
+    later, as more threads than a launch holds, so that no call gets further.)"""
+    B = V = 1 << 20
+    n, at = B * V * 2, 1 << 45
+
+    def call(out):
+        return _lib().spec_process_logits(at, out, SV_BF16, None, None, None, 0, None, None, 0, 0, None, None, None, None, None, 0,
+                                          None, 0, None, None, B, 1, V, None)
+
+    assert call(at) == call(at + n) == call(at - n) == call(FAKE) == SV_ERR_UNSUPPORTED
+    assert call(at + 2) == call(at - 2) == call(at + n - 2) == call(at - n + 2) == call(at + n // 2) == SV_ERR_ARG
+
+
 def test_strerror_and_missing_library(monkeypatch, tmp_path):
     _lib()
     for code in (0, -1, -2, -4, 17):
