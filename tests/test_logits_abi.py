@@ -151,7 +151,7 @@ def test_process_refuses_a_partial_overlap():
         return _lib().spec_process_logits(at, out, SV_BF16, None, None, None, 0, None, None, 0, 0, None, None, None, None, None, 0,
                                           None, 0, None, None, B, 1, V, None)
 
-    assert call(at) == call(at + n) == call(at - n) == call(FAKE) == SV_ERR_UNSUPPORTED
+    assert call(at + n) == call(at - n) == call(FAKE) == SV_ERR_UNSUPPORTED
     assert call(at + 2) == call(at - 2) == call(at + n - 2) == call(at - n + 2) == call(at + n // 2) == SV_ERR_ARG
 
 
