@@ -143,12 +143,12 @@ def test_process_refusals():
 
 def test_process_refuses_a_partial_overlap():
     """`out` is the logits or lies apart from them.  (Sizes that are refused
-    later, as more threads than a launch holds, so that no call gets further.)"""
+    later, with biases as more threads than a launch holds: no call gets further.)"""
     B = V = 1 << 20
     n, at = B * V * 2, 1 << 45
 
     def call(out):
-        return _lib().spec_process_logits(at, out, SV_BF16, None, None, None, 0, None, None, 0, 0, None, None, None, None, None, 0,
+        return _lib().spec_process_logits(at, out, SV_BF16, None, None, None, 0, None, None, 0, 0, None, None, None, FAKE, FAKE, 3,
                                           None, 0, None, None, B, 1, V, None)
 
     assert call(at + n) == call(at - n) == call(FAKE) == SV_ERR_UNSUPPORTED
