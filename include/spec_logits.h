@@ -47,7 +47,7 @@ extern "C" {
  *  hidden   [R][K] bf16 or fp32 (hidden_dtype), 16-byte aligned.
  *  weights  [N][K/2] bytes, 16-byte aligned: byte j of row n holds w[n][2j] in its low and
  *           w[n][2j+1] in its high four bits, each 0..15.
- *  scales   [N][K/group] bf16 or fp32 (scale_dtype), aligned to its element; finite.
+ *  scales   [N][K/group] bf16 or fp32 (scale_dtype), aligned to its element; finite, below 2^124.
  *  zeros    [N][K/group] bytes, each 0..15 (the low four bits are used), or NULL: 8 everywhere.
  *  group    values of k that share a scale: 32, 64 or a multiple of 128; K is a multiple of it.
  *  R, K, N  R >= 0 and <= SL_MAX_ROWS (R == 0 is a no-op), 32 <= K <= SL_MAX_K, 1 <= N <= SV_MAX_VOCAB.
@@ -58,11 +58,13 @@ extern "C" {
  *           256-byte aligned (NULL where that is 0, as it is for few rows); it needs no
  *           preparation and holds nothing after the call.  Calls that share one must be ordered.
  *
- * The products are exact, the sums are held in float32 and rounded once, to
- * nearest even, at the end.  A row of `hidden` with a NaN or an infinity gives
- * a row of NaN (which the verify reports as invalid); other rows are not
- * affected.  A value of `hidden` beyond 2^115 may give NaN too, because the
- * sums inside a group are formed before its scale.
+ * The products w x are exact.  Sums are held in float32, those of the weights
+ * and of the zero points apart within 256 values of k, and rounded once, to
+ * nearest even, at the end: the error is that of a float32 product.  A row of
+ * `hidden` with a NaN or an infinity gives a row of NaN (which the verify
+ * reports as invalid); other rows are not affected.  A value of `hidden` beyond
+ * 2^115 may give NaN too, because the sums inside a group are formed before its
+ * scale.
  * Returns SV_OK or a negative code (nothing enqueued).
  */
 size_t spec_logits_w4_workspace_bytes(int hidden_dtype, int group, int R, int K);

@@ -29,19 +29,22 @@ def w4_product(hidden, weights, scales, zeros=None) -> np.ndarray:
 
 
 def w4_error_bound(hidden, weights, scales, zeros=None, parts: int = 1) -> np.ndarray:
-    """How far float32 sums may be from w4_product.  Inside a group the terms
-    (16 + w) x of every part and their correction (16 + z) x are added in some
-    order, at most (parts * K / G) roundings deep, then G group results are
-    added, with a few roundings each for the correction and the scale: every
-    rounding is at most 2^-24 of a partial sum, which is at most the sum of the
-    absolute terms."""
+    """How far float32 sums may be from w4_product.  The terms w x of every part
+    and z x are summed apart within at most 128 k and then over those entries of
+    K.  A term passes at most a rounding for each product of its entry, or the 24
+    of its entry's sum of x, then two for each entry (the scaled sum is added, the
+    zero points are taken out) and two of its own (the factors s z and z X); a
+    column that up to 16 wavefronts share takes 15 additions more.  Every rounding
+    is at most 2^-24 of a partial sum, which is at most the sum of the absolute
+    terms."""
     q = unpack_w4(weights).astype(np.float64)
     s = np.abs(np.asarray(scales, dtype=np.float64))
     N, G = s.shape
     K = q.shape[1]
     z = np.full((N, G), 8.0) if zeros is None else (np.asarray(zeros, dtype=np.int64) & 15).astype(np.float64)
-    w = ((16 + q.reshape(N, G, K // G) + 16 + z[:, :, None]) * s[:, :, None]).reshape(N, K)
-    return 2.0 ** -24 * (parts * (K // G) + G + 6) * (np.abs(np.asarray(hidden, dtype=np.float64)) @ w.T)
+    w = ((q.reshape(N, G, K // G) + z[:, :, None]) * s[:, :, None]).reshape(N, K)
+    entry = min(K // G, 128)
+    return 2.0 ** -24 * (max(parts * entry, 24) + 2 * (-(-K // entry)) + 17) * (np.abs(np.asarray(hidden, dtype=np.float64)) @ w.T)
 
 
 class TokenHistory:

@@ -2,14 +2,18 @@
 //
 //   out[r][n] = sum_g s[n][g] * sum_{k in g} (w[n][k] - z[n][g]) * x[r][k].
 //
-// The inner sums run on the matrix cores in bf16 with float32 accumulators,
-// and nothing in them is rounded but the accumulators: a weight enters as the
-// bf16 number 16 + w (16..31, exact: 0x4180 + 8 w, one shift and one and-or
-// for two weights), and the 16 + z that is too much is taken out per group as
-// (16 + z) * X_g with X_g = sum of the group's x, itself a product with ones.
-// The scale multiplies the group's float32 sum.  fp32 hidden states are split
-// into three bf16 parts (8 + 8 + 8 significand bits, truncated, so the parts
-// add up to the value exactly) that take three products.
+// The inner sums run on the matrix cores in bf16 with float32 accumulators: a
+// weight enters as the bf16 number w, the products w x are exact, and what the
+// zero point is too much, z times the sum of the x, is taken out in float32
+// within 256 of k.  As the fp8 (e4m3) number with its code, a nibble is w * 2^-9
+// (codes 0..7 are the subnormals, 8..15 the binade above them, in the same
+// steps), so one conversion with a scale of 2^9 gives two weights: with the
+// nibbles taken apart, seven operations for eight.  (16 + w, as 0x4180 + 8 w,
+// takes eight, and its sums are three times as large.)  fp32 hidden states are
+// split into three bf16 parts (8 + 8 + 8 significand bits, truncated, so the
+// parts add up to the value exactly) that take a product each: of 8 consecutive
+// k, an instruction cuts off what lies below the last bit of the largest
+// product, so parts of different size do not share one.
 //
 // Two forms.  Up to 16 rows (32 where K is short) the weight bytes bound: the
 // rows of x stay in LDS and the weights are streamed (w4_stream_kernel).  With
@@ -45,28 +49,25 @@ struct W4Args {
   char* xsum;
 };
 
-// The eight weights of a word as bf16 numbers 16 + w, in the order 0 4 1 5 2 6 3 7.
-// The constants are kept in registers (one operand of an instruction may be a
-// constant), so that a pair takes a shift and a v_and_or_b32.
+// The eight weights of a word as bf16 numbers, in the order 0 2 4 6 1 3 5 7.
+__device__ __forceinline__ uint32_t w4_pair(uint32_t codes) {        // of the lower two bytes
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, 512.0f, false));
+}
+__device__ __forceinline__ uint32_t w4_pair_high(uint32_t codes) {   // of the upper two
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, 512.0f, true));
+}
 __device__ __forceinline__ bf16x8 w4_expand(uint32_t w) {
-  uint32_t mask = 0x00780078u, base = 0x41804180u;
-  asm("" : "+s"(mask));
-  asm("" : "+v"(base));
-  u32x4 v;
-  v.x = ((w << 3) & mask) | base;
-  v.y = ((w >> 1) & mask) | base;
-  v.z = ((w >> 5) & mask) | base;
-  v.w = ((w >> 9) & mask) | base;
-  return __builtin_bit_cast(bf16x8, v);
+  const uint32_t even = w & 0x0F0F0F0Fu, odd = (w >> 4) & 0x0F0F0F0Fu;
+  return __builtin_bit_cast(bf16x8, u32x4{w4_pair(even), w4_pair_high(even), w4_pair(odd), w4_pair_high(odd)});
 }
 
 // Eight consecutive bf16 values in the same order.
 __device__ __forceinline__ bf16x8 w4_order(uint4 a) {
   uint4 v;
-  v.x = __builtin_amdgcn_perm(a.z, a.x, 0x05040100u);
-  v.y = __builtin_amdgcn_perm(a.z, a.x, 0x07060302u);
-  v.z = __builtin_amdgcn_perm(a.w, a.y, 0x05040100u);
-  v.w = __builtin_amdgcn_perm(a.w, a.y, 0x07060302u);
+  v.x = __builtin_amdgcn_perm(a.y, a.x, 0x05040100u);
+  v.y = __builtin_amdgcn_perm(a.w, a.z, 0x05040100u);
+  v.z = __builtin_amdgcn_perm(a.y, a.x, 0x07060302u);
+  v.w = __builtin_amdgcn_perm(a.w, a.z, 0x07060302u);
   return __builtin_bit_cast(bf16x8, v);
 }
 
@@ -95,13 +96,13 @@ template <> struct W4Hidden<float> {
     f[1] = pack(m);
     f[2] = pack(l);
   }
-  // The upper halves of eight words in the order 0 4 1 5 2 6 3 7.
+  // The upper halves of eight words in the order 0 2 4 6 1 3 5 7.
   __device__ __forceinline__ static bf16x8 pack(const uint32_t (&u)[8]) {
     uint4 v;
-    v.x = __builtin_amdgcn_perm(u[4], u[0], 0x07060302u);
-    v.y = __builtin_amdgcn_perm(u[5], u[1], 0x07060302u);
-    v.z = __builtin_amdgcn_perm(u[6], u[2], 0x07060302u);
-    v.w = __builtin_amdgcn_perm(u[7], u[3], 0x07060302u);
+    v.x = __builtin_amdgcn_perm(u[2], u[0], 0x07060302u);
+    v.y = __builtin_amdgcn_perm(u[6], u[4], 0x07060302u);
+    v.z = __builtin_amdgcn_perm(u[3], u[1], 0x07060302u);
+    v.w = __builtin_amdgcn_perm(u[7], u[5], 0x07060302u);
     return __builtin_bit_cast(bf16x8, v);
   }
 };
@@ -138,9 +139,9 @@ __device__ __forceinline__ float w4_get(const uint32_t* w, int i, const float*) 
 __device__ __forceinline__ void w4_put(uint32_t* w, int i, uint16_t v) { w[i >> 1] |= (uint32_t)v << (16 * (i & 1)); }
 __device__ __forceinline__ void w4_put(uint32_t* w, int i, float v) { w[i] = __float_as_uint(v); }
 
-// 16 + z of entry i.
-__device__ __forceinline__ float w4_shift(const W4Args& a, const uint32_t* z, int i) {
-  return 16.0f + (float)(a.z ? (z[i >> 2] >> (8 * (i & 3))) & 15u : 8u);
+// The zero point of entry i.
+__device__ __forceinline__ float w4_zero(const W4Args& a, const uint32_t* z, int i) {
+  return (float)(a.z ? (z[i >> 2] >> (8 * (i & 3))) & 15u : 8u);
 }
 
 // Sixteen weight rows of a column tile: their first row (uniform over the
@@ -163,29 +164,36 @@ __device__ __forceinline__ uint32_t w4_group(const W4Args& a, int j) {
   return (uint32_t)min(a.gb == 1 ? j : j / a.gb, a.G - 1);
 }
 
-// COUNT scales and, with ZEROS, zeros of the lane's row from entry j on.
-// TOGETHER: they lie side by side inside the row; else one by one, and entries
-// behind the row's end repeat its last.
-template <typename ST, int COUNT, bool ZEROS, bool TOGETHER, int SW, int ZW>
-__device__ __forceinline__ void w4_fetch_scales(const W4Args& a, uint32_t (&sw)[SW], uint32_t (&zw)[ZW], const W4Rows& r,
-                                                int j) {
+// COUNT scales of the lane's row from entry j on.  TOGETHER: they lie side by
+// side inside the row; else one by one, and entries behind the row's end repeat
+// its last.
+template <typename ST, int COUNT, bool TOGETHER, int SW>
+__device__ __forceinline__ void w4_fetch_scales(const W4Args& a, uint32_t (&sw)[SW], const W4Rows& r, int j) {
   const ST* s = reinterpret_cast<const ST*>(a.s) + r.first * a.G;
-  const uint8_t* z = a.z + r.first * a.G;
   const uint32_t row = r.local * (uint32_t)a.G;
   if (TOGETHER) {
     __builtin_memcpy(sw, s + (row + (uint32_t)j), COUNT * sizeof(ST));
-    if (ZEROS && a.z) __builtin_memcpy(zw, z + (row + (uint32_t)j), COUNT);
   } else {
 #pragma unroll
     for (int i = 0; i < SW; ++i) sw[i] = 0;
 #pragma unroll
     for (int i = 0; i < COUNT; ++i) w4_put(sw, i, s[row + w4_group(a, j + i)]);
-    if (ZEROS && a.z) {
+  }
+}
+
+// The same for the zero points, where there are any.
+template <int COUNT, bool TOGETHER, int ZW>
+__device__ __forceinline__ void w4_fetch_zeros(const W4Args& a, uint32_t (&zw)[ZW], const W4Rows& r, int j) {
+  if (!a.z) return;
+  const uint8_t* z = a.z + r.first * a.G;
+  const uint32_t row = r.local * (uint32_t)a.G;
+  if (TOGETHER) {
+    __builtin_memcpy(zw, z + (row + (uint32_t)j), COUNT);
+  } else {
 #pragma unroll
-      for (int i = 0; i < ZW; ++i) zw[i] = 0;
+    for (int i = 0; i < ZW; ++i) zw[i] = 0;
 #pragma unroll
-      for (int i = 0; i < COUNT; ++i) zw[i >> 2] |= (uint32_t)z[row + w4_group(a, j + i)] << (8 * (i & 3));
-    }
+    for (int i = 0; i < COUNT; ++i) zw[i >> 2] |= (uint32_t)z[row + w4_group(a, j + i)] << (8 * (i & 3));
   }
 }
 
@@ -199,8 +207,13 @@ __device__ __forceinline__ void w4_fetch(const W4Args& a, W4Ahead<ST, SUB, U>& h
 #pragma unroll
   for (int u = 0; u < U; ++u)
     h.w[u] = *reinterpret_cast<const u32x4*>(w + (row + (uint32_t)min((b + u) * 64 + quad * 16, a.K / 2 - 16)));
-  if (a.gb == 1 && (b + U) * SUB <= a.G) w4_fetch_scales<ST, NS, true, true>(a, h.s, h.z, r, b * SUB);
-  else w4_fetch_scales<ST, NS, true, false>(a, h.s, h.z, r, b * SUB);
+  if (a.gb == 1 && (b + U) * SUB <= a.G) {
+    w4_fetch_scales<ST, NS, true>(a, h.s, r, b * SUB);
+    w4_fetch_zeros<NS, true>(a, h.z, r, b * SUB);
+  } else {
+    w4_fetch_scales<ST, NS, false>(a, h.s, r, b * SUB);
+    w4_fetch_zeros<NS, false>(a, h.z, r, b * SUB);
+  }
 }
 
 // Block u of what was fetched, times the rows of x in LDS, onto tot.  x: the
@@ -228,7 +241,7 @@ __device__ __forceinline__ void w4_block(const W4Args& a, const W4Ahead<ST, SUB,
         }
       }
     }
-    const float sc = w4_get(h.s, u * SUB + sg, (const ST*)nullptr), zz = w4_shift(a, h.z, u * SUB + sg);
+    const float sc = w4_get(h.s, u * SUB + sg, (const ST*)nullptr), zz = w4_zero(a, h.z, u * SUB + sg);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       const f32x4 x4 = *reinterpret_cast<const f32x4*>(xsum + m * ms + sg * 64);
@@ -414,38 +427,30 @@ __global__ __launch_bounds__(W4S_NT) void w4_stream_kernel(W4Args a) {
 // order of the products' operands in a workspace (small: it stays in the L2);
 // the second is tiled over rows and columns.
 //
-// Here the 16 + z that a weight is too much costs more than it may: an
-// operation for each result and group.  So it is taken out by a product of its
-// own, tot = - sum_j t[n][j] * X[r][j] over the groups j, t = s * (16 + z): both
-// sides float32, split into three bf16 parts each, of whose products the six
-// above 2^-24 are formed -- 6 products for 16 groups, which have 32 to 128 of
-// their own.
+// Here a vector operation for each result and group would cost more than it
+// may, so the zero points are taken out by products of their own, in float32,
+// one for two entries (an entry: 128 k, or a group where that is less): tot -=
+// sum s * z * X.  So no sum holds more than two entries' zero points: an error of
+// 1e-7 to 3.7e-7 of the results' norm at K = 4096 and 8192, in either type, with
+// states of mean 0 or half of their spread, where a float32 product's is 2e-7 to
+// 1e-6.  (With the zero points of all of K taken out at the start, in bf16
+// parts, 1e-6 to 1e-5.)
 //
-// R=320, K=4096, N=128256, groups of 128 with zeros: 380-389 us, 870 TFLOP/s, where
+// R=320, K=4096, N=128256, groups of 128 with zeros: 381-388 us, 870 TFLOP/s, where
 // the library's bf16 product of the same shape, with 4 times the weight bytes,
 // takes 470 us (715) and its best on 8192^3 is 1198.  On the way: 16x16x32
-// products with a shift of each group, 942 us; with the product above, 566; the
-// checks out of the loop and the weights' pairs by two operations, 433; 32x32x16
-// products, two column tiles a wavefront, 390; one column tile, which two
-// workgroups of a CU then share, 380 (at N=32000 153 -> 117).  Leaving out, one
-// at a time, the fetch of the weights, the LDS reads, the expansion or the
-// scaling changed the 390 by less than 6%, and half as many workgroups on half
-// the CUs took half the time: what bounds it is shared by the CUs.  Chunks of
-// two blocks (403 us), two blocks ahead (451) and workgroups of four wavefronts
-// (413) were slower.  Groups of 32: 573 us (16 scalings for 4 products).  R=64:
-// 107 us, R=32: 83 us (3.4 TB/s, of which the first launch is 5 us): there a
-// chunk's barrier and its wait for the weights.
+// products with a shift of each group, 942 us; with zero points by products,
+// 566; the checks out of the loop, 433; 32x32x16 products, two column tiles a
+// wavefront, 390; one column tile, which two workgroups of a CU then share, 380.
+// Scales and zero points fetched for each block by itself: 443 (a lane's lie in
+// a cache line of their own, so a fetch of one byte takes as long as one of 16).
+// Chunks of two blocks, two blocks ahead and workgroups of four wavefronts were
+// slower.  Groups of 64: 410 us, of 32: 518 (16 scalings for 4 products).  R=64:
+// 98 us; R=32, N=128255: 75 us (3.8 TB/s, of which the first launch is 5 us).
 // ---------------------------------------------------------------------------
 
 // Blocks of 128 k in the workspace: an even number.
 __host__ __device__ __forceinline__ int w4_blocks(int K) { return (K + 255) / 256 * 2; }
-
-__device__ __forceinline__ void w4_split(float v, uint32_t (&o)[3]) {
-  o[0] = __float_as_uint(v) & 0xFFFF0000u;
-  const float r = v - __uint_as_float(o[0]);
-  o[1] = __float_as_uint(r) & 0xFFFF0000u;
-  o[2] = __float_as_uint(r - __uint_as_float(o[1])) & 0xFFFF0000u;
-}
 
 // The products here are v_mfma_f32_32x32x16_bf16 (lane l holds row / column
 // l % 32 of either operand at k = 8 * (l / 32) + 0..7, and rows 8 * (r / 4) +
@@ -471,15 +476,15 @@ __device__ __forceinline__ void w4_place(int u, int& t, int& h) {   // of the bl
 }
 
 // One workgroup per 32 rows and 128 k.  xop: [row tile][block][t][part] of 1 KB
-// ([h][row] 16 bytes), the rows' values; xsum: [row tile][16 entries][part] of
-// 1 KB ([h][row] 8 entries), their sums over each 128 / SUB of k.  Rows beyond
-// R, k beyond K and entries beyond the last are zeros, so that the product
-// needs no checks: what it reads of the weights there meets zeros.
+// ([h][row] 16 bytes), the rows' values; xsum: [row tile][block][SUB][row] float,
+// their sums over each 128 / SUB of k.  Rows beyond R and k beyond K are zeros, so
+// that the product needs no checks: what it reads of the weights there meets
+// zeros.
 template <typename XT, int SUB>
 __global__ __launch_bounds__(512) void w4_order_kernel(W4Args a) {
   constexpr int P = W4Hidden<XT>::PARTS;
   __shared__ float part[16][33];
-  const int nblk = w4_blocks(a.K), n16 = (nblk * SUB + 15) / 16;
+  const int nblk = w4_blocks(a.K);
   const int rt = (int)(blockIdx.x / (unsigned)nblk), b = (int)(blockIdx.x % (unsigned)nblk);
   const int r = threadIdx.x >> 4, u = threadIdx.x & 15;   // u: 8 of the block's 128 k
   const int row = rt * 32 + r, k = b * 128 + u * 8;
@@ -501,34 +506,22 @@ __global__ __launch_bounds__(512) void w4_order_kernel(W4Args a) {
   for (int p = 0; p < P; ++p) *reinterpret_cast<bf16x8*>(o + p * 1024) = f[p];
   part[u][r] = sum;
   __syncthreads();
-  // The block's entries, and behind the last block those up to the next 16.
-  const int j1 = b + 1 == nblk ? n16 * 16 : (b + 1) * SUB;
-  for (int q = threadIdx.x; q < (j1 - b * SUB) * 32; q += 512) {
-    const int sg = q >> 5, rr = q & 31, j = b * SUB + sg;
-    float t = 0.0f;
-    if (sg < SUB) {
+  if (threadIdx.x < SUB * 32) {
+    const int sg = threadIdx.x >> 5, rr = threadIdx.x & 31;
+    float x = 0.0f;
 #pragma unroll
-      for (int e = 0; e < 16 / SUB; ++e) t += part[sg * (16 / SUB) + e][rr];
-    }
-    uint32_t v[3];
-    w4_split(t, v);
-#pragma unroll
-    for (int p = 0; p < 3; ++p)
-      *reinterpret_cast<uint16_t*>(a.xsum + (((size_t)rt * n16 + (j >> 4)) * 3 + p) * 1024 + (((j >> 3) & 1) * 32 + rr) * 16 +
-                                   (j & 7) * 2) = (uint16_t)(v[p] >> 16);
+    for (int e = 0; e < 16 / SUB; ++e) x += part[sg * (16 / SUB) + e][rr];
+    reinterpret_cast<float*>(a.xsum)[(size_t)blockIdx.x * SUB * 32 + threadIdx.x] = x;
   }
 }
 
-template <int NL> struct W4Stage { u32x4 v[NL]; };
+template <int NL> struct W4Stage {
+  u32x4 v[NL];
+  float sum;
+};
 
 // What a wavefront fetches ahead of one column tile of 32: U blocks of 128 k.
-template <typename ST, int SUB, int U>
-struct W4Wide {
-  static constexpr int NS = U * SUB;
-  static constexpr int SW = (NS * (int)sizeof(ST) + 3) / 4;
-  u32x4 w[U][2];
-  uint32_t s[SW];
-};
+template <int U> struct W4Wide { u32x4 w[U][2]; };
 
 constexpr int W4_NT = 512;                 // threads per workgroup
 constexpr int W4_WAVES = W4_NT / 64;
@@ -539,218 +532,192 @@ constexpr int W4_WAVES = W4_NT / 64;
 // after it, one barrier a chunk.  Weights go from memory to registers, U
 // blocks ahead.
 template <typename XT, typename ST, int SUB, int MT, int U, int KC>
-__global__ __launch_bounds__(W4_NT) __attribute__((amdgpu_waves_per_eu(2))) void w4_tile_kernel(W4Args a) {
+__global__ __launch_bounds__(W4_NT, W4Hidden<XT>::PARTS == 1 ? 4 : 2) void w4_tile_kernel(W4Args a) {
   constexpr int P = W4Hidden<XT>::PARTS;
-  constexpr int NT = 1;   // column tiles of 32 a wavefront; two take twice the registers, half the wavefronts
   constexpr int ROW = KC * 8 * P * 1024, OPS = MT * ROW;   // bytes of a chunk: one row tile's, all
   constexpr int NL = OPS / 16 / W4_NT;                     // 16-byte loads a thread
-  static_assert(OPS % (16 * W4_NT) == 0 && KC % U == 0, "chunk does not fit the workgroup");
-  typedef W4Wide<ST, SUB, U> Wide;
+  constexpr int CE = KC * SUB < 2 ? 2 : KC * SUB;          // entries of a chunk, or of it and its neighbour
+  constexpr int SROW = CE * 32, SUMS = MT * SROW;          // their sums
+  static_assert(OPS % (16 * W4_NT) == 0 && KC % U == 0 && SUMS <= W4_NT, "chunk does not fit the workgroup");
+  typedef W4Wide<U> Wide;
+  // A lane's row is a line of its own, so a fetch of a few bytes takes as long as one of 16: scales and zero points come
+  // for several blocks at a time.
+  constexpr int SE = U * SUB > 4 ? U * SUB : 4, ZE = SUB == 1 ? 4 : 8;
   __shared__ __align__(16) char xs[2][OPS];
+  __shared__ float sums[2][W4_NT];                         // SUMS of them, and what the other threads load again
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, l32 = lane & 31, half = lane >> 5;
   const int nblk = w4_blocks(a.K);
-  const long long sets = (long long)((a.N + W4_WAVES * NT * 32 - 1) / (W4_WAVES * NT * 32)) * a.row_tiles;
+  const long long sets = (long long)((a.N + W4_WAVES * 32 - 1) / (W4_WAVES * 32)) * a.row_tiles;
   // The row tiles of a column tile run on one XCD, one after the other.
   const long long set = (long long)(blockIdx.x & 7) * a.per_xcd + (blockIdx.x >> 3);
   if (set >= sets) return;
   const int rt = (int)(set % a.row_tiles);
-  const int n0 = ((int)(set / a.row_tiles) * W4_WAVES + __builtin_amdgcn_readfirstlane(wave)) * NT * 32;
+  const int n0 = ((int)(set / a.row_tiles) * W4_WAVES + __builtin_amdgcn_readfirstlane(wave)) * 32;
   const uint32_t len = (uint32_t)nblk * 8 * P * 1024;      // operands of a row tile
+  const uint32_t slen = (uint32_t)nblk * SUB * 32;         // sums of a row tile
   const char* xop = a.xop + (size_t)rt * MT * len;
-  W4Rows rows[NT];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) rows[nt] = w4_rows(a, n0 + nt * 32, l32);
+  const float* xsum = reinterpret_cast<const float*>(a.xsum) + (size_t)rt * MT * slen + (tid % SUMS / SROW * slen + tid % SROW);
+  const W4Rows rows = w4_rows(a, n0, l32);
 
   W4Stage<NL> sr;
   // Chunk c's operands, ROW bytes of each row tile (behind the last chunk, the first again).
   auto stage_load = [&](W4Stage<NL>& g, int c) __attribute__((always_inline)) {
+    const bool more = (uint32_t)c * ROW < len;
+    const uint32_t at = more ? (uint32_t)c * ROW : 0u;
+    g.sum = xsum[more ? (uint32_t)(c * KC * SUB & ~1) * 32 : 0u];
 #pragma unroll
     for (int q = 0; q < NL; ++q) {
       const int o = (q * W4_NT + tid) * 16, m = o / ROW;
-      const uint32_t at = (uint32_t)c * ROW < len ? (uint32_t)c * ROW : 0u;
       g.v[q] = *reinterpret_cast<const u32x4*>(xop + at + ((uint32_t)m * len + o % ROW));
     }
   };
   auto stage_write = [&](const W4Stage<NL>& g, int buf) __attribute__((always_inline)) {
 #pragma unroll
     for (int q = 0; q < NL; ++q) *reinterpret_cast<u32x4*>(xs[buf] + (q * W4_NT + tid) * 16) = g.v[q];
+    sums[buf][tid] = g.sum;
   };
-  auto fetch = [&](Wide (&g)[NT], int b) __attribute__((always_inline)) {
+  auto fetch = [&](Wide& g, int b) __attribute__((always_inline)) {
+    const uint8_t* w = a.w + rows.first * (size_t)(a.K / 2);
+    const uint32_t row = rows.local * (uint32_t)(a.K / 2);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const uint8_t* w = a.w + rows[nt].first * (size_t)(a.K / 2);
-      const uint32_t row = rows[nt].local * (uint32_t)(a.K / 2);
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          g[nt].w[u][j] =
-              *reinterpret_cast<const u32x4*>(w + (row + (uint32_t)min((b + u) * 64 + j * 32 + half * 16, a.K / 2 - 16)));
-    }
-    if (Wide::NS <= 2) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        uint32_t none[1];
-        w4_fetch_scales<ST, Wide::NS, false, false>(a, g[nt].s, none, rows[nt], b * SUB);
-      }
-    } else if (a.gb == 1 && (b + U) * SUB <= a.G) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        uint32_t none[1];
-        w4_fetch_scales<ST, Wide::NS, false, true>(a, g[nt].s, none, rows[nt], b * SUB);
-      }
-    } else {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        uint32_t none[1];
-        w4_fetch_scales<ST, Wide::NS, false, false>(a, g[nt].s, none, rows[nt], b * SUB);
-      }
-    }
+      for (int j = 0; j < 2; ++j)
+        g.w[u][j] = *reinterpret_cast<const u32x4*>(w + (row + (uint32_t)min((b + u) * 64 + j * 32 + half * 16, a.K / 2 - 16)));
   };
 
-  Wide ha[NT], hb[NT];
+  // The scales and zero points in use, and the next ones, which are fetched a step after those were taken.
+  struct Some { uint32_t s[SE * sizeof(ST) / 4], z[ZE / 4]; } now, next;
+  auto fetch_scales = [&](int j) __attribute__((always_inline)) {
+    if (a.gb == 1 && j + SE <= a.G) w4_fetch_scales<ST, SE, true>(a, next.s, rows, j);
+    else w4_fetch_scales<ST, SE, false>(a, next.s, rows, j);
+  };
+  auto fetch_zeros = [&](int j) __attribute__((always_inline)) {
+    if (a.gb == 1 && j + ZE <= a.G) w4_fetch_zeros<ZE, true>(a, next.z, rows, j);
+    else w4_fetch_zeros<ZE, false>(a, next.z, rows, j);
+  };
+#pragma unroll
+  for (int i = 0; i < ZE / 4; ++i) next.z[i] = 0;
+
+  Wide ha, hb;
+  fetch_scales(0);
+  fetch_zeros(0);
   fetch(ha, 0);
   stage_load(sr, 0);
 
-  // tot = - sum_j s * (16 + z) * X.
-  f32x16 tot[MT][NT];
+  f32x16 tot[MT];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) tot[m][nt][r] = 0.0f;
-  const int n16 = (nblk * SUB + 15) / 16;
-  for (int j = 0; j < n16; ++j) {
-    // The lane's eight entries of each column; behind the last they meet zeros.
-    uint32_t sw[NT][8 * sizeof(ST) / 4], zw[NT][2];
-    if (a.gb == 1 && (j + 1) * 16 <= a.G) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) w4_fetch_scales<ST, 8, true, true>(a, sw[nt], zw[nt], rows[nt], j * 16 + half * 8);
-    } else {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) w4_fetch_scales<ST, 8, true, false>(a, sw[nt], zw[nt], rows[nt], j * 16 + half * 8);
-    }
-    bf16x8 t[NT][3];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      uint32_t w[3][4];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        uint32_t v[3];
-        w4_split(-w4_get(sw[nt], e, (const ST*)nullptr) * w4_shift(a, zw[nt], e), v);
-#pragma unroll
-        for (int p = 0; p < 3; ++p) w[p][e >> 1] = e & 1 ? w[p][e >> 1] | v[p] : v[p] >> 16;
-      }
-#pragma unroll
-      for (int p = 0; p < 3; ++p) t[nt][p] = __builtin_bit_cast(bf16x8, u32x4{w[p][0], w[p][1], w[p][2], w[p][3]});
-    }
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const char* xp = a.xsum + (((size_t)(rt * MT + m) * n16 + j) * 3) * 1024 + lane * 16;
-      bf16x8 x[3];
-#pragma unroll
-      for (int p = 0; p < 3; ++p) x[p] = *reinterpret_cast<const bf16x8*>(xp + p * 1024);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        f32x16 v = tot[m][nt];
-        v = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[0], t[nt][2], v, 0, 0, 0);
-        v = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[2], t[nt][0], v, 0, 0, 0);
-        v = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[1], t[nt][1], v, 0, 0, 0);
-        v = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[0], t[nt][1], v, 0, 0, 0);
-        v = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[1], t[nt][0], v, 0, 0, 0);
-        v = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[0], t[nt][0], v, 0, 0, 0);
-        tot[m][nt] = v;
-      }
-    }
-  }
+    for (int r = 0; r < 16; ++r) tot[m][r] = 0.0f;
 
-  // Block u of what was fetched, times its rows of x (this lane's in x), onto tot.
-  auto block = [&](const Wide (&g)[NT], int u, const char* x) __attribute__((always_inline)) {
+  // Block u of step q of the loop, times its rows of x (this lane's in x), onto tot.
+  auto block = [&](const Wide& g, int q, int u, const char* x) __attribute__((always_inline)) {
     constexpr int TG = 8 / SUB;   // products of a group
 #pragma unroll
     for (int sg = 0; sg < SUB; ++sg) {
-      f32x16 blk[MT][NT];
+      f32x16 blk[MT];
 #pragma unroll
-      for (int q = 0; q < TG; ++q) {
-        const int t = sg * TG + q, j = t >> 2;
-        bf16x8 wv[NT];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          uint32_t d;
-          if constexpr (SUB == 4) {
-            const auto pair = __builtin_amdgcn_permlane32_swap(g[nt].w[u][j][2 * q], g[nt].w[u][j][2 * q + 1], false, false);
-            d = pair[sg & 1];
-          } else {
-            d = g[nt].w[u][j][t & 3];
-          }
-          wv[nt] = w4_expand(d);
+      for (int i = 0; i < TG; ++i) {
+        const int t = sg * TG + i, j = t >> 2;
+        uint32_t d;
+        if constexpr (SUB == 4) {
+          const auto pair = __builtin_amdgcn_permlane32_swap(g.w[u][j][2 * i], g.w[u][j][2 * i + 1], false, false);
+          d = pair[sg & 1];
+        } else {
+          d = g.w[u][j][t & 3];
         }
+        const bf16x8 wv = w4_expand(d);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
 #pragma unroll
           for (int p = P - 1; p >= 0; --p) {
             const bf16x8 f = *reinterpret_cast<const bf16x8*>(x + m * ROW + (t * P + p) * 1024);
+            if (i == 0 && p == P - 1) {
+              f32x16 zero;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              if (q == 0 && p == P - 1) {
-                f32x16 zero;
-#pragma unroll
-                for (int r = 0; r < 16; ++r) zero[r] = 0.0f;
-                blk[m][nt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, wv[nt], zero, 0, 0, 0);
-              } else {
-                blk[m][nt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, wv[nt], blk[m][nt], 0, 0, 0);
-              }
+              for (int r = 0; r < 16; ++r) zero[r] = 0.0f;
+              blk[m] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, wv, zero, 0, 0, 0);
+            } else {
+              blk[m] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, wv, blk[m], 0, 0, 0);
             }
           }
         }
       }
+      const float scale = w4_get(now.s, (q * U + u) * SUB % SE + sg, (const ST*)nullptr);
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int m = 0; m < MT; ++m) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const float sc = w4_get(g[nt].s, u * SUB + sg, (const ST*)nullptr);
-#pragma unroll
-          for (int r = 0; r < 16; ++r) tot[m][nt][r] = __builtin_fmaf(sc, blk[m][nt][r], tot[m][nt][r]);
-        }
+        for (int r = 0; r < 16; ++r) tot[m][r] = __builtin_fmaf(scale, blk[m][r], tot[m][r]);
+        // Here and not in the next step, where the compiler would take them: blk's registers (164 instead of 128 with
+        // groups of 128) would cost the CU its second workgroup.
+        if (P == 1) asm volatile("" : "+v"(tot[m]));
+      }
     }
+  };
+
+  // - sum s * z * X over a pair of entries (the ones at e), one to a half of the lanes, onto tot.  In float32: of a
+  // product's 8 consecutive k, v_mfma_f32_32x32x16_bf16 cuts off what lies below the last bit of the largest, so that
+  // X and s * z as bf16 parts side by side lost up to three such bits, always downwards.
+  const uint32_t z_and = a.z ? 15u : 0u, z_or = a.z ? 0u : 8u;
+  auto zero_points = [&](int e, const float* x) __attribute__((always_inline)) {
+    const float lo = w4_get(now.s, e % SE, (const ST*)nullptr), hi = w4_get(now.s, e % SE + 1, (const ST*)nullptr);
+    const uint32_t z = now.z[e % ZE >> 2] >> (8 * (e & 3) + 8 * half);
+    const float t = (half ? hi : lo) * -(float)((z & z_and) | z_or);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) tot[m] = __builtin_amdgcn_mfma_f32_32x32x2f32(x[m * SROW], t, tot[m], 0, 0, 0);
   };
 
   stage_write(sr, 0);
   __syncthreads();
   const int nsteps = nblk / U;
-  auto step = [&](const Wide (&cur)[NT], Wide (&nxt)[NT], int s) __attribute__((always_inline)) {
+  // One step, q its place in the loop below.
+  auto step = [&](const Wide& cur, Wide& nxt, int s, int q) __attribute__((always_inline)) {
+    constexpr int NS = U * SUB;   // entries of a step
     const int b = s * U, c = b / KC;
-    fetch(nxt, min(b + U, nblk - U));
     if (b % KC == 0) stage_load(sr, c + 1);
+    if (q * NS % SE == 0) __builtin_memcpy(now.s, next.s, sizeof now.s);
+    if (q * NS % ZE == 0) __builtin_memcpy(now.z, next.z, sizeof now.z);
+    if (q * NS % ZE == NS % ZE) fetch_zeros(b * SUB - NS % ZE + ZE);
+    if (q * NS % SE == NS % SE) fetch_scales(b * SUB - NS % SE + SE);
+    fetch(nxt, min(b + U, nblk - U));
 #pragma unroll
-    for (int u = 0; u < U; ++u) block(cur, u, xs[c & 1] + (b % KC + u) * 8 * P * 1024 + lane * 16);
+    for (int u = 0; u < U; ++u) block(cur, q, u, xs[c & 1] + (b % KC + u) * 8 * P * 1024 + lane * 16);
+    if (NS >= 2) {
+#pragma unroll
+      for (int e = 0; e < NS; e += 2) zero_points(q * NS + e, sums[c & 1] + (b % KC * SUB + e) * 32 + lane);
+    } else if (q % 2) {           // one entry a step: the pair of this step and the last
+      zero_points(q - 1, sums[c & 1] + lane);
+    }
     if ((b + U) % KC == 0) {
       stage_write(sr, (c + 1) & 1);
       __syncthreads();
     }
   };
+  // Four steps or two, so that the scales and zero points of a step lie in the same place each time (Four where two
+  // do: 18.5 us instead of 18.0 at R=40, K=512, N=3001, fp32 states, groups of 32.)
   for (int s = 0;;) {
-    step(ha, hb, s);
+    step(ha, hb, s, 0);
     if (U == 2 && s + 1 == nsteps) break;
-    step(hb, ha, s + 1);
+    step(hb, ha, s + 1, 1);
+    if ((s += 2) >= nsteps) break;
+    if (U == 2 || SUB == 4) continue;
+    step(ha, hb, s, 2);
+    step(hb, ha, s + 1, 3);
     if ((s += 2) >= nsteps) break;
   }
 
+  const int n = n0 + l32;
+  if (n >= a.N) return;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int n = n0 + nt * 32 + l32;
-    if (n >= a.N) continue;
+  for (int m = 0; m < MT; ++m) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int row = (rt * MT + m) * 32 + (r >> 2) * 8 + half * 4 + (r & 3);
-        if (row >= a.R) continue;
-        const size_t o = (size_t)row * a.N + n;
-        if (a.out_bf16) store_out(reinterpret_cast<uint16_t*>(a.out) + o, tot[m][nt][r]);
-        else store_out(reinterpret_cast<float*>(a.out) + o, tot[m][nt][r]);
-      }
+    for (int r = 0; r < 16; ++r) {
+      const int row = (rt * MT + m) * 32 + (r >> 2) * 8 + half * 4 + (r & 3);
+      if (row >= a.R) continue;
+      const size_t o = (size_t)row * a.N + n;
+      if (a.out_bf16) store_out(reinterpret_cast<uint16_t*>(a.out) + o, tot[m][r]);
+      else store_out(reinterpret_cast<float*>(a.out) + o, tot[m][r]);
     }
   }
 }

@@ -81,9 +81,8 @@ static W4Plan w4_plan(int hidden_dtype, int group, int R, int K) {
   }
   const int tile = w4_tile_rows(R);
   p.row_tiles = (R + 32 * tile - 1) / (32 * tile) * tile;
-  const int blocks = w4_blocks(K);
-  p.op_bytes = (size_t)p.row_tiles * blocks * 8 * parts * 1024;
-  p.bytes = p.op_bytes + (size_t)p.row_tiles * ((blocks * sub + 15) / 16) * 3 * 1024;
+  p.op_bytes = (size_t)p.row_tiles * w4_blocks(K) * 8 * parts * 1024;
+  p.bytes = p.op_bytes + (size_t)p.row_tiles * w4_blocks(K) * sub * 128;
   return p;
 }
 
