@@ -10,18 +10,18 @@
 // their counts, in LDS.  Out of place, a row's piece goes through an LDS tile in
 // which the touched values are adjusted between the load and the store, while
 // the next row is being loaded: the logits are read and written once, in whole
-// 16-byte units.  B=256, J=8, V=152064 with 2000 tokens held: 288 us, 4.3 TB/s
+// 16-byte units.  B=256, J=8, V=152064 with 2000 tokens held: 291 us, 4.3 TB/s
 // (a plain copy by this kernel 249, by the library 233).  Writing the touched
 // values again after a row was copied took 471 us, right behind each lane's own
 // store 520: two more passes over scattered lines.  B=128, J=9, V=128256, ragged
-// rows, a mask a row, 300 biases: 119 us, of which reading the lists, hashing
+// rows, a mask a row, 300 biases: 118 us, of which reading the lists, hashing
 // the biased ids and the dependent loads before them are about half.  B=1000,
-// J=5, V=1000 in fp32: 18 us, a chain of such loads in one round of workgroups.
+// J=5, V=1000 in fp32: 19.5 us, a chain of such loads in one round of workgroups.
 // In place, only units that the mask changes are written, and then the touched
 // values (B=64, J=5, V=128255, masks alone: 24 us; mixed masks touch nearly every
 // unit, so 82 MB are read and written).  Without masks nothing is streamed: the
 // lists are walked (process_lists_kernel; 97 us for the case above that takes
-// 288 out of place).
+// 291 out of place).
 #pragma once
 
 #include "sl_common.h"
@@ -58,7 +58,7 @@ struct ProcessArgs {
   int wide;     // 1: the bases of in and out are 16-byte aligned
   int tile_off; // the tile's place in LDS
   int tile_rows; // rows that it holds
-  int hmask;    // slots of the ids' hash table - 1: at least twice as many as there are ids
+  int hmask;    // slots of the names' hash table - 1: at least one and a half times as many as there are names
 };
 
 struct Penalty {
@@ -119,9 +119,10 @@ template <typename ET> struct Raw;
 template <> struct Raw<uint16_t> { typedef uint16_t type; };
 template <> struct Raw<float> { typedef uint32_t type; };
 
-// A unit that this call does not touch again goes past the caches (stores, at
-// B=128, J=9, V=128256 with masks, penalties and biases: 126 -> 101 us; loads:
-// 125 -> 119 us on inputs that no cache holds).
+// A unit that this call does not touch again goes past the caches.  B=128, J=9,
+// V=128256 with masks, penalties and biases: stores 126 -> 101 us where the
+// inputs of the last call are still in a cache, loads 125 -> 119 us on inputs
+// that no cache holds.
 __device__ __forceinline__ uint4 load_stream(const void* p) {
   typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
   const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));

@@ -53,8 +53,16 @@ static hipError_t launch_tile(W4Args a, hipStream_t st) {
 }
 
 // The plan of a call, a function of its sizes and types alone.  The rows of x
-// stay in LDS where they fit it: at R=16, K=4096, N=152064 that takes 82 us and
-// the tiles 118, at R=32, K=2048, N=128256 43.5 and 46.5, K=1024 26 and 30.
+// stay in LDS where they fit it.  In us, LDS and tiles, at N=32000 and 128256:
+//   R=16, K=4096, groups of 32:   29.5, 43.4   80.8, 100
+//                 groups of 128:  24.0, 33.8   64.0, 70.1
+//   R=32, K=2048, groups of 32:   25.5, 26.1   62.3, 54.4
+//                 groups of 64:   20.0, 22.3   47.7, 45.5
+//                 groups of 128:  17.4, 19.3   43.4, 39.9
+//   R=32, K=1024, fp32 states:    18.3, 18.6   39.0, 39.4 (groups of 128)
+// (17 to 32 rows lose a little where N is large, most with groups of 32, whose
+// kernel keeps 44 to 84 bytes a lane in scratch; N does not enter the workspace's
+// size, so it does not decide.)
 struct W4Plan {
   int stream;        // row tiles of the streaming kernel (1, 2), 0: two launches
   int rp;            // rows staged of a tile (streaming kernel)
