@@ -52,7 +52,7 @@ extern "C" {
  *  group    values of k that share a scale: 32, 64 or a multiple of 128; K is a multiple of it.
  *  R, K, N  R >= 0 and <= SL_MAX_ROWS (R == 0 is a no-op), 32 <= K <= SL_MAX_K, 1 <= N <= SV_MAX_VOCAB.
  *           R * N and R * K below 2^34 (SV_ERR_UNSUPPORTED beyond).
- *  out      [R][N] bf16 or fp32 (out_dtype), aligned to its element; overlaps no input.
+ *  out      [R][N] bf16 or fp32 (out_dtype), aligned to its element; overlaps no input (SV_ERR_ARG).
  *
  *  workspace  device buffer of spec_logits_w4_workspace_bytes(hidden_dtype, group, R, K) bytes,
  *           256-byte aligned (NULL where that is 0, as it is for few rows); it needs no

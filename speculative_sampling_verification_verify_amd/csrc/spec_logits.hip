@@ -147,6 +147,10 @@ extern "C" int spec_logits_w4(const void* hidden, int hidden_dtype, const uint8_
     return SV_ERR_ARG;
   const W4Plan p = w4_plan(hidden_dtype, group, R, K);
   if (p.bytes && (!workspace || workspace_bytes < p.bytes || misaligned(workspace, 256))) return SV_ERR_WORKSPACE;
+  const size_t no = (size_t)R * N * size_of(out_dtype), groups = (size_t)N * (K / group);
+  if (overlap(out, no, hidden, (size_t)R * K * size_of(hidden_dtype)) || overlap(out, no, weights, (size_t)N * (K / 2)) ||
+      overlap(out, no, scales, groups * size_of(scale_dtype)) || (zeros && overlap(out, no, zeros, groups)))
+    return SV_ERR_ARG;
   W4Args a;
   memset(&a, 0, sizeof a);
   a.x = hidden;

@@ -89,6 +89,16 @@ def test_w4_largest_sizes():
         assert R * N >= 1 << 34 and w4(R=R, N=N) == SV_ERR_UNSUPPORTED, (R, N)
 
 
+def test_w4_refuses_an_output_over_an_input():
+    """The whole output is apart from every input.  (Only refused calls are made.)"""
+    at = {"x": 1 << 40, "w": 1 << 41, "s": 1 << 42, "z": 1 << 43}
+    R, K, N, group = 2, 128, 10, 64
+    size = {"x": R * K * 2, "w": N * K // 2, "s": N * (K // group) * 2, "z": N * (K // group)}
+    for k in at:
+        for out in (at[k], at[k] + size[k] // 4 * 4 - 4, at[k] - R * N * 4 + 4):
+            assert w4(**at, R=R, K=K, N=N, group=group, out=out) == SV_ERR_ARG, (k, hex(out))
+
+
 def test_history_refusals():
     def append(c=FAKE, i=FAKE, n=FAKE, S=4, V=100, slots=FAKE, t=FAKE, B=3, T=5):
         return _lib().spec_history_append(c, i, n, S, V, slots, t, B, T, 0, None)
