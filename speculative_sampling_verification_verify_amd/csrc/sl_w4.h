@@ -431,9 +431,9 @@ __global__ __launch_bounds__(W4S_NT) void w4_stream_kernel(W4Args a) {
 // may, so the zero points are taken out by products of their own, in float32,
 // one for two entries (an entry: 128 k, or a group where that is less): tot -=
 // sum s * z * X.  So no sum holds more than two entries' zero points: an error of
-// 1e-7 to 3.7e-7 of the results' norm at K = 4096 and 8192, in either type, with
-// states of mean 0 or half of their spread, where a float32 product's is 2e-7 to
-// 1e-6.  (With the zero points of all of K taken out at the start, in bf16
+// 1e-7 to 5e-7 of the results' norm at K = 4096 and 8192, in either type, with
+// states of mean 0 or half of their spread, where torch's float32 product has
+// 2e-7 to 1.5e-6.  (With the zero points of all of K taken out at the start, in bf16
 // parts, 1e-6 to 1e-5.)
 //
 // R=320, K=4096, N=128256, groups of 128 with zeros: 381-388 us, 870 TFLOP/s, where
@@ -446,7 +446,11 @@ __global__ __launch_bounds__(W4S_NT) void w4_stream_kernel(W4Args a) {
 // a cache line of their own, so a fetch of one byte takes as long as one of 16).
 // Chunks of two blocks, two blocks ahead and workgroups of four wavefronts were
 // slower.  Groups of 64: 410 us, of 32: 518 (16 scalings for 4 products).  R=64:
-// 98 us; R=32, N=128255: 75 us (3.8 TB/s, of which the first launch is 5 us).
+// 98 us; R=32, N=128255: 69-75 us (3.8-4.1 TB/s, of which the first launch is 5 us).
+// Counters at R=320: the matrix cores are busy 46% of the SIMDs' time, the vector
+// units 41% (with groups of 32, 45% and 59%), the LDS 27%, at 2.0 GHz where R=64
+// runs at 2.5: what bounds it is the SIMDs' instructions, expanding and scaling
+// among them, and the clock that this load leaves.
 // ---------------------------------------------------------------------------
 
 // Blocks of 128 k in the workspace: an even number.

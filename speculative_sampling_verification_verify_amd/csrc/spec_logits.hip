@@ -70,8 +70,9 @@ struct W4Plan {
   size_t op_bytes, bytes;
 };
 
-// Row tiles of 32 of a workgroup in the two-launch form: two above 32 rows (one
-// takes 148 us instead of 110 at R=64, K=4096, N=128256).
+// Row tiles of 32 of a workgroup in the two-launch form: two above 32 rows, which
+// expand a weight once for 64 rows (one at R=64, K=4096: 133 us instead of 106 at
+// N=128256; but 36 instead of 50 at N=32000, where two fill half of the CUs).
 static int w4_tile_rows(int R) { return R > 32 ? 2 : 1; }
 
 static W4Plan w4_plan(int hidden_dtype, int group, int R, int K) {
