@@ -316,10 +316,10 @@ class Verifier:
         if processor is not None:
             # A call that is refused leaves the logits as they were: what the verify would refuse, here first.
             _require(draft_tokens=draft_tokens, uniforms=uniforms, temperature=temperature)
-            need = spec_verify_workspace_bytes(*sizes)
-            both = SV_HINT_NO_DENSE | SV_HINT_ALL_DENSE
-            if need == 0 or need > self.workspace.numel() or self.hints & ~(both | SV_HINT_UNFILTERED) or \
-                    self.hints & both == both:
+            fits, both = True, SV_HINT_NO_DENSE | SV_HINT_ALL_DENSE
+            if sizes != (self.B, self.G, self.V, self.dtype):
+                fits = 0 < spec_verify_workspace_bytes(*sizes) <= self.workspace.numel()
+            if not fits or self.hints & ~(both | SV_HINT_UNFILTERED) or self.hints & both == both:
                 raise ValueError("the verifier's workspace or hints do not fit these logits")
             rows = None
             if gamma_len is not None:   # target rows beyond gamma_b stay as they are
@@ -446,7 +446,7 @@ class Sampler:
         _check(top_p, "top_p", torch.float32, (R,), dev)
         if processor is not None:   # after every check: a call that is refused leaves the logits as they were
             _require(uniforms=uniforms, temperature=temperature)
-            if spec_sample_workspace_bytes(R, V, dt) > self.workspace.numel():
+            if dt != self.dtype and spec_sample_workspace_bytes(R, V, dt) > self.workspace.numel():
                 raise ValueError("the sampler's workspace does not fit these logits")
             processor(logits, draft_tokens, 0 if draft_tokens is None else draft_tokens.shape[1], mask_rows,
                       stream=stream)
