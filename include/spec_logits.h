@@ -4,16 +4,19 @@
  *
  *   spec_logits_w4        logits from hidden states and a head of 4-bit weights
  *                         with group scales
+ *   spec_logits_f8        the same from a head of 8-bit floating-point weights with a
+ *                         scale for each block of 128, whose quantiser is
+ *   spec_quantize_f8      (for a head's weights and for hidden states)
  *   spec_process_logits   penalties for repeated tokens, biases and grammar
  *                         masks on logits, position by position of a draft
  *   spec_history_append,  the state of the penalties: which tokens a sequence
  *   spec_history_reset    holds, and how often
  *
  * A round of speculative decoding calls them in this order: the drafter's
- * hidden state -> spec_logits_w4 -> spec_process_logits -> spec_sample, once
- * per draft; the target's hidden states -> spec_logits_w4 ->
- * spec_process_logits -> spec_verify -> spec_history_append of its output
- * tokens.
+ * hidden state -> spec_logits_w4 or spec_logits_f8 -> spec_process_logits ->
+ * spec_sample, once per draft; the target's hidden states -> spec_logits_w4 or
+ * spec_logits_f8 -> spec_process_logits -> spec_verify -> spec_history_append of
+ * its output tokens.
  *
  * Conventions are those of spec_verify.h: device pointers are the caller's,
  * dense and row-major; work is enqueued on `stream` (a hipStream_t of the
@@ -35,7 +38,7 @@ extern "C" {
 #endif
 
 /* Limits (checked synchronously). */
-#define SL_MAX_K 65536         /* contraction length of spec_logits_w4           */
+#define SL_MAX_K 65536         /* contraction length of the products             */
 #define SL_MAX_ROWS (1 << 20)  /* rows of one call                               */
 #define SL_MAX_DRAFT 64        /* draft tokens per sequence                      */
 #define SL_MAX_BIAS 1024       /* bias entries per sequence                      */
@@ -70,6 +73,58 @@ extern "C" {
 size_t spec_logits_w4_workspace_bytes(int hidden_dtype, int group, int R, int K);
 int spec_logits_w4(const void* hidden, int hidden_dtype, const uint8_t* weights, const void* scales, int scale_dtype,
                    const uint8_t* zeros, int group, int R, int K, int N, void* out, int out_dtype, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
+/*
+ * 8-bit floating-point codes (e4m3: 4 exponent and 3 fraction bits, largest value 448, no
+ * infinities) of x, with a scale for each block of SL_F8_BLOCK values along k:
+ *
+ *   scale = max(max |x| of the block / 448, 2^-126),  code = e4m3(x / scale)
+ *
+ * in float32, the quotient rounded to float32 and then to nearest even.
+ *
+ *  x        [R][K] bf16 or fp32 (x_dtype), aligned to its element (16-byte alignment and K a
+ *           multiple of 8 take the wide path).
+ *  rows     rows that share a scale: 1 (hidden states) or SL_F8_BLOCK (a head's weights).
+ *  R, K     0 <= R <= SL_MAX_ROWS (R == 0 is a no-op), 1 <= K <= SL_MAX_K, R * K below 2^34.
+ *  codes    [R][K] bytes.
+ *  scales   [ceil(R / rows)][ceil(K / 128)] float.  The three arrays do not overlap (SV_ERR_ARG).
+ *
+ * A NaN or an infinity of x becomes the code NaN; the scale is that of the block's largest
+ * other value, or infinite with an infinity.
+ */
+#define SL_F8_BLOCK 128
+int spec_quantize_f8(const void* x, int x_dtype, int rows, int R, int K, uint8_t* codes, float* scales, void* stream);
+
+/*
+ * out[r][n] = round( sum_b hs[r][b] * scales[n / 128][b] * sum_{k in block b} h[r][k] * weights[n][k] ),
+ *
+ * b the blocks of SL_F8_BLOCK along k (the last may be shorter), h and hs the codes and scales
+ * of the hidden states.
+ *
+ *  hidden   [R][K] bf16 or fp32 (hidden_dtype), quantised in the call as by spec_quantize_f8 with
+ *           rows = 1, or with hidden_dtype SL_F8 codes; 16-byte aligned.
+ *  hidden_scales  [R][ceil(K / 128)] float with SL_F8, else NULL.
+ *  weights  [N][K] codes, 16-byte aligned.
+ *  scales   [ceil(N / 128)][ceil(K / 128)] float.
+ *  R, K, N  R >= 0 and <= SL_MAX_ROWS (R == 0 is a no-op), K a multiple of 16, 16 <= K <= SL_MAX_K,
+ *           1 <= N <= SV_MAX_VOCAB.  R * N and R * K below 2^34 (SV_ERR_UNSUPPORTED beyond).
+ *  out      [R][N] bf16 or fp32 (out_dtype), aligned to its element; overlaps no input (SV_ERR_ARG).
+ *  workspace  as for spec_logits_w4, of spec_logits_f8_workspace_bytes(out_dtype, R, K)
+ *           bytes.
+ *
+ * The products of the codes are exact; sums are held in float32 and rounded once, to nearest
+ * even, at the end.  An output in bf16 of more than 64 rows is formed by the matrix cores' 8-bit
+ * products, which cut off, in the sum of 8 consecutive k, what lies below 2^-13 of the largest of
+ * the 8 products' binade: an error well below a step of bf16 for sums of many products of like
+ * size (1e-4 of their norm).  Ask for fp32 where every bit of float32 counts.  A row of `hidden` with a NaN or an infinity gives a row of NaN, a weight
+ * code of NaN a column of NaN; others are not affected.
+ * Returns SV_OK or a negative code (nothing enqueued).
+ */
+#define SL_F8 2 /* hidden_dtype: e4m3 codes */
+size_t spec_logits_f8_workspace_bytes(int out_dtype, int R, int K);
+int spec_logits_f8(const void* hidden, int hidden_dtype, const float* hidden_scales, const uint8_t* weights,
+                   const float* scales, int R, int K, int N, void* out, int out_dtype, void* workspace,
                    size_t workspace_bytes, void* stream);
 
 /*

@@ -10,3 +10,4 @@ from .verify import (decode_row, process, inverse_cdf, verify_sequence,  # noqa:
 from . import analytics  # noqa: F401
 from . import kseq  # noqa: F401
 from . import logits  # noqa: F401
+from . import f8  # noqa: F401

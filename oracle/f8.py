@@ -1,0 +1,76 @@
+"""CPU oracle for the 8-bit floating-point quantiser and product (test
+infrastructure only), from the format's definition: e4m3 codes have a sign bit,
+4 exponent bits with bias 7 and 3 fraction bits; exponent 0 is subnormal, and
+the code with all exponent and fraction bits set is NaN."""
+import numpy as np
+
+BLOCK = 128
+TINY = np.float32(2.0 ** -126)
+
+
+def _table():
+    t = np.zeros(256)
+    for c in range(256):
+        e, f = c >> 3 & 15, c & 7
+        v = np.nan if (e, f) == (15, 7) else f * 2.0 ** -9 if e == 0 else (8 + f) * 2.0 ** (e - 10)
+        t[c] = -v if c & 128 else v
+    return t
+
+
+VALUES = _table()                 # the value of each code
+_POSITIVE = VALUES[:127]          # ascending
+
+
+def encode(v):
+    """Codes of float32 values in [-448 - 16, 448 + 16]: the nearest value, ties to the even code."""
+    v = np.asarray(v, dtype=np.float64)
+    a = np.abs(v)
+    hi = np.clip(np.searchsorted(_POSITIVE, a, side="left"), 1, 126)
+    lo = hi - 1
+    down, up = a - _POSITIVE[lo], _POSITIVE[hi] - a
+    c = np.where((down < up) | ((down == up) & (lo % 2 == 0)), lo, hi)
+    c = np.where(np.isnan(v), 127, c)
+    return (c | (np.signbit(v).astype(np.int64) << 7)).astype(np.uint8)
+
+
+def quantize(x, rows=1):
+    """(codes [R, K] uint8, scales float32) of float32 values [R, K]."""
+    x = np.asarray(x, dtype=np.float32)
+    R, K = x.shape
+    RB, KB = -(-R // rows), -(-K // BLOCK)
+    pad = np.zeros((RB * rows, KB * BLOCK), dtype=np.float32)
+    pad[:R, :K] = x
+    blocks = pad.reshape(RB, rows, KB, BLOCK)
+    s = np.maximum(np.abs(blocks).max((1, 3)) / np.float32(448), TINY).astype(np.float32)
+    q = blocks / s[:, None, :, None]
+    return encode(q).reshape(pad.shape)[:R, :K], s
+
+
+def product(codes, hs, weights, scales, codes_as_they_are=False):
+    """[R, N] in float64, and the largest error of a float32 form of it.
+
+    With codes_as_they_are, of a form on matrix cores that cut off, of each of 8
+    consecutive products, what lies below 2^-13 of the largest one's binade.  Else:
+    A block's sum of up to 128 products of 8-bit significands: every product is
+    aligned to the largest, so that what an addition drops is below 2^-23 of that
+    largest one's binade (at most 2^-22 of it), for the 128 products and the up to
+    4 partial results of the instructions.  The product of the scales, the scaled
+    block and the running sum are rounded once each (2^-24)."""
+    h, w = VALUES[codes], VALUES[weights]
+    R, K = h.shape
+    N = w.shape[0]
+    out, bound, run = np.zeros((R, N)), np.zeros((R, N)), np.zeros((R, N))
+    for b in range(-(-K // BLOCK)):
+        hb, wb = h[:, b * BLOCK:(b + 1) * BLOCK], w[:, b * BLOCK:(b + 1) * BLOCK]
+        s = hs[:, b:b + 1].astype(np.float64) * np.repeat(scales[:, b].astype(np.float64), BLOCK)[:N]
+        dot = hb @ wb.T
+        most = np.abs(hb).max(1)[:, None] * np.abs(wb).max(1)[None, :]
+        out += s * dot
+        run = run + np.abs(s * dot)
+        for g in range(0, hb.shape[1] if codes_as_they_are else 0, 8):
+            top = np.zeros((R, N))
+            for k in range(g, min(g + 8, hb.shape[1])):
+                top = np.maximum(top, np.abs(hb[:, k:k + 1] * wb[:, k]))
+            bound += s * 8 * 2.0 ** -13 * top
+        bound += s * 132 * 2.0 ** -22 * most + 2 * 2.0 ** -24 * np.abs(s * dot) + 2.0 ** -24 * run
+    return out, bound * (1 + 2.0 ** -20)

@@ -1,0 +1,508 @@
+// 8-bit floating point (e4m3, 4 exponent bits, largest finite value 448) with a
+// scale for each block of 128, and logits from a head of such weights:
+//
+//   q = e4m3(x / s),  s = max(max |x| of the block / 448, 2^-126)
+//   out[r][n] = sum_b sx[r][b] * sw[n / 128][b] * sum_{k in b} qx[r][k] * qw[n][k]
+//
+// The matrix cores multiply such codes at twice the rate of bf16, but they align
+// the products of 8 consecutive codes to the largest and cut off what lies below
+// 2^-13 of its binade (measured, the same for every instruction that takes these
+// codes); only sums of those have 24 bits.  For sums of N(0, 1) values that is an
+// error of about 1e-4 of their norm.  Expanded to bf16, which is exact, the
+// products are summed as float32.  So the codes are multiplied as they are only
+// where the result is rounded to bf16 (2^-9) and the products' rate bounds: more
+// than F8_EXACT_ROWS rows.  Everywhere else they are expanded.
+//
+// Up to 16 rows the weight bytes bound: the rows of x are quantised into LDS by
+// every workgroup and the weights are streamed (f8_stream_kernel).  With more
+// rows x is quantised into operand order first (f8_order_kernel), then tiles
+// over rows and columns (f8_tile_kernel).
+#pragma once
+
+#include "sl_common.h"
+
+namespace sl {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+constexpr float F8_TINY = 0x1p-126f;
+
+struct F8Args {
+  const void* x;
+  const float* xs;    // scales of x where x is given as codes, else null
+  const uint8_t* w;
+  const float* s;
+  void* out;
+  int R, K, N;
+  int KB;             // blocks of 128 along k
+  int out_bf16;
+  int rp;             // few rows: rows staged of a tile (a power of two, 16 unless R is smaller)
+  int row_tiles;      // more rows: workgroup tiles over the rows
+  int per_xcd;        // workgroups of one XCD
+  char* xop;          // x in operand order and its scales (workspace)
+  float* xsc;
+};
+
+// Eight consecutive values as float32.
+__device__ __forceinline__ void f8_load(const uint16_t* p, float (&v)[8]) {
+  uint32_t d[4];
+  __builtin_memcpy(d, p, 16);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(d[i] << 16);
+    v[2 * i + 1] = __uint_as_float(d[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void f8_load(const float* p, float (&v)[8]) { __builtin_memcpy(v, p, 32); }
+
+// The largest over 16 consecutive lanes, in every one of them.
+__device__ __forceinline__ float f8_max16(float v) {
+  const auto step = [](float a, int b) { return fmaxf(a, __uint_as_float((uint32_t)b)); };
+  v = step(v, __builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), 0x121, 0xF, 0xF, false));   // row_ror:1
+  v = step(v, __builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), 0x122, 0xF, 0xF, false));
+  v = step(v, __builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), 0x124, 0xF, 0xF, false));
+  return step(v, __builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), 0x128, 0xF, 0xF, false));
+}
+
+__device__ __forceinline__ float f8_amax(const float (&v)[8]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+  return m;
+}
+
+__device__ __forceinline__ float f8_scale(float amax) { return fmaxf(amax / 448.0f, F8_TINY); }
+
+// Eight codes.  The quotients are at most 448 (1 + 2^-23), which rounds to 448.
+__device__ __forceinline__ uint2 f8_codes(const float (&v)[8], float s) {
+  uint2 c;
+  int a = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] / s, v[1] / s, 0, false);
+  c.x = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[2] / s, v[3] / s, a, true);
+  a = __builtin_amdgcn_cvt_pk_fp8_f32(v[4] / s, v[5] / s, 0, false);
+  c.y = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[6] / s, v[7] / s, a, true);
+  return c;
+}
+
+// ---------------------------------------------------------------------------
+// The quantiser.
+// ---------------------------------------------------------------------------
+constexpr int FQ_NT = 256;
+
+struct F8QuantArgs {
+  const void* x;
+  uint8_t* q;
+  float* s;
+  int R, K, KB;
+  int wide;   // rows of whole 16-byte units, aligned bases
+};
+
+// Eight values from column k of a row on, zeros behind its end.
+template <typename XT, bool WIDE>
+__device__ __forceinline__ void fq_load(const XT* row, int k, int K, float (&v)[8]) {
+  if (WIDE) {
+    if (k < K) {
+      f8_load(row + k, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = k + i < K ? load_in(row + k + i) : 0.0f;
+  }
+}
+
+template <bool WIDE>
+__device__ __forceinline__ void fq_store(uint8_t* row, int k, int K, uint2 c) {
+  if (WIDE) {
+    if (k < K) *reinterpret_cast<uint2*>(row + k) = c;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (k + i < K) row[k + i] = (uint8_t)((i < 4 ? c.x : c.y) >> (8 * (i & 3)));
+  }
+}
+
+// A scale for each row and 128 of k: 16 lanes to a block.
+template <typename XT, bool WIDE>
+__global__ __launch_bounds__(FQ_NT) void quantize_rows_kernel(F8QuantArgs a) {
+  const int u = threadIdx.x & 15;
+  const long long block = (long long)blockIdx.x * (FQ_NT / 16) + (threadIdx.x >> 4);
+  if (block >= (long long)a.R * a.KB) return;   // 16 lanes together
+  const int r = (int)(block / a.KB), b = (int)(block % a.KB), k = b * 128 + u * 8;
+  float v[8];
+  fq_load<XT, WIDE>(reinterpret_cast<const XT*>(a.x) + (size_t)r * a.K, k, a.K, v);
+  const float s = f8_scale(f8_max16(f8_amax(v)));
+  fq_store<WIDE>(a.q + (size_t)r * a.K, k, a.K, f8_codes(v, s));
+  if (u == 0) a.s[block] = s;
+}
+
+// A scale for each tile of 128 x 128: one workgroup, its values in registers.
+template <typename XT, bool WIDE>
+__global__ __launch_bounds__(FQ_NT) void quantize_tiles_kernel(F8QuantArgs a) {
+  __shared__ float part[FQ_NT / 64];
+  const int u = threadIdx.x & 15, r0 = threadIdx.x >> 4;
+  const int rb = (int)(blockIdx.x / (unsigned)a.KB), b = (int)(blockIdx.x % (unsigned)a.KB), k = b * 128 + u * 8;
+  float v[8][8], m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = rb * 128 + i * 16 + r0;
+    if (r < a.R) {
+      fq_load<XT, WIDE>(reinterpret_cast<const XT*>(a.x) + (size_t)r * a.K, k, a.K, v[i]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] = 0.0f;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, f8_amax(v[i]));
+  m = f8_max16(m);
+  m = fmaxf(m, __shfl_xor(m, 16, 64));
+  m = fmaxf(m, __shfl_xor(m, 32, 64));
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < FQ_NT / 64; ++i) m = fmaxf(m, part[i]);
+  const float s = f8_scale(m);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = rb * 128 + i * 16 + r0;
+    if (r < a.R) fq_store<WIDE>(a.q + (size_t)r * a.K, k, a.K, f8_codes(v[i], s));
+  }
+  if (threadIdx.x == 0) a.s[blockIdx.x] = s;
+}
+
+// ---------------------------------------------------------------------------
+// The rows of x as codes: eight values from column k of a row, quantised over
+// the 16 lanes that hold a block (codes as they are, with their scale).
+// ---------------------------------------------------------------------------
+template <typename XT>
+__device__ __forceinline__ uint2 f8_take(const F8Args& a, int row, int b, int k, float* s) {
+  float v[8];
+  fq_load<XT, true>(reinterpret_cast<const XT*>(a.x) + (size_t)row * a.K, k, a.K, v);
+  *s = f8_scale(f8_max16(f8_amax(v)));
+  return f8_codes(v, *s);
+}
+template <>
+__device__ __forceinline__ uint2 f8_take<uint8_t>(const F8Args& a, int row, int b, int k, float* s) {
+  uint2 c = make_uint2(0, 0);
+  if (k < a.K) c = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint8_t*>(a.x) + (size_t)row * a.K + k);
+  *s = a.xs[(size_t)row * a.KB + b];
+  return c;
+}
+
+// Eight codes as bf16 values, exactly.
+__device__ __forceinline__ bf16x8 f8_expand(uint32_t lo, uint32_t hi) {
+  const auto pair = [](uint32_t c, bool high) {
+    return __builtin_bit_cast(uint32_t, high ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, true)
+                                             : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, false));
+  };
+  return __builtin_bit_cast(bf16x8, u32x4{pair(lo, false), pair(lo, true), pair(hi, false), pair(hi, true)});
+}
+
+__device__ __forceinline__ i32x8 f8_join(i32x4 a, i32x4 b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); }
+
+// ---------------------------------------------------------------------------
+// Few rows: one workgroup per CU with a run of tiles of 16 weight rows, whose
+// steps of U blocks its 16 wavefronts share out evenly.  A wavefront streams
+// its share without a barrier, one step ahead across tile borders; a tile that
+// lies in several shares is added up at the end, in the order of the
+// wavefronts.
+//
+// A block takes four v_mfma_f32_16x16x32_bf16: lane l holds 8 values of row /
+// column l % 16 of either operand, and rows 4 * (l / 16) + 0..3 of column l % 16 of
+// the result.  Which k a lane's values are is free, as long as both operands
+// agree: in product t 64 (t / 2) + 16 (l / 16) + 8 (t % 2) + 0..7, so that a load of
+// 16 bytes a lane takes 64 consecutive bytes of a row.
+// ---------------------------------------------------------------------------
+constexpr int F8S_NT = 1024;
+constexpr int F8S_WAVES = F8S_NT / 64;
+constexpr int F8S_LDS = 156 * 1024;
+constexpr int F8S_U = 2;
+
+template <int U> struct F8Ahead {
+  i32x4 w[U][2];
+  float s[U];
+};
+
+// LDS bytes of the staged rows: values [block][t][quad][rp] 16 bytes, then scales [block][16].
+__host__ __device__ __forceinline__ long long f8_stream_lds(int KB, int rp) { return (long long)KB * (256 * rp + 64); }
+
+template <typename XT>
+__global__ __launch_bounds__(F8S_NT) void f8_stream_kernel(F8Args a) {
+  constexpr int U = F8S_U;
+  __shared__ __align__(16) char smem[F8S_LDS];
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), lane = threadIdx.x & 63, l16 = lane & 15,
+            quad = lane >> 4;
+  const int KB = a.KB, rp = a.rp;
+  float* sx = reinterpret_cast<float*>(smem + KB * 256 * rp);
+  const int tiles = (a.N + 15) / 16, steps = (KB + U - 1) / U;
+  const int t0 = (int)((long long)tiles * blockIdx.x / gridDim.x), t1 = (int)((long long)tiles * (blockIdx.x + 1) / gridDim.x);
+  const long long all = (long long)(t1 - t0) * steps;
+  const int first = (int)(all * wave / F8S_WAVES), last = (int)(all * (wave + 1) / F8S_WAVES);
+  int tile = t0 + first / steps, step = first % steps;
+  int ftile = tile, fstep = step;
+
+  // What lies beyond K repeats the row's end: it meets zeros of x.
+  auto fetch = [&](F8Ahead<U>& h) {
+    const int n0 = min(ftile * 16, a.N - 1);
+    const uint8_t* w = a.w + (size_t)n0 * a.K;
+    const uint32_t row = (uint32_t)min(l16, a.N - 1 - n0) * (uint32_t)a.K;
+    const float* s = a.s + (size_t)(n0 / 128) * KB;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int b = fstep * U + u;
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        h.w[u][c] = *reinterpret_cast<const i32x4*>(w + (row + (uint32_t)min(b * 128 + c * 64 + quad * 16, a.K - 16)));
+      h.s[u] = s[min(b, KB - 1)];
+    }
+    if (++fstep == steps) {
+      fstep = 0;
+      ++ftile;
+    }
+  };
+  auto store = [&](int t, const f32x4& v) {
+    const int n = t * 16 + l16;
+    if (n >= a.N) return;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = quad * 4 + r;
+      if (row >= a.R) continue;
+      const size_t o = (size_t)row * a.N + n;
+      if (a.out_bf16) store_out(reinterpret_cast<uint16_t*>(a.out) + o, v[r]);
+      else store_out(reinterpret_cast<float*>(a.out) + o, v[r]);
+    }
+  };
+  f32x4 tot = {0, 0, 0, 0}, head = {0, 0, 0, 0};
+  bool begun = step == 0;   // the current tile's first block is this wavefront's
+  const int loff = (quad * rp + min(l16, rp - 1)) * 16;
+  auto compute = [&](const F8Ahead<U>& h) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int b = step * U + u;
+      if (b < KB) {
+        const char* x = smem + b * 256 * rp + loff;
+        f32x4 p = {0, 0, 0, 0};
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(*reinterpret_cast<const bf16x8*>(x + t * 64 * rp),
+                                                      f8_expand((uint32_t)h.w[u][t >> 1][2 * (t & 1)], (uint32_t)h.w[u][t >> 1][2 * (t & 1) + 1]), p, 0, 0, 0);
+        const f32x4 s4 = *reinterpret_cast<const f32x4*>(sx + b * 16 + quad * 4);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) tot[r] = __builtin_fmaf(h.s[u] * s4[r], p[r], tot[r]);
+      }
+    }
+    if (++step == steps) {
+      if (begun) store(tile, tot);
+      else head = tot;
+      tot = f32x4{0, 0, 0, 0};
+      step = 0;
+      ++tile;
+      begun = true;
+    }
+  };
+
+  F8Ahead<U> ha, hb;
+  const int n = last - first;
+  if (n > 0) fetch(ha);
+  for (int q = threadIdx.x; q < KB * rp * 16; q += F8S_NT) {
+    const int u = q & 15, r = q >> 4 & (rp - 1), b = (q >> 4) / rp, k = b * 128 + u * 8;
+    float s;
+    const uint2 c = f8_take<XT>(a, min(r, a.R - 1), b, k, &s);
+    const int t = (u >> 3) * 2 + (u & 1);
+    *reinterpret_cast<bf16x8*>(smem + b * 256 * rp + ((t * 4 + (u >> 1 & 3)) * rp + r) * 16) = f8_expand(c.x, c.y);
+    if (u == 0) sx[b * 16 + r] = s;
+  }
+  __syncthreads();
+  for (int i = 0; i < n; i += 2) {
+    if (i + 1 < n) fetch(hb);
+    compute(ha);
+    if (i + 1 >= n) break;
+    if (i + 2 < n) fetch(ha);
+    compute(hb);
+  }
+
+  // What is left in tot: a tile that the next wavefronts go on with, begun
+  // here, or all of this share is inside a tile.
+  if (n > 0 && step > 0 && !begun) head = tot;
+  f32x4* part = reinterpret_cast<f32x4*>(smem);   // [wave][lane], over the staged rows
+  __syncthreads();
+  part[wave * 64 + lane] = head;
+  __syncthreads();
+  if (n > 0 && step > 0 && begun) {
+    const long long end = (long long)(tile - t0 + 1) * steps;
+    for (int w = wave + 1; w < F8S_WAVES && all * w / F8S_WAVES < end; ++w) tot += part[w * 64 + lane];
+    store(tile, tot);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// More rows: x into operand order first.  A block of 128 k is two products
+// v_mfma_f32_32x32x64_f8f6f4 (F8) or eight v_mfma_f32_32x32x16_bf16: lane l holds 32
+// or 8 values of row / column l % 32 of either operand, and rows 8 * (r / 4) +
+// 4 * (l / 32) + r % 4 of column l % 32 of the result.  A lane's values of a block
+// are k = 64 (l / 32) + 0..63, in their order.
+//
+// One workgroup per 32 rows and block.  xop: [row tile][block] of 4 KB, [16 codes][lane] (F8),
+// or of 8 KB, [8 values][lane]; xsc: [row tile][block][row].  Rows beyond R and k beyond K
+// are zeros.
+// ---------------------------------------------------------------------------
+template <bool F8> __host__ __device__ constexpr int f8_block_bytes() { return F8 ? 4096 : 8192; }
+
+template <typename XT, bool F8>
+__global__ __launch_bounds__(512) void f8_order_kernel(F8Args a) {
+  const int rt = (int)(blockIdx.x / (unsigned)a.KB), b = (int)(blockIdx.x % (unsigned)a.KB);
+  const int r = threadIdx.x >> 4, u = threadIdx.x & 15;
+  const int row = rt * 32 + r;
+  uint2 c = make_uint2(0, 0);
+  float s = 0.0f;
+  if (row < a.R) c = f8_take<XT>(a, row, b, b * 128 + u * 8, &s);   // 16 lanes together
+  const int lane = (u >> 3) * 32 + r;
+  char* o = a.xop + (size_t)blockIdx.x * f8_block_bytes<F8>();
+  if (F8) *reinterpret_cast<uint2*>(o + (u >> 1 & 3) * 1024 + lane * 16 + (u & 1) * 8) = c;
+  else *reinterpret_cast<bf16x8*>(o + (u & 7) * 1024 + lane * 16) = f8_expand(c.x, c.y);
+  if (u == 0) a.xsc[(size_t)blockIdx.x * 32 + r] = s;
+}
+
+// 16 bytes a lane from memory into consecutive LDS, past the registers.
+__device__ __forceinline__ void f8_to_lds(const void* g, char* lds) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)g,
+                                   (__attribute__((address_space(3))) void*)lds, 16, 0, 0);
+}
+
+// Four wavefronts side by side along the weight rows, 64 of them each, by
+// MT * 32 rows of x.  Weight rows are the products' rows, rows of x their
+// columns: a lane's results share a row of x, hence one scale a block.  Both
+// come from memory into LDS without registers in between.  The weights of a
+// wavefront pass through its own part of LDS (loaded in whole lines, read in
+// operand order; position q of a row holds its 16-byte unit q ^ (row % 8), so
+// that the reads do not conflict): a block is read into registers, then the
+// next one is loaded in its place.  The operands of x are shared, in two
+// buffers.
+constexpr int F8T_NT = 256;
+constexpr int F8T_N = 256;   // weight rows of a workgroup
+
+template <int MT, bool F8>
+__global__ __launch_bounds__(F8T_NT, 2) void f8_tile_kernel(F8Args a) {
+  constexpr int XB = f8_block_bytes<F8>();
+  __shared__ __align__(16) char wlds[4][8192];
+  __shared__ __align__(16) char xlds[2][MT * XB];
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, l32 = lane & 31,
+            half = lane >> 5;
+  const int KB = a.KB;
+  const long long sets = (long long)((a.N + F8T_N - 1) / F8T_N) * a.row_tiles;
+  // The row tiles of a column tile run on one XCD, one after the other.
+  const long long set = (long long)(blockIdx.x & 7) * a.per_xcd + (blockIdx.x >> 3);
+  if (set >= sets) return;
+  const int rt = (int)(set % a.row_tiles) * MT;
+  const int n0 = (int)(set / a.row_tiles) * F8T_N + wave * 64;
+  const char* xop = a.xop + (size_t)rt * KB * XB;
+  const float* xsc = a.xsc + (size_t)rt * KB * 32;
+  // Behind the last weight row it is repeated.
+  const int nb = min(n0, a.N - 1);
+  const float* sw = a.s + (size_t)(nb / 128) * KB;
+  const uint8_t* wbase = a.w + (size_t)nb * a.K;
+  uint32_t wrow[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) wrow[i] = (uint32_t)min(i * 8 + (lane >> 3), a.N - 1 - nb) * (uint32_t)a.K;
+  const int wk = ((lane & 7) ^ (lane >> 3)) * 16;
+  char* wl = wlds[wave];
+
+  // What lies beyond K repeats the row's end: it meets zeros of x.
+  auto load_w = [&](int b) __attribute__((always_inline)) {
+    const uint32_t k = (uint32_t)min(b * 128 + wk, a.K - 16);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f8_to_lds(wbase + (wrow[i] + k), wl + i * 1024);
+  };
+  auto load_x = [&](int b) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < MT * XB / 4096; ++i) {
+      const int at = i * 4096 + wave * 1024, m = at / XB;   // XB is a multiple of 4096: m does not depend on the wavefront
+      f8_to_lds(xop + ((size_t)m * KB + b) * XB + (at % XB + lane * 16), xlds[b & 1] + at);
+    }
+  };
+
+  f32x16 tot[2][MT];
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) tot[c][m][r] = 0.0f;
+  f32x16 zero;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) zero[r] = 0.0f;
+
+  load_w(0);
+  load_x(0);
+  for (int b = 0; b < KB; ++b) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // this wavefront's loads into LDS have landed
+    __syncthreads();                                   // and everyone's
+    i32x4 wv[2][4];
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        wv[c][q] = *reinterpret_cast<const i32x4*>(wl + (c * 32 + l32) * 128 + (((half * 4 + q) ^ (l32 & 7)) << 4));
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the block is in registers: its place is free
+    float sx[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) sx[m] = xsc[((size_t)m * KB + b) * 32 + l32] * sw[b];
+    if (b + 1 < KB) {
+      load_w(b + 1);
+      load_x(b + 1);
+    }
+    const char* xl = xlds[b & 1] + lane * 16;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      if constexpr (F8) {
+        i32x8 xv[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          xv[j] = f8_join(*reinterpret_cast<const i32x4*>(xl + m * XB + j * 2048), *reinterpret_cast<const i32x4*>(xl + m * XB + j * 2048 + 1024));
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          f32x16 p = zero;
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            p = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f8_join(wv[c][2 * j], wv[c][2 * j + 1]), xv[j], p, 0, 0, 0, 0, 0, 0);
+#pragma unroll
+          for (int r = 0; r < 16; ++r) tot[c][m][r] = __builtin_fmaf(sx[m], p[r], tot[c][m][r]);
+        }
+      } else {
+        f32x16 p[2] = {zero, zero};
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+          const bf16x8 xv = *reinterpret_cast<const bf16x8*>(xl + m * XB + t * 1024);
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            p[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f8_expand((uint32_t)wv[c][t >> 1][2 * (t & 1)], (uint32_t)wv[c][t >> 1][2 * (t & 1) + 1]), xv, p[c], 0, 0, 0);
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) tot[c][m][r] = __builtin_fmaf(sx[m], p[c][r], tot[c][m][r]);
+      }
+    }
+  }
+
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    const int row = (rt + m) * 32 + l32;
+    if (row >= a.R) continue;
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int n = n0 + c * 32 + 8 * (r / 4) + 4 * half + r % 4;
+        if (n >= a.N) continue;
+        const size_t o = (size_t)row * a.N + n;
+        if (a.out_bf16) store_out(reinterpret_cast<uint16_t*>(a.out) + o, tot[c][m][r]);
+        else store_out(reinterpret_cast<float*>(a.out) + o, tot[c][m][r]);
+      }
+  }
+}
+
+}  // namespace sl

@@ -2,6 +2,7 @@
 // (gfx950): kernels and their C ABI (see spec_logits.h).
 
 #include "sl_w4.h"
+#include "sl_f8.h"
 #include "sl_process.h"
 
 #include <stdio.h>
@@ -174,6 +175,150 @@ extern "C" int spec_logits_w4(const void* hidden, int hidden_dtype, const uint8_
   else
     e = scale_dtype == SV_BF16 ? launch_w4<float, uint16_t>(a, group, p, st) : launch_w4<float, float>(a, group, p, st);
   return hip_status(e);
+}
+
+// ---------------------------------------------------------------------------
+// spec_quantize_f8, spec_logits_f8
+// ---------------------------------------------------------------------------
+namespace sl {
+
+static int f8_sizes(int R, int K) {
+  if (R > SL_MAX_ROWS || K > SL_MAX_K) return SV_ERR_UNSUPPORTED;
+  if (R < 0 || K < 1) return SV_ERR_ARG;
+  return (long long)R * K < W4_MOST ? SV_OK : SV_ERR_UNSUPPORTED;
+}
+
+template <typename XT, bool WIDE>
+static int launch_quantize(const F8QuantArgs& a, int rows, hipStream_t st) {
+  const long long blocks = (long long)(rows == 1 ? a.R : (a.R + 127) / 128) * a.KB;
+  const long long grid = rows == 1 ? (blocks + FQ_NT / 16 - 1) / (FQ_NT / 16) : blocks;
+  if (!fits(grid, FQ_NT)) return SV_ERR_UNSUPPORTED;
+  if (rows == 1) hipLaunchKernelGGL((quantize_rows_kernel<XT, WIDE>), dim3((unsigned)grid), dim3(FQ_NT), 0, st, a);
+  else hipLaunchKernelGGL((quantize_tiles_kernel<XT, WIDE>), dim3((unsigned)grid), dim3(FQ_NT), 0, st, a);
+  return hip_status(hipGetLastError());
+}
+
+// The plan of a product, a function of its sizes and types alone: few rows go to
+// the streaming kernel where they fit LDS.
+constexpr int F8_EXACT_ROWS = 64;
+
+struct F8Plan {
+  int stream, rp, mt, f8, row_tiles;
+  size_t op_bytes, bytes;
+};
+static F8Plan f8_plan(int out_dtype, int R, int K) {
+  F8Plan p;
+  memset(&p, 0, sizeof p);
+  const int KB = (K + 127) / 128;
+  p.rp = 16;
+  while (p.rp / 2 >= R) p.rp /= 2;
+  if (R <= 16 && f8_stream_lds(KB, p.rp) <= F8S_LDS) {
+    p.stream = 1;
+    return p;
+  }
+  p.f8 = out_dtype == SV_BF16 && R > F8_EXACT_ROWS;
+  p.mt = p.f8 ? 4 : R <= 32 ? 1 : 2;
+  p.row_tiles = (R + 32 * p.mt - 1) / (32 * p.mt);
+  p.op_bytes = (size_t)p.row_tiles * p.mt * KB * (p.f8 ? f8_block_bytes<true>() : f8_block_bytes<false>());
+  p.bytes = p.op_bytes + (size_t)p.row_tiles * p.mt * KB * 128;
+  return p;
+}
+
+template <int MT, bool F8>
+static hipError_t launch_f8_tile(F8Args a, hipStream_t st) {
+  const long long sets = (long long)((a.N + F8T_N - 1) / F8T_N) * a.row_tiles;
+  a.per_xcd = (int)((sets + 7) / 8);
+  hipLaunchKernelGGL((f8_tile_kernel<MT, F8>), dim3((unsigned)a.per_xcd * 8), dim3(F8T_NT), 0, st, a);
+  return hipGetLastError();
+}
+
+template <typename XT>
+static hipError_t launch_f8(F8Args a, const F8Plan& p, hipStream_t st) {
+  a.rp = p.rp;
+  a.row_tiles = p.row_tiles;
+  if (p.stream) {
+    const int tiles = (a.N + 15) / 16;
+    hipLaunchKernelGGL((f8_stream_kernel<XT>), dim3((unsigned)(tiles < W4S_GRID ? tiles : W4S_GRID)), dim3(F8S_NT), 0, st, a);
+    return hipGetLastError();
+  }
+  const dim3 grid((unsigned)(p.row_tiles * p.mt * a.KB));
+  if (p.f8) hipLaunchKernelGGL((f8_order_kernel<XT, true>), grid, dim3(512), 0, st, a);
+  else hipLaunchKernelGGL((f8_order_kernel<XT, false>), grid, dim3(512), 0, st, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if (p.f8) return launch_f8_tile<4, true>(a, st);
+  return p.mt == 1 ? launch_f8_tile<1, false>(a, st) : launch_f8_tile<2, false>(a, st);
+}
+
+}  // namespace sl
+
+extern "C" int spec_quantize_f8(const void* x, int x_dtype, int rows, int R, int K, uint8_t* codes, float* scales,
+                                void* stream) {
+  if (!known(x_dtype) || (rows != 1 && rows != SL_F8_BLOCK)) return SV_ERR_UNSUPPORTED;
+  const int rc = f8_sizes(R, K);
+  if (rc != SV_OK) return rc;
+  if (R == 0) return SV_OK;
+  if (!x || !codes || !scales) return SV_ERR_ARG;
+  if (misaligned(x, size_of(x_dtype)) || misaligned(scales, 4)) return SV_ERR_ARG;
+  F8QuantArgs a;
+  memset(&a, 0, sizeof a);
+  a.x = x;
+  a.q = codes;
+  a.s = scales;
+  a.R = R;
+  a.K = K;
+  a.KB = (K + 127) / 128;
+  const size_t nx = (size_t)R * K * size_of(x_dtype), ns = (size_t)((R + rows - 1) / rows) * a.KB * 4;
+  if (overlap(codes, (size_t)R * K, x, nx) || overlap(scales, ns, x, nx) || overlap(scales, ns, codes, (size_t)R * K))
+    return SV_ERR_ARG;
+  const bool wide = K % 8 == 0 && !misaligned(x, 16) && !misaligned(codes, 8);
+  hipStream_t st = (hipStream_t)stream;
+  if (x_dtype == SV_BF16) return wide ? launch_quantize<uint16_t, true>(a, rows, st) : launch_quantize<uint16_t, false>(a, rows, st);
+  return wide ? launch_quantize<float, true>(a, rows, st) : launch_quantize<float, false>(a, rows, st);
+}
+
+extern "C" size_t spec_logits_f8_workspace_bytes(int out_dtype, int R, int K) {
+  return known(out_dtype) && f8_sizes(R, K) == SV_OK && K % 16 == 0 && R > 0 ? f8_plan(out_dtype, R, K).bytes : 0;
+}
+
+extern "C" int spec_logits_f8(const void* hidden, int hidden_dtype, const float* hidden_scales, const uint8_t* weights,
+                              const float* scales, int R, int K, int N, void* out, int out_dtype, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  if ((!known(hidden_dtype) && hidden_dtype != SL_F8) || !known(out_dtype) || N > SV_MAX_VOCAB) return SV_ERR_UNSUPPORTED;
+  const int rc = f8_sizes(R, K);
+  if (rc != SV_OK) return rc;
+  if (N < 1 || K % 16 != 0) return SV_ERR_ARG;
+  if ((long long)R * N >= W4_MOST) return SV_ERR_UNSUPPORTED;
+  if ((hidden_dtype == SL_F8) != (hidden_scales != nullptr)) return SV_ERR_ARG;
+  if (R == 0) return SV_OK;
+  if (!hidden || !weights || !scales || !out) return SV_ERR_ARG;
+  if (misaligned(hidden, 16) || misaligned(weights, 16) || misaligned(scales, 4) || misaligned(hidden_scales, 4) ||
+      misaligned(out, size_of(out_dtype)))
+    return SV_ERR_ARG;
+  const F8Plan p = f8_plan(out_dtype, R, K);
+  if (p.bytes && (!workspace || workspace_bytes < p.bytes || misaligned(workspace, 256))) return SV_ERR_WORKSPACE;
+  F8Args a;
+  memset(&a, 0, sizeof a);
+  a.KB = (K + 127) / 128;
+  const size_t no = (size_t)R * N * size_of(out_dtype), nx = (size_t)R * K * (hidden_dtype == SL_F8 ? 1 : size_of(hidden_dtype));
+  if (overlap(out, no, hidden, nx) || overlap(out, no, weights, (size_t)N * K) ||
+      overlap(out, no, scales, (size_t)((N + 127) / 128) * a.KB * 4) ||
+      (hidden_scales && overlap(out, no, hidden_scales, (size_t)R * a.KB * 4)))
+    return SV_ERR_ARG;
+  a.x = hidden;
+  a.xs = hidden_scales;
+  a.w = weights;
+  a.s = scales;
+  a.out = out;
+  a.R = R;
+  a.K = K;
+  a.N = N;
+  a.out_bf16 = out_dtype == SV_BF16;
+  a.xop = (char*)workspace;
+  a.xsc = (float*)((char*)workspace + p.op_bytes);
+  hipStream_t st = (hipStream_t)stream;
+  if (hidden_dtype == SL_F8) return hip_status(launch_f8<uint8_t>(a, p, st));
+  return hip_status(hidden_dtype == SV_BF16 ? launch_f8<uint16_t>(a, p, st) : launch_f8<float>(a, p, st));
 }
 
 // ---------------------------------------------------------------------------

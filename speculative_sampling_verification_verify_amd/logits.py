@@ -2,9 +2,9 @@
 operators between a model and the verify / sampling calls of ``binding``.
 
 Argument marshalling only, as in ``binding``: the functions keep the C names.
-``History`` holds the three arrays of a token history, ``W4Head`` a 4-bit head,
-and ``LogitProcessor`` what a batch of sequences asks of its logits; the last
-two are also taken by ``binding.Verifier`` and ``binding.Sampler``.
+``History`` holds the three arrays of a token history, ``W4Head`` a 4-bit and
+``F8Head`` an 8-bit head, and ``LogitProcessor`` what a batch of sequences asks
+of its logits; the last three are also taken by ``binding.Verifier`` and ``binding.Sampler``.
 """
 from __future__ import annotations
 
@@ -28,7 +28,11 @@ SL_MAX_DRAFT = 64
 SL_MAX_BIAS = 1024
 SL_MAX_MASKS = 1 << 20
 
-EXPORTED = ("spec_logits_w4", "spec_logits_w4_workspace_bytes", "spec_history_append", "spec_history_reset", "spec_process_logits",
+SL_F8 = 2
+SL_F8_BLOCK = 128
+
+EXPORTED = ("spec_logits_w4", "spec_logits_w4_workspace_bytes", "spec_quantize_f8", "spec_logits_f8",
+            "spec_logits_f8_workspace_bytes", "spec_history_append", "spec_history_reset", "spec_process_logits",
             "spec_logits_strerror")
 
 _lib = None
@@ -52,6 +56,12 @@ def lib() -> ctypes.CDLL:
         L.spec_logits_w4_workspace_bytes.restype = sz
         L.spec_logits_w4.argtypes = [vp, i, vp, vp, i, vp, i, i, i, i, vp, i, vp, sz, vp]
         L.spec_logits_w4.restype = i
+        L.spec_quantize_f8.argtypes = [vp, i, i, i, i, vp, vp, vp]
+        L.spec_quantize_f8.restype = i
+        L.spec_logits_f8_workspace_bytes.argtypes = [i, i, i]
+        L.spec_logits_f8_workspace_bytes.restype = sz
+        L.spec_logits_f8.argtypes = [vp, i, vp, vp, vp, i, i, i, vp, i, vp, sz, vp]
+        L.spec_logits_f8.restype = i
         L.spec_history_append.argtypes = [vp, vp, vp, i, i, vp, vp, i, i, i, vp]
         L.spec_history_append.restype = i
         L.spec_history_reset.argtypes = [vp, vp, vp, i, i, vp, i, vp]
@@ -171,6 +181,105 @@ class W4Head:
 
     def __call__(self, hidden, out=None, out_dtype=None, stream=None):
         return spec_logits_w4(hidden, self.weights, self.scales, self.zeros, out, out_dtype, stream)
+
+
+# ---------------------------------------------------------------------------
+# 8-bit floating point with a scale for each block of 128.
+# ---------------------------------------------------------------------------
+_F8 = torch.float8_e4m3fn
+
+
+def _codes(t: torch.Tensor, name: str, shape, dev) -> int:
+    """The address of a tensor of e4m3 codes (float8_e4m3fn, or uint8 bit patterns)."""
+    return _arg(t, name, torch.uint8 if t.dtype is torch.uint8 else _F8, shape, dev)
+
+
+def _blocks(n: int) -> int:
+    return (n + SL_F8_BLOCK - 1) // SL_F8_BLOCK
+
+
+def spec_quantize_f8(x: torch.Tensor, rows: int = 1, codes: Optional[torch.Tensor] = None,
+                     scales: Optional[torch.Tensor] = None, stream=None):
+    """x [..., K] bf16 or fp32 as e4m3 codes [..., K] with one scale for each 128
+    values of a row (rows = 1: scales [..., ceil(K / 128)]) or for each tile of
+    128 x 128 (rows = 128, x [R, K]: scales [ceil(R / 128), ceil(K / 128)]).
+    Returns (codes, scales), new tensors where they are not given."""
+    if x.dim() < 1 or (rows != 1 and x.dim() != 2):
+        raise ValueError("x must be [..., K], or [R, K] where rows share a scale")
+    if rows not in (1, SL_F8_BLOCK):
+        raise ValueError(f"rows: 1 or {SL_F8_BLOCK}, got {rows}")
+    dev = _gpu(x, "x")
+    lead, K = x.shape[:-1], x.shape[-1]
+    R = lead.numel()
+    p = _arg(x, "x", x.dtype, x.shape, dev)
+    xt = _dtype_code(x)
+    shape = (*lead, _blocks(K)) if rows == 1 else (_blocks(R), _blocks(K))
+    if codes is None or scales is None:
+        with on_stream(stream, dev):
+            if codes is None:
+                codes = torch.empty(x.shape, dtype=_F8, device=dev)
+            if scales is None:
+                scales = torch.empty(shape, dtype=torch.float32, device=dev)
+    _call(lib().spec_quantize_f8, "spec_quantize_f8", dev, stream, p, xt, rows, R, K,
+          _codes(codes, "codes", x.shape, dev), _arg(scales, "scales", torch.float32, shape, dev))
+    return codes, scales
+
+
+def spec_logits_f8(hidden: torch.Tensor, weights: torch.Tensor, scales: torch.Tensor,
+                   hidden_scales: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                   out_dtype: Optional[torch.dtype] = None, stream=None) -> torch.Tensor:
+    """out[..., n] = sum over blocks b of 128 k of hs[..., b] * scales[n // 128, b] *
+    sum_{k in b} h[..., k] * weights[n, k].
+
+    weights [N, K] e4m3 codes (float8_e4m3fn, or uint8 bit patterns) with scales
+    [ceil(N / 128), ceil(K / 128)] float32.  hidden [..., K] bf16 or fp32, quantised
+    in the call as by spec_quantize_f8; or codes, with their hidden_scales [...,
+    ceil(K / 128)].  `out` [..., N] or a new tensor of out_dtype (hidden's; bf16
+    for codes).  The workspace of many rows is torch's, allocated on the stream
+    for the call."""
+    if hidden.dim() < 1 or weights.dim() != 2:
+        raise ValueError("hidden must be [..., K] and weights [N, K]")
+    dev = _gpu(hidden, "hidden")
+    lead, K = hidden.shape[:-1], hidden.shape[-1]
+    N, R = weights.shape[0], lead.numel()
+    if hidden_scales is None:
+        xt = _dtype_code(hidden)
+        x, xs = _arg(hidden, "hidden", hidden.dtype, hidden.shape, dev), None
+    else:
+        xt, x = SL_F8, _codes(hidden, "hidden", hidden.shape, dev)
+        xs = _arg(hidden_scales, "hidden_scales", torch.float32, (*lead, _blocks(K)), dev)
+    w = _codes(weights, "weights", (N, K), dev)
+    s = _arg(scales, "scales", torch.float32, (_blocks(N), _blocks(K)), dev)
+    if out is None:
+        with on_stream(stream, dev):
+            out = torch.empty((*lead, N), dtype=out_dtype or (torch.bfloat16 if xt == SL_F8 else hidden.dtype), device=dev)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out: expected {out_dtype}, got {out.dtype}")
+    o, ot = _arg(out, "out", out.dtype, (*lead, N), dev), _dtype_code(out)
+    need = lib().spec_logits_f8_workspace_bytes(ot, R, K)
+    ws = None
+    if need:
+        with on_stream(stream, dev):
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    _call(_lib.spec_logits_f8, "spec_logits_f8", dev, stream, x, xt, xs, w, s, R, K, N, o, ot,
+          None if ws is None else ws.data_ptr(), need)
+    return out
+
+
+class F8Head:
+    """A head of 8-bit floating-point weights: called with hidden states, gives their logits."""
+
+    def __init__(self, weights: torch.Tensor, scales: torch.Tensor):
+        self.weights, self.scales = weights, scales
+        self.N, self.K = weights.shape
+
+    @classmethod
+    def quantize(cls, weights: torch.Tensor, stream=None) -> "F8Head":
+        """The head of bf16 or fp32 weights [N, K], quantised."""
+        return cls(*spec_quantize_f8(weights, SL_F8_BLOCK, stream=stream))
+
+    def __call__(self, hidden, out=None, out_dtype=None, stream=None):
+        return spec_logits_f8(hidden, self.weights, self.scales, None, out, out_dtype, stream)
 
 
 # ---------------------------------------------------------------------------
