@@ -364,6 +364,40 @@ int spec_verify_spectr(const void* p_logits, const void* q_logits, int dtype, co
                        const float* top_p, int B, int K, int L, int V, int32_t* out_tokens,
                        int32_t* out_n, int32_t* out_node_tokens, void* stream);
 
+/*
+ * Sampling and verifying with min-p: of a row's values, only those whose probability is at least
+ * min_p times the largest one's, z >= zmax + T ln(min_p), are kept.  The order is temperature,
+ * min-p, top-k, top-p, then normalise; top-k and top-p are those of spec_verify, of what is kept
+ * so far.  Where drafts were sampled so, only a verify of distributions processed in the same way
+ * outputs the target's.
+ *
+ *  min_p        [B] or [R] float: above 0 and at most 1; 0 or less: no min-p; above 1 or NaN makes
+ *               the sequence invalid.  NULL: none has min-p.  T = 0 is argmax, whatever min_p is.
+ *  hints        0, or SV_HINT_ALL_MIN_P: the caller knows that every sequence has min_p > 0 or
+ *               T = 0, and the launch that takes the other sequences is left out.  One that breaks
+ *               the promise, or keeps more than the call's lists hold (1024 values of a row), still
+ *               gets its exact result, from a slower path.
+ *  out_prob     [R] float or NULL: the processed probability of the token drawn (NaN for an invalid
+ *               row), which a verify reports as q(x).
+ *  workspace    spec_verify_min_p_workspace_bytes(B, gamma_max, V, dtype) bytes (gamma_max = 0 and
+ *               B = R rows for spec_sample_min_p), 256-byte aligned.  It needs no preparation and
+ *               holds nothing after the call; calls that share one must be ordered.
+ * Every other argument, the outputs and the error behaviour are those of spec_verify_ex and
+ * spec_sample; base pointers need only be aligned to their element.  Probabilities, normalisers and
+ * nucleus masses are held in 64 bits.  At most 2^24 row parts of 2^11 to 2^14 values
+ * (SV_ERR_UNSUPPORTED beyond).
+ */
+#define SV_HINT_ALL_MIN_P 8
+size_t spec_verify_min_p_workspace_bytes(int B, int gamma_max, int V, int dtype);
+int spec_verify_min_p(const void* p_logits, const void* q_logits, int dtype, const int32_t* draft_tokens,
+                      const int32_t* gamma_len, const float* uniforms, const float* temperature,
+                      const int32_t* top_k, const float* top_p, const float* min_p, const float* lenience,
+                      int hints, int B, int gamma_max, int V, int32_t* out_tokens, int32_t* out_n_accepted,
+                      float* out_alpha, float* out_pq, void* workspace, size_t workspace_bytes, void* stream);
+int spec_sample_min_p(const void* logits, int dtype, const float* uniforms, const float* temperature,
+                      const int32_t* top_k, const float* top_p, const float* min_p, int hints, int R, int V,
+                      int32_t* out_tokens, float* out_prob, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Kernels of one call, for spec_verify_set_stage_events. */
 enum {
   SV_KERNEL_SELECT = 0,  /* streaming top-k / argmax select over the logit rows      */

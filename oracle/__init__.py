@@ -11,3 +11,4 @@ from . import analytics  # noqa: F401
 from . import kseq  # noqa: F401
 from . import logits  # noqa: F401
 from . import f8  # noqa: F401
+from . import minp  # noqa: F401

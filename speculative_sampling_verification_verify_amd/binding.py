@@ -26,6 +26,7 @@ SV_MAX_CANDIDATES = 64
 SV_HINT_NO_DENSE = 1
 SV_HINT_ALL_DENSE = 2
 SV_HINT_UNFILTERED = 4
+SV_HINT_ALL_MIN_P = 8
 SV_MAX_GAMMA = 64
 SV_MAX_VOCAB = 1 << 20
 
@@ -35,7 +36,7 @@ EXPORTED = ("spec_verify_workspace_bytes", "spec_verify_workspace_init", "spec_v
             "spec_verify_expected_tokens", "spec_verify_speedup", "spec_verify_operations",
             "spec_verify_optimal_gamma", "spec_verify_acceptance_length", "spec_verify_spectr",
             "spec_verify_gumbel_workspace_bytes", "spec_verify_gumbel_workspace_init", "spec_verify_gumbel_ex",
-            "spec_verify_noalloc")
+            "spec_verify_noalloc", "spec_verify_min_p_workspace_bytes", "spec_verify_min_p", "spec_sample_min_p")
 
 _lib = None
 
@@ -87,6 +88,12 @@ def lib() -> ctypes.CDLL:
         L.spec_sample_gumbel.restype = i
         L.spec_verify_spectr.argtypes = [vp, vp, i, vp, vp, vp, vp, vp, i, i, i, i, vp, vp, vp, vp]
         L.spec_verify_spectr.restype = i
+        L.spec_verify_min_p_workspace_bytes.argtypes = [i, i, i, i]
+        L.spec_verify_min_p_workspace_bytes.restype = sz
+        L.spec_verify_min_p.argtypes = [vp, vp, i, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, vp, vp, vp, vp, vp, sz, vp]
+        L.spec_verify_min_p.restype = i
+        L.spec_sample_min_p.argtypes = [vp, i, vp, vp, vp, vp, vp, i, i, i, vp, vp, vp, sz, vp]
+        L.spec_sample_min_p.restype = i
         d = ctypes.c_double
         L.spec_verify_expected_tokens.argtypes = [d, i]
         L.spec_verify_expected_tokens.restype = d
@@ -284,26 +291,45 @@ def _logits_buffer(head, hidden, buffer, shape, dtype, dev, stream):
     return out
 
 
+def spec_verify_min_p_workspace_bytes(B: int, gamma_max: int, V: int, dtype: int) -> int:
+    return int(lib().spec_verify_min_p_workspace_bytes(B, gamma_max, V, dtype))
+
+
+def _min_p_workspace(B: int, gamma_max: int, V: int, dtype: int, device) -> torch.Tensor:
+    nbytes = spec_verify_min_p_workspace_bytes(B, gamma_max, V, dtype)
+    if nbytes == 0:
+        raise ValueError("unsupported sizes")
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 class Verifier:
-    """Owns a workspace and output buffers for calls of one shape."""
+    """Owns a workspace and output buffers for calls of one shape.  With
+    min_p=True, also the workspace of calls with min_p (spec_verify_min_p);
+    the hint SV_HINT_ALL_MIN_P concerns those calls alone, the other hints the
+    calls without."""
 
     def __init__(self, B: int, gamma_max: int, V: int, dtype: int = SV_BF16, device="cuda", with_pq=True,
-                 hints: int = 0):
-        self.B, self.G, self.V, self.dtype, self.hints = B, gamma_max, V, dtype, hints
+                 hints: int = 0, min_p: bool = False):
+        self.B, self.G, self.V, self.dtype = B, gamma_max, V, dtype
+        self.hints, self.min_p_hints = hints & ~SV_HINT_ALL_MIN_P, hints & SV_HINT_ALL_MIN_P
         dev = torch.device(device)
         nbytes = spec_verify_workspace_bytes(B, gamma_max, V, dtype)
         if nbytes == 0:
             raise ValueError("unsupported sizes")
         self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         spec_verify_workspace_init(self.workspace, B, gamma_max, V, dtype)
+        self.min_p_workspace = _min_p_workspace(B, gamma_max, V, dtype, dev) if min_p else None
         self.tokens = torch.empty((B, gamma_max + 1), dtype=torch.int32, device=dev)
         self.n_accepted = torch.empty((B,), dtype=torch.int32, device=dev)
         self.alpha = torch.empty((B, gamma_max), dtype=torch.float32, device=dev)
         self.pq = torch.empty((B, gamma_max, 2), dtype=torch.float32, device=dev) if with_pq else None
 
     def __call__(self, p_logits, q_logits, draft_tokens, uniforms, temperature, top_k=None, top_p=None,
-                 gamma_len=None, stream=None, lenience=None, processor=None, mask_rows=None):
-        """With `processor` (logits.LogitProcessor), p_logits are adjusted in
+                 gamma_len=None, stream=None, lenience=None, processor=None, mask_rows=None, min_p=None):
+        """With `min_p` ([B] float32; needs Verifier(min_p=True)), the distributions
+        are cut by it before top-k and top-p, as a Sampler given it does.
+
+        With `processor` (logits.LogitProcessor), p_logits are adjusted in
         place before the verify, position by position of the drafts; mask_rows
         [B, gamma_max+1] picks its grammar masks (needed where it has any).  q_logits must be what the
         drafts were sampled from: a Sampler given the same processor leaves
@@ -313,13 +339,21 @@ class Verifier:
         args = (p_logits, q_logits, draft_tokens, gamma_len, uniforms, temperature, top_k, top_p,
                 self.tokens, self.n_accepted, self.alpha, self.pq)
         sizes = _check_verify(*args, lenience)
+        B, G, V, dt = sizes
+        if min_p is not None:
+            _check(min_p, "min_p", torch.float32, (B,), p_logits.device)
+            if self.min_p_workspace is None:
+                raise ValueError("min_p needs a Verifier(min_p=True)")
         if processor is not None:
             # A call that is refused leaves the logits as they were: what the verify would refuse, here first.
             _require(draft_tokens=draft_tokens, uniforms=uniforms, temperature=temperature)
             fits, both = True, SV_HINT_NO_DENSE | SV_HINT_ALL_DENSE
             if sizes != (self.B, self.G, self.V, self.dtype):
-                fits = 0 < spec_verify_workspace_bytes(*sizes) <= self.workspace.numel()
-            if not fits or self.hints & ~(both | SV_HINT_UNFILTERED) or self.hints & both == both:
+                if min_p is not None:
+                    fits = 0 < spec_verify_min_p_workspace_bytes(*sizes) <= self.min_p_workspace.numel()
+                else:
+                    fits = 0 < spec_verify_workspace_bytes(*sizes) <= self.workspace.numel()
+            if not fits or min_p is None and (self.hints & ~(both | SV_HINT_UNFILTERED) or self.hints & both == both):
                 raise ValueError("the verifier's workspace or hints do not fit these logits")
             rows = None
             if gamma_len is not None:   # target rows beyond gamma_b stay as they are
@@ -327,12 +361,22 @@ class Verifier:
                 with on_stream(stream, p_logits.device):
                     rows = gamma_len + 1
             processor(p_logits, draft_tokens, 0, mask_rows, rows, stream=stream)
-        _enqueue_verify(*args, self.workspace, stream, lenience, self.hints, *sizes)
+        if min_p is None:
+            _enqueue_verify(*args, self.workspace, stream, lenience, self.hints, *sizes)
+            return self.tokens, self.n_accepted, self.alpha, self.pq
+        rc = lib().spec_verify_min_p(_ptr(p_logits), _ptr(q_logits), dt, _ptr(draft_tokens), _ptr(gamma_len), _ptr(uniforms),
+                                     _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(lenience),
+                                     self.min_p_hints, B, G, V, _ptr(self.tokens), _ptr(self.n_accepted), _ptr(self.alpha),
+                                     _ptr(self.pq), _ptr(self.min_p_workspace), self.min_p_workspace.numel(),
+                                     _stream_handle(stream))
+        if rc != SV_OK:
+            raise SpecVerifyError(rc, "spec_verify_min_p")
         return self.tokens, self.n_accepted, self.alpha, self.pq
 
     def from_hidden(self, hidden, head, q_logits, draft_tokens, uniforms, temperature, stream=None, **kw):
         """The same from the target's hidden states [B, gamma_max+1, K] and its
-        4-bit head (logits.W4Head); the logits stay in self.p_logits."""
+        4-bit or 8-bit head (logits.W4Head, logits.F8Head); the logits stay in
+        self.p_logits."""
         self.p_logits = _logits_buffer(head, hidden, getattr(self, "p_logits", None), (self.B, self.G + 1, self.V),
                                        self.dtype, self.tokens.device, stream)
         return self(self.p_logits, q_logits, draft_tokens, uniforms, temperature, stream=stream, **kw)
@@ -411,10 +455,12 @@ def spec_sample_workspace_bytes(R: int, V: int, dtype: int) -> int:
 
 class Sampler:
     """One token per row from the processed distribution, by inverse CDF at a
-    uniform (spec_sample); owns the workspace and the output for one shape."""
+    uniform (spec_sample); owns the workspace and the output for one shape.
+    With min_p=True, also those of calls with min_p (spec_sample_min_p, whose
+    hints these are), which leave the drawn tokens' probabilities in self.prob."""
 
-    def __init__(self, R: int, V: int, dtype: int = SV_BF16, device="cuda"):
-        self.R, self.V, self.dtype = R, V, dtype
+    def __init__(self, R: int, V: int, dtype: int = SV_BF16, device="cuda", hints: int = 0, min_p: bool = False):
+        self.R, self.V, self.dtype, self.hints = R, V, dtype, hints
         dev = torch.device(device)
         nbytes = spec_sample_workspace_bytes(R, V, dtype)
         if nbytes == 0:
@@ -424,11 +470,16 @@ class Sampler:
                                               _stream_handle(None))
         if rc != SV_OK:
             raise SpecVerifyError(rc, "spec_sample_workspace_init")
+        self.min_p_workspace = _min_p_workspace(R, 0, V, dtype, dev) if min_p else None
         self.tokens = torch.empty((R,), dtype=torch.int32, device=dev)
+        self.prob = torch.empty((R,), dtype=torch.float32, device=dev) if min_p else None
 
     def __call__(self, logits, uniforms, temperature, top_k=None, top_p=None, stream=None, processor=None,
-                 draft_tokens=None, mask_rows=None):
-        """With `processor` (logits.LogitProcessor), the logits are adjusted in
+                 draft_tokens=None, mask_rows=None, min_p=None):
+        """With `min_p` ([R] float32; needs Sampler(min_p=True)), the distribution is
+        cut by it before top-k and top-p.
+
+        With `processor` (logits.LogitProcessor), the logits are adjusted in
         place before the draw: they follow the history and draft_tokens [R, n],
         the sequence's drafts so far; mask_rows [R] picks its grammar masks
         (needed where it has any)."""
@@ -444,12 +495,27 @@ class Sampler:
         _check(temperature, "temperature", torch.float32, (R,), dev)
         _check(top_k, "top_k", torch.int32, (R,), dev)
         _check(top_p, "top_p", torch.float32, (R,), dev)
+        if min_p is not None:
+            _check(min_p, "min_p", torch.float32, (R,), dev)
+            if self.min_p_workspace is None:
+                raise ValueError("min_p needs a Sampler(min_p=True)")
+            if self.hints & ~SV_HINT_ALL_MIN_P:
+                raise ValueError("the sampler takes no other hint than SV_HINT_ALL_MIN_P")
         if processor is not None:   # after every check: a call that is refused leaves the logits as they were
             _require(uniforms=uniforms, temperature=temperature)
-            if dt != self.dtype and spec_sample_workspace_bytes(R, V, dt) > self.workspace.numel():
+            need, ws = (spec_sample_workspace_bytes, self.workspace) if min_p is None else \
+                (lambda *n: spec_verify_min_p_workspace_bytes(n[0], 0, *n[1:]), self.min_p_workspace)
+            if dt != self.dtype and need(R, V, dt) > ws.numel():
                 raise ValueError("the sampler's workspace does not fit these logits")
             processor(logits, draft_tokens, 0 if draft_tokens is None else draft_tokens.shape[1], mask_rows,
                       stream=stream)
+        if min_p is not None:
+            rc = lib().spec_sample_min_p(_ptr(logits), dt, _ptr(uniforms), _ptr(temperature), _ptr(top_k), _ptr(top_p),
+                                         _ptr(min_p), self.hints, R, V, _ptr(self.tokens), _ptr(self.prob),
+                                         _ptr(self.min_p_workspace), self.min_p_workspace.numel(), _stream_handle(stream))
+            if rc != SV_OK:
+                raise SpecVerifyError(rc, "spec_sample_min_p")
+            return self.tokens
         rc = lib().spec_sample(_ptr(logits), dt, _ptr(uniforms), _ptr(temperature), _ptr(top_k), _ptr(top_p), R, V,
                                _ptr(self.tokens), _ptr(self.workspace),
                                self.workspace.numel() * self.workspace.element_size(), _stream_handle(stream))
@@ -458,8 +524,8 @@ class Sampler:
         return self.tokens
 
     def from_hidden(self, hidden, head, uniforms, temperature, out=None, stream=None, **kw):
-        """The same from the drafter's hidden states [R, K] and its 4-bit head
-        (logits.W4Head).  The logits, which the verify needs as its q rows, go to
+        """The same from the drafter's hidden states [R, K] and its 4-bit or 8-bit
+        head (logits.W4Head, logits.F8Head).  The logits, which the verify needs as its q rows, go to
         `out` [R, V] (None: a buffer of the sampler's, overwritten by the next
         such call) and stay reachable as self.logits."""
         if out is None:

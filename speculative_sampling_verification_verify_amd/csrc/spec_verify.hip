@@ -41,6 +41,7 @@
 #include "sv_finish.h"
 #include "sv_gumbel.h"
 #include "sv_kseq.h"
+#include "sv_minp.h"
 
 #include <math.h>
 #include <stdio.h>
@@ -950,4 +951,153 @@ extern "C" double spec_verify_acceptance_length(const double* alpha, int gamma) 
     tau += run;
   }
   return tau;
+}
+
+// ---------------------------------------------------------------------------
+// min-p
+// ---------------------------------------------------------------------------
+namespace sv {
+
+struct MinpPlan {
+  int vpl;    // 16-byte units a thread of the cut kernel
+  int NP, PL;
+  size_t flags_off, pos_off, redo_off, max_off, count_off, list_off, total;
+};
+
+// Row parts of 32 KB; of 8 KB in calls of few, which then spread over the chip.
+constexpr long long MP_FEW = 1024;
+
+static MinpPlan minp_plan(int B, int G, int V, int dtype) {
+  MinpPlan p;
+  const int vec = dtype == SV_BF16 ? 8 : 4;
+  const size_t rows = (size_t)B * (2 * G + 1), np = (size_t)B * (G + 1);
+  const auto parts = [&](int vpl) { return (V + MP_NT * vpl * vec - 1) / (MP_NT * vpl * vec); };
+  p.vpl = (long long)rows * parts(8) < MP_FEW ? 2 : 8;
+  p.NP = parts(p.vpl);
+  p.PL = MP_NT * p.vpl * vec;
+  const size_t units = rows * p.NP;
+  const auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  p.flags_off = 256;
+  p.pos_off = up(p.flags_off + (size_t)B * 4);
+  p.redo_off = up(p.pos_off + np * sizeof(PosRec));
+  p.max_off = up(p.redo_off + np * 4);
+  p.count_off = up(p.max_off + units * 4);
+  p.list_off = up(p.count_off + units * 4);
+  p.total = p.list_off + units * MP_PART_CAP * (dtype == SV_BF16 ? sizeof(MinpEntry<uint16_t>::type) : sizeof(MinpEntry<float>::type));
+  return p;
+}
+
+static size_t minp_bytes(int B, int G, int V, int dtype) {
+  if (B < 0 || G < 0 || G > SV_MAX_GAMMA || V < 1 || V > SV_MAX_VOCAB || (dtype != SV_BF16 && dtype != SV_FP32)) return 0;
+  return B == 0 ? 256 : minp_plan(B, G, V, dtype).total;
+}
+
+template <typename ET>
+static hipError_t launch_minp(const MinpArgs& ma, const MinpPlan& p, int hints, hipStream_t st) {
+  const Args& a = ma.a;
+  const dim3 units((unsigned)((long long)a.B * a.RS * a.NP)), positions((unsigned)((long long)a.B * (a.G + 1)));
+  hipError_t e;
+  if (p.vpl == 8) hipLaunchKernelGGL((minp_cut_kernel<ET, 8>), units, dim3(MP_NT), 0, st, ma);
+  else hipLaunchKernelGGL((minp_cut_kernel<ET, 2>), units, dim3(MP_NT), 0, st, ma);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  if (hints & SV_HINT_ALL_MIN_P) {
+    hipLaunchKernelGGL((minp_position_kernel<ET, true>), positions, dim3(MP_NT), 0, st, ma);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  } else {
+    hipLaunchKernelGGL((minp_position_kernel<ET, false>), positions, dim3(MP_NT), 0, st, ma);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    hipLaunchKernelGGL((minp_row_kernel<ET>), dim3(MP_ROW_GRID), dim3(MP_ROW_NT), 0, st, ma);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  if (a.sampler) return hipSuccess;
+  constexpr int per = MP_FIN_NT / 64;
+  hipLaunchKernelGGL(minp_finish_kernel, dim3((unsigned)((a.B + per - 1) / per)), dim3(MP_FIN_NT), 0, st, ma);
+  return hipGetLastError();
+}
+
+static int run_minp(const void* p_logits, const void* q_logits, int dtype, const int32_t* draft_tokens,
+                    const int32_t* gamma_len, const float* uniforms, const float* temperature, const int32_t* top_k,
+                    const float* top_p, const float* min_p, const float* lenience, int hints, int B, int G, int V,
+                    int32_t* out_tokens, int32_t* out_n, float* out_alpha, float* out_pq, float* out_prob,
+                    void* workspace, size_t workspace_bytes, void* stream, int sampler) {
+  if (hints & ~SV_HINT_ALL_MIN_P) return SV_ERR_ARG;
+  const int rc = check_verify_args(p_logits, q_logits, dtype, draft_tokens, uniforms, temperature, 0, out_tokens, out_n,
+                                   out_alpha, sampler);
+  if (rc != SV_OK) return rc;
+  const MinpPlan p = minp_plan(B, G, V, dtype);
+  if (!workspace || workspace_bytes < p.total || ((uintptr_t)workspace % 256)) return SV_ERR_WORKSPACE;
+  // A launch holds fewer than 2^32 threads.
+  if ((long long)B * (2 * G + 1) * p.NP * MP_NT >= (1LL << 32)) return SV_ERR_UNSUPPORTED;
+  char* ws = (char*)workspace;
+  MinpArgs ma;
+  memset(&ma, 0, sizeof ma);
+  Args& a = ma.a;
+  a.p = p_logits;
+  a.q = q_logits;
+  a.draft = draft_tokens;
+  a.gamma_len = gamma_len;
+  a.u = uniforms;
+  a.temp = temperature;
+  a.topk = top_k;
+  a.topp = top_p;
+  a.lenience = lenience;
+  a.sampler = sampler;
+  a.B = B;
+  a.G = G;
+  a.V = V;
+  a.RS = 2 * G + 1;
+  a.NP = p.NP;
+  a.PL = p.PL;
+  a.out_tokens = out_tokens;
+  a.out_n = out_n;
+  a.out_alpha = out_alpha;
+  a.out_pq = out_pq;
+  a.dense_count = reinterpret_cast<uint32_t*>(ws);
+  a.seq_flags = reinterpret_cast<uint32_t*>(ws + p.flags_off);
+  a.pos = reinterpret_cast<PosRec*>(ws + p.pos_off);
+  a.dense_list = reinterpret_cast<int32_t*>(ws + p.redo_off);
+  ma.min_p = min_p;
+  ma.part_max = reinterpret_cast<uint32_t*>(ws + p.max_off);
+  ma.part_count = reinterpret_cast<uint32_t*>(ws + p.count_off);
+  ma.part_list = ws + p.list_off;
+  ma.out_prob = out_prob;
+  hipStream_t st = (hipStream_t)stream;
+  const hipError_t e = dtype == SV_BF16 ? launch_minp<uint16_t>(ma, p, hints, st) : launch_minp<float>(ma, p, hints, st);
+  if (e != hipSuccess) {
+    snprintf(g_errbuf, sizeof g_errbuf, "HIP error: %s", hipGetErrorString(e));
+    return SV_ERR_HIP;
+  }
+  return SV_OK;
+}
+
+}  // namespace sv
+
+extern "C" size_t spec_verify_min_p_workspace_bytes(int B, int gamma_max, int V, int dtype) {
+  return minp_bytes(B, gamma_max, V, dtype);
+}
+
+extern "C" int spec_verify_min_p(const void* p_logits, const void* q_logits, int dtype, const int32_t* draft_tokens,
+                                 const int32_t* gamma_len, const float* uniforms, const float* temperature,
+                                 const int32_t* top_k, const float* top_p, const float* min_p, const float* lenience,
+                                 int hints, int B, int gamma_max, int V, int32_t* out_tokens, int32_t* out_n_accepted,
+                                 float* out_alpha, float* out_pq, void* workspace, size_t workspace_bytes, void* stream) {
+  if (dtype != SV_BF16 && dtype != SV_FP32) return SV_ERR_UNSUPPORTED;
+  if (gamma_max > SV_MAX_GAMMA || V > SV_MAX_VOCAB) return SV_ERR_UNSUPPORTED;
+  if (!sizes_ok(B, gamma_max, V)) return SV_ERR_ARG;
+  if (B == 0) return SV_OK;
+  return run_minp(p_logits, q_logits, dtype, draft_tokens, gamma_len, uniforms, temperature, top_k, top_p, min_p, lenience,
+                  hints, B, gamma_max, V, out_tokens, out_n_accepted, out_alpha, out_pq, nullptr, workspace,
+                  workspace_bytes, stream, 0);
+}
+
+extern "C" int spec_sample_min_p(const void* logits, int dtype, const float* uniforms, const float* temperature,
+                                 const int32_t* top_k, const float* top_p, const float* min_p, int hints, int R, int V,
+                                 int32_t* out_tokens, float* out_prob, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+  if (dtype != SV_BF16 && dtype != SV_FP32) return SV_ERR_UNSUPPORTED;
+  if (V > SV_MAX_VOCAB) return SV_ERR_UNSUPPORTED;
+  if (R < 0 || V < 1) return SV_ERR_ARG;
+  if (R == 0) return SV_OK;
+  return run_minp(logits, nullptr, dtype, nullptr, nullptr, uniforms, temperature, top_k, top_p, min_p, nullptr, hints, R,
+                  0, V, out_tokens, nullptr, nullptr, nullptr, out_prob, workspace, workspace_bytes, stream, 1);
 }

@@ -1,0 +1,801 @@
+// Sampling and verifying with min-p, temperature, top-k and top-p.
+//
+// min-p keeps p(v) >= min_p * max p, which is z(v) >= zmax + T ln(min_p): a bound
+// on the value, as top-k and top-p are.  It comes first (temperature, min-p,
+// top-k, top-p), so that everything after it works on the few values that it
+// keeps, and a row's processed distribution is its values >= thr, with one sum.
+//
+//   minp_cut_kernel       one workgroup per (logit row, row part): the part is
+//                         read once, into registers; its maximum and the
+//                         values that may be kept go to the workspace
+//   minp_position_kernel  one workgroup per (sequence, position): the kept
+//                         values of the position's target and draft row,
+//                         gathered in LDS, give p(x), q(x), the overlap and the
+//                         draw as if the first rejection were there
+//   minp_row_kernel       the same from the logits, for rows without min-p and
+//                         rows that keep more than the lists hold
+//   minp_finish_kernel    one wavefront per sequence: acceptance and outputs
+//
+// Probabilities, normalisers and nucleus masses are held in 64 bits (the masses
+// as fixed-point numbers, whose sum does not depend on its order), so that a
+// decision differs from the exact one only within about 1e-12 of its border.
+#pragma once
+
+#include "sv_common.h"
+#include "sv_finish.h"
+
+namespace sv {
+
+constexpr int MP_NT = 256;        // threads of a cut or position workgroup
+constexpr int MP_WAVES = MP_NT / 64;
+constexpr int MP_PART_CAP = 512;  // list entries of a row part
+constexpr int MP_CAP = 1024;      // kept values of a row that the position kernel holds
+constexpr int MP_ROW_NT = 1024;   // threads of a row workgroup
+constexpr int MP_ROW_GRID = 512;
+constexpr int MP_FIX = 42;        // fraction bits of a mass: at most 2^20 masses of at most 1
+
+// Flags in a part's count.
+constexpr uint32_t MP_BAD = 1u << 30;    // NaN or +inf
+constexpr uint32_t MP_OVER = 1u << 31;   // more than MP_PART_CAP entries
+
+struct MinpArgs {
+  Args a;                 // rows, parameters, outputs; a.pos the records, a.dense_count[0] the number of
+                          // positions left to the row kernel, a.dense_list those positions
+  const float* min_p;     // [B] or null (0)
+  uint32_t* part_max;     // [rows][NP] largest key
+  uint32_t* part_count;   // [rows][NP] entries, or flags
+  void* part_list;        // [rows][NP][MP_PART_CAP] MinpEntry
+  float* out_prob;        // sampler: [R] or null
+};
+
+template <typename ET> struct MinpEntry;
+template <> struct MinpEntry<uint16_t> {
+  typedef uint32_t type;   // bits, index in the part (a part has at most 2^14)
+  __device__ __forceinline__ static type make(uint32_t bits, uint32_t i) { return bits << 16 | i; }
+  __device__ __forceinline__ static uint32_t bits(type e) { return e >> 16; }
+  __device__ __forceinline__ static uint32_t index(type e) { return e & 0xFFFFu; }
+};
+template <> struct MinpEntry<float> {
+  typedef uint2 type;
+  __device__ __forceinline__ static type make(uint32_t bits, uint32_t i) { return make_uint2(bits, i); }
+  __device__ __forceinline__ static uint32_t bits(type e) { return e.x; }
+  __device__ __forceinline__ static uint32_t index(type e) { return e.y; }
+};
+
+// How min-p treats sequence b.
+enum { MP_INVALID = 0, MP_GREEDY = 1, MP_LIST = 2, MP_ROW = 3 };   // MP_ROW: min-p is off
+struct MinpMode {
+  Mode m;
+  int kind, k;     // k: top-k, 0: off
+  float mp;
+  double cut;      // T ln(min_p)
+};
+__device__ __forceinline__ MinpMode minp_mode(const MinpArgs& ma, int b) {
+  MinpMode r;
+  r.m = seq_mode(ma.a, b);
+  const int k = ma.a.topk ? ma.a.topk[b] : 0;
+  r.k = k > 0 && k < ma.a.V ? k : 0;
+  r.mp = ma.min_p ? ma.min_p[b] : 0.0f;
+  r.cut = 0.0;
+  const int gl = ma.a.gamma_len ? ma.a.gamma_len[b] : ma.a.G;
+  const bool ok = r.m.mode != MODE_INVALID && r.m.tp == r.m.tp && r.mp <= 1.0f && (ma.a.sampler || (gl >= 1 && gl <= ma.a.G));
+  r.kind = !ok ? MP_INVALID : r.m.mode == MODE_GREEDY ? MP_GREEDY : r.mp > 0.0f ? MP_LIST : MP_ROW;
+  return r;
+}
+
+// ---------------------------------------------------------------------------
+// Integers in the order of the values: of a bit pattern, pattern ^ (sign ?
+// 0x7FF.. : 0), signed.  -0 comes right below +0.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ int mp_order32(float f) {
+  const int b = __float_as_int(f);
+  return b ^ ((b >> 31) & 0x7FFFFFFF);
+}
+template <typename ET> __device__ __forceinline__ uint32_t mp_key_of_order(int o);
+template <> __device__ __forceinline__ uint32_t mp_key_of_order<uint16_t>(int o) { return 0x8000u + (uint32_t)o + (o < 0 ? 1u : 0u); }
+template <> __device__ __forceinline__ uint32_t mp_key_of_order<float>(int o) { return 0x80000000u + (uint32_t)o + (o < 0 ? 1u : 0u); }
+
+// The smallest key whose value is not below c.
+template <typename ET>
+__device__ __forceinline__ uint32_t mp_key_from(double c) {
+  if (!(c > -3.4028234663852886e38)) return Key<ET>::NEG_INF + 1;   // every finite value
+  float f = (float)c;
+  int o = mp_order32(f);
+  if ((double)f < c) ++o;
+  if (sizeof(ET) == 2) o = o >= 0 ? (int)(((uint32_t)o + 0xFFFFu) >> 16) : o >> 16;
+  return mp_key_of_order<ET>(o);
+}
+
+// exp(x) for x <= 0 in 64 bits: 2^k times the Taylor polynomial of exp on
+// [-ln 2 / 2, ln 2 / 2], whose 13th term is below 2^-53.
+__device__ __forceinline__ double mp_exp(double x) {
+  if (!(x > -745.0)) return x == x ? 0.0 : x;
+  const double k = rint(x * 1.4426950408889634);
+  const double r = fma(k, -0x1.cf79abc9e3b3ap-40, fma(k, -0x1.62e42fefap-1, x));   // ln 2 in two parts, the first of 36 bits
+  double p = 1.0 / 6227020800.0;
+  p = fma(p, r, 1.0 / 479001600.0);
+  p = fma(p, r, 1.0 / 39916800.0);
+  p = fma(p, r, 1.0 / 3628800.0);
+  p = fma(p, r, 1.0 / 362880.0);
+  p = fma(p, r, 1.0 / 40320.0);
+  p = fma(p, r, 1.0 / 5040.0);
+  p = fma(p, r, 1.0 / 720.0);
+  p = fma(p, r, 1.0 / 120.0);
+  p = fma(p, r, 1.0 / 24.0);
+  p = fma(p, r, 1.0 / 6.0);
+  p = fma(p, r, 0.5);
+  p = fma(p, r, 1.0);
+  p = fma(p, r, 1.0);
+  return ldexp(p, (int)k);
+}
+
+// ---------------------------------------------------------------------------
+// The cut: one workgroup per (row, part).
+// ---------------------------------------------------------------------------
+
+// The 16 bytes of a row from element e on; -inf behind its end.
+__device__ __forceinline__ u32x4 mp_load(const uint16_t* row, int e, int V) {
+  u32x4 v = {0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u};
+  if (e + 8 <= V) {
+    __builtin_memcpy(&v, row + e, 16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (e + i < V) v[i / 2] = i & 1 ? (v[i / 2] & 0xFFFFu) | (uint32_t)row[e + i] << 16 : (v[i / 2] & 0xFFFF0000u) | row[e + i];
+  }
+  return v;
+}
+__device__ __forceinline__ u32x4 mp_load(const float* row, int e, int V) {
+  u32x4 v = {0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u};
+  if (e + 4 <= V) {
+    __builtin_memcpy(&v, row + e, 16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (e + i < V) v[i] = __float_as_uint(row[e + i]);
+  }
+  return v;
+}
+
+typedef short s16x2 __attribute__((ext_vector_type(2)));
+
+// Ordered integers of a 16-byte unit, in place, with their largest and smallest.
+template <typename ET> struct MinpOrder;
+template <> struct MinpOrder<uint16_t> {
+  typedef s16x2 T;
+  static constexpr int LOW = -32641;   // -inf
+  static constexpr int HIGH = 32640;   // +inf
+  __device__ __forceinline__ static T map(uint32_t x) {
+    const s16x2 v = __builtin_bit_cast(s16x2, x);
+    return v ^ ((v >> 15) & (short)0x7FFF);
+  }
+  __device__ __forceinline__ static T hi(T a, T b) { return __builtin_elementwise_max(a, b); }
+  __device__ __forceinline__ static T lo(T a, T b) { return __builtin_elementwise_min(a, b); }
+  __device__ __forceinline__ static int hi(T a) { return a.x > a.y ? a.x : a.y; }
+  __device__ __forceinline__ static int lo(T a) { return a.x < a.y ? a.x : a.y; }
+  __device__ __forceinline__ static int get(T a, int i) { return i ? a.y : a.x; }
+  __device__ __forceinline__ static float value(int o) {
+    return __uint_as_float((uint32_t)(o ^ ((o >> 31) & 0x7FFF)) << 16);
+  }
+  __device__ __forceinline__ static uint32_t bits(int o) { return (uint32_t)(o ^ ((o >> 31) & 0x7FFF)) & 0xFFFFu; }
+  // No value >= f has a smaller integer than this.
+  __device__ __forceinline__ static int floor_of(float f) { return mp_order32(f) >> 16; }
+};
+template <> struct MinpOrder<float> {
+  typedef int T;
+  static constexpr int LOW = (int)0x807FFFFFu;
+  static constexpr int HIGH = 0x7F800000;
+  __device__ __forceinline__ static T map(uint32_t x) { return (int)x ^ (((int)x >> 31) & 0x7FFFFFFF); }
+  __device__ __forceinline__ static T hi(T a, T b) { return max(a, b); }
+  __device__ __forceinline__ static T lo(T a, T b) { return min(a, b); }
+  __device__ __forceinline__ static int get(T a, int) { return a; }
+  __device__ __forceinline__ static float value(int o) { return __int_as_float(o ^ ((o >> 31) & 0x7FFFFFFF)); }
+  __device__ __forceinline__ static uint32_t bits(int o) { return (uint32_t)(o ^ ((o >> 31) & 0x7FFFFFFF)); }
+  __device__ __forceinline__ static int floor_of(float f) { return mp_order32(f); }
+};
+template <typename ET> __device__ __forceinline__ int mp_hi(typename MinpOrder<ET>::T v) { return MinpOrder<ET>::hi(v); }
+template <> __device__ __forceinline__ int mp_hi<float>(int v) { return v; }
+template <typename ET> __device__ __forceinline__ int mp_lo(typename MinpOrder<ET>::T v) { return MinpOrder<ET>::lo(v); }
+template <> __device__ __forceinline__ int mp_lo<float>(int v) { return v; }
+
+__device__ __forceinline__ int wave_max_i32(int v) { return (int)(wave_max_dpp((uint32_t)v ^ 0x80000000u) ^ 0x80000000u); }
+__device__ __forceinline__ int wave_min_i32(int v) { return (int)(wave_min_dpp((uint32_t)v ^ 0x80000000u) ^ 0x80000000u); }
+
+template <typename ET, int VPL>
+__global__ __launch_bounds__(MP_NT) void minp_cut_kernel(MinpArgs ma) {
+  typedef MinpOrder<ET> O;
+  typedef typename O::T T;
+  typedef MinpEntry<ET> E;
+  constexpr int VEC = Key<ET>::VEC, PER = 4 / sizeof(ET);   // values of a unit, of a word
+  __shared__ int smax[MP_WAVES], smin[MP_WAVES];
+  __shared__ uint32_t scnt[MP_WAVES];
+  __shared__ typename E::type stage[MP_WAVES][MP_PART_CAP];
+  const Args& a = ma.a;
+  const long long unit = blockIdx.x;
+  if (unit == 0 && threadIdx.x == 0) a.dense_count[0] = 0;   // the workspace needs no preparation
+  const int part = (int)(unit % a.NP);
+  const long long rowid = unit / a.NP;
+  const int b = (int)(rowid / a.RS), slot = (int)(rowid % a.RS);
+  const MinpMode mm = minp_mode(ma, b);
+  const bool isP = slot <= a.G;
+  const int pos = isP ? slot : slot - a.G - 1;
+  if ((mm.kind != MP_LIST && mm.kind != MP_GREEDY) || pos > mm.m.g || (!isP && pos >= mm.m.g)) return;   // not used
+  const ET* row = row_ptr<ET>(a, b, isP, pos);
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int e0 = part * a.PL, w0 = (wave * VPL * 64 + lane) * VEC;   // the lane's first value in the part
+  u32x4 raw[VPL];
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) raw[j] = mp_load(row, e0 + w0 + j * 64 * VEC, a.V);
+  T v[VPL][4], hi, lo;
+#pragma unroll
+  for (int j = 0; j < VPL; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[j][i] = O::map(raw[j][i]);
+      hi = j + i == 0 ? v[j][i] : O::hi(hi, v[j][i]);
+      lo = j + i == 0 ? v[j][i] : O::lo(lo, v[j][i]);
+    }
+  const int wh = wave_max_i32(mp_hi<ET>(hi)), wl = wave_min_i32(mp_lo<ET>(lo));
+  if (lane == 0) {
+    smax[wave] = wh;
+    smin[wave] = wl;
+  }
+  __syncthreads();
+  int top = smax[0], bot = smin[0];
+#pragma unroll
+  for (int i = 1; i < MP_WAVES; ++i) {
+    top = max(top, smax[i]);
+    bot = min(bot, smin[i]);
+  }
+  const bool bad = top >= O::HIGH || bot < O::LOW;
+  // What may be kept: at least the part's maximum plus T ln(min_p), the sum
+  // formed in 32 bits with room for its rounding.
+  int t = top;
+  if (mm.kind == MP_LIST) {
+    const float z = O::value(top), d = mm.m.T * logf(mm.mp);
+    const float c = z + d - 1e-5f * (fabsf(z) + fabsf(d)) - 1e-6f * mm.m.T;
+    t = c > -3.4e38f ? O::floor_of(c) : O::LOW + 1;   // (also where T is infinite)
+  }
+  t = max(min(t, top), O::LOW + 1);
+  if (t == 0) t = -1;   // -0 is not below +0
+  uint32_t n = 0;
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) {
+    const T m = O::hi(O::hi(v[j][0], v[j][1]), O::hi(v[j][2], v[j][3]));
+    const bool any = mp_hi<ET>(m) >= t;
+    if (__ballot(any) == 0ull) continue;
+    uint32_t c = 0;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) c += O::get(v[j][i / PER], i % PER) >= t ? 1u : 0u;
+    const uint32_t incl = wave_incl_scan_dpp(c);
+    uint32_t at = n + incl - c;
+    n += (uint32_t)__builtin_amdgcn_readlane((int)incl, 63);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      const int o = O::get(v[j][i / PER], i % PER);
+      if (o >= t) {
+        if (at < (uint32_t)MP_PART_CAP) stage[wave][at] = E::make(O::bits(o), (uint32_t)(w0 + j * 64 * VEC + i));
+        ++at;
+      }
+    }
+  }
+  if (lane == 0) scnt[wave] = n;
+  __syncthreads();
+  uint32_t base = 0, total = 0;
+#pragma unroll
+  for (int i = 0; i < MP_WAVES; ++i) {
+    if (i == wave) base = total;
+    total += scnt[i];
+  }
+  typename E::type* out = reinterpret_cast<typename E::type*>(ma.part_list) + (size_t)unit * MP_PART_CAP;
+  for (uint32_t i = lane; i < min(n, (uint32_t)MP_PART_CAP); i += 64)
+    if (base + i < (uint32_t)MP_PART_CAP) out[base + i] = stage[wave][i];
+  if (threadIdx.x == 0) {
+    ma.part_max[unit] = mp_key_of_order<ET>(top);
+    // Of equal maxima only the first counts where the token is the argmax.
+    const bool over = total > (uint32_t)MP_PART_CAP && mm.kind != MP_GREEDY;
+    ma.part_count[unit] = bad ? MP_BAD : over ? MP_OVER : min(total, (uint32_t)MP_PART_CAP);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Block-wide pieces for workgroups of NTHR threads; `red` is NTHR / 64 slots.
+// ---------------------------------------------------------------------------
+template <int NTHR>
+__device__ __forceinline__ double mp_sum(double v, double* red) {
+  v = wave_sum_dpp(v);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  double r = 0.0;
+#pragma unroll
+  for (int i = 0; i < NTHR / 64; ++i) r += red[i];
+  return r;
+}
+// The exclusive prefix of v in thread order, and the total.
+template <int NTHR>
+__device__ __forceinline__ double mp_scan(double v, double* red, double* total) {
+  const double incl = wave_incl_scan_f64(v);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 63) red[threadIdx.x >> 6] = incl;
+  __syncthreads();
+  double base = 0.0, all = 0.0;
+#pragma unroll
+  for (int i = 0; i < NTHR / 64; ++i) {
+    if (i < (int)(threadIdx.x >> 6)) base += red[i];
+    all += red[i];
+  }
+  *total = all;
+  return base + incl - v;
+}
+template <int NTHR>
+__device__ __forceinline__ uint32_t mp_scan_u32(uint32_t v, uint32_t* red, uint32_t* total) {
+  const uint32_t incl = wave_incl_scan_dpp(v);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 63) red[threadIdx.x >> 6] = incl;
+  __syncthreads();
+  uint32_t base = 0, all = 0;
+#pragma unroll
+  for (int i = 0; i < NTHR / 64; ++i) {
+    if (i < (int)(threadIdx.x >> 6)) base += red[i];
+    all += red[i];
+  }
+  *total = all;
+  return base + incl - v;
+}
+template <int NTHR, class Op>
+__device__ __forceinline__ uint32_t mp_reduce_u32(uint32_t v, uint32_t neutral, uint32_t* red, Op op) {
+  v = wave_reduce_dpp_u32(v, neutral, op);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  uint32_t r = neutral;
+#pragma unroll
+  for (int i = 0; i < NTHR / 64; ++i) r = op(r, red[i]);
+  return r;
+}
+
+struct MinpScratch {
+  unsigned long long hist[256];
+  double red[MP_ROW_NT / 64];
+  uint32_t red_u[MP_ROW_NT / 64];
+  uint32_t bc[8];
+};
+
+// The largest key t with mass(key >= t) >= tau, of the keys that feed gives
+// (with their masses), a radix select from the top digit down; 0 if there is
+// none.
+template <int LEVELS, int NTHR, class Feed>
+__device__ __forceinline__ uint32_t mp_nucleus(Feed feed, double tau, MinpScratch& s) {
+  uint32_t prefix = 0, pmask = 0;
+  unsigned long long above = 0;
+  for (int lvl = 0; lvl < LEVELS; ++lvl) {
+    const int shift = 8 * (LEVELS - 1 - lvl);
+    __syncthreads();
+    for (int i = threadIdx.x; i < 256; i += NTHR) s.hist[i] = 0ull;
+    __syncthreads();
+    feed([&](uint32_t key, double e) {
+      if ((key & pmask) == prefix) atomicAdd(&s.hist[(key >> shift) & 255u], (unsigned long long)(e * (double)(1ull << MP_FIX)));
+    });
+    __syncthreads();
+    if (threadIdx.x < 64) {
+      const int lane = threadIdx.x, first = 255 - 4 * lane;   // four digits a lane, from the top
+      unsigned long long c[4], sum = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        c[i] = s.hist[first - i];
+        sum += c[i];
+      }
+      unsigned long long incl = sum;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const unsigned long long u = shfl_up_u64(incl, o);
+        if (lane >= o) incl += u;
+      }
+      const unsigned long long reach = __ballot((double)(above + incl) >= tau);
+      const int hit = reach ? __ffsll((long long)reach) - 1 : -1;
+      if (lane == hit) {
+        unsigned long long run = above + incl - sum;
+        int d = 3;
+#pragma unroll
+        for (int i = 3; i >= 0; --i) {
+          unsigned long long upto = run;
+#pragma unroll
+          for (int q = 0; q <= i; ++q) upto += c[q];
+          if ((double)upto >= tau) d = i;
+        }
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+          if (q < d) run += c[q];
+        s.bc[0] = (uint32_t)(first - d);
+        s.bc[1] = (uint32_t)run;
+        s.bc[2] = (uint32_t)(run >> 32);
+      }
+      if (lane == 0 && hit < 0) s.bc[0] = NONE;
+    }
+    __syncthreads();
+    const uint32_t d = s.bc[0];
+    above = ((unsigned long long)s.bc[2] << 32) | s.bc[1];
+    if (d == NONE) return 0;
+    prefix |= d << shift;
+    pmask |= 255u << shift;
+  }
+  return prefix;
+}
+
+// A row's processed distribution: its values with keys >= thr, exp((z - zmax) / T) / S each.
+struct MinpRow {
+  uint32_t thr;
+  float zmax;
+  double invS;
+};
+
+// top-k and top-p of the keys >= thr that feed gives (with any others below),
+// then their sum.
+template <typename ET, int NTHR, class Feed>
+__device__ __forceinline__ void mp_filter(Feed feed, const MinpMode& mm, uint32_t kmax, double invT, MinpScratch& s, MinpRow& r) {
+  constexpr int LEVELS = Key<ET>::LEVELS;
+  const double z0 = (double)r.zmax;
+  const auto weight = [&](uint32_t key) { return mp_exp(((double)Key<ET>::value(key) - z0) * invT); };
+  if (mm.k) {
+    __syncthreads();
+    const uint32_t t = block_kth_largest<LEVELS, NTHR>(
+        [&](auto fn) { feed([&](uint32_t key) { fn(key >= r.thr ? key : 0u); }); }, (uint32_t)mm.k,
+        reinterpret_cast<uint32_t*>(s.hist), s.bc);
+    r.thr = max(r.thr, t);
+  }
+  const auto total = [&]() {
+    double x = 0.0;
+    feed([&](uint32_t key) {
+      if (key >= r.thr) x += weight(key);
+    });
+    return mp_sum<NTHR>(x, s.red);
+  };
+  double S = total();
+  if (mm.m.tp < 1.0f) {
+    const uint32_t t = mm.m.tp <= 0.0f ? kmax
+                                       : mp_nucleus<LEVELS, NTHR>([&](auto fn) {
+                                           feed([&](uint32_t key) {
+                                             if (key >= r.thr) fn(key, weight(key));
+                                           });
+                                         }, (double)mm.m.tp * S * (double)(1ull << MP_FIX), s);
+    if (t > r.thr) {
+      r.thr = t;
+      S = total();
+    }
+  }
+  r.invS = 1.0 / S;
+}
+
+// ---------------------------------------------------------------------------
+// One position from the logits.
+// ---------------------------------------------------------------------------
+template <typename ET, int NTHR, class F>
+__device__ __forceinline__ void mp_for_row(const ET* row, int V, F fn) {
+  constexpr int VEC = Key<ET>::VEC, PER = 4 / sizeof(ET);
+  for (int e = (int)threadIdx.x * VEC; e < V; e += NTHR * VEC) {
+    const u32x4 raw = mp_load(row, e, V);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      const uint32_t bits = sizeof(ET) == 2 ? (raw[i / PER] >> (16 * (i % PER))) & 0xFFFFu : raw[i / PER];
+      if (e + i < V) fn(Key<ET>::of_bits(bits), e + i);
+    }
+  }
+}
+
+template <typename ET, int NTHR>
+__device__ __forceinline__ PosRec mp_position_from_rows(const MinpArgs& ma, const MinpMode& mm, int b, int i, MinpScratch& s) {
+  const Args& a = ma.a;
+  const int V = a.V;
+  const bool two = i < mm.m.g;
+  PosRec rec{0.0, 0.0, 0.0, -1, 0u};
+  const double invT = 1.0 / (double)mm.m.T;
+  const ET* row[2] = {row_ptr<ET>(a, b, true, i), two ? row_ptr<ET>(a, b, false, i) : nullptr};
+  MinpRow r[2];
+  r[1].thr = 0xFFFFFFFFu;
+  r[1].zmax = 0.0f;
+  r[1].invS = 0.0;
+  for (int h = 0; h < (two ? 2 : 1); ++h) {
+    uint32_t kmax = 0, bad = 0;
+    mp_for_row<ET, NTHR>(row[h], V, [&](uint32_t key, int) {
+      kmax = max(kmax, key);
+      bad |= key_valid<ET>(key) ? 0u : 1u;
+    });
+    kmax = mp_reduce_u32<NTHR>(kmax, 0u, s.red_u, [](uint32_t x, uint32_t y) { return x > y ? x : y; });
+    bad = mp_reduce_u32<NTHR>(bad, 0u, s.red_u, [](uint32_t x, uint32_t y) { return x | y; });
+    if (bad || kmax <= Key<ET>::NEG_INF) {
+      rec.bad = 1u;
+      return rec;
+    }
+    r[h].zmax = Key<ET>::value(kmax);
+    r[h].thr = mm.mp > 0.0f ? min(mp_key_from<ET>((double)r[h].zmax + (double)mm.m.T * log((double)mm.mp)), kmax) : Key<ET>::NEG_INF + 1;
+    mp_filter<ET, NTHR>([&](auto fn) { mp_for_row<ET, NTHR>(row[h], V, [&](uint32_t key, int) { fn(key); }); }, mm, kmax, invT, s, r[h]);
+  }
+  const auto prob = [&](int h, uint32_t key) {
+    return key >= r[h].thr ? mp_exp(((double)Key<ET>::value(key) - (double)r[h].zmax) * invT) * r[h].invS : 0.0;
+  };
+  double al = 0.0, z = 0.0;
+  mp_for_row<ET, NTHR>(row[0], V, [&](uint32_t key, int v) {
+    const double p = prob(0, key);
+    if (p > 0.0) {
+      const double q = two ? prob(1, Key<ET>::load_key(row[1], v)) : 0.0;
+      al += fmin(p, q);
+      z += fmax(p - q, 0.0);
+    }
+  });
+  rec.alpha = mp_sum<NTHR>(al, s.red);
+  double Z = mp_sum<NTHR>(z, s.red);
+  bool resid = two;
+  if (!(Z > 0.0)) {   // no residual is left: draw from p
+    resid = false;
+    z = 0.0;
+    mp_for_row<ET, NTHR>(row[0], V, [&](uint32_t key, int) { z += prob(0, key); });
+    Z = mp_sum<NTHR>(z, s.red);
+  }
+  const int x = two ? a.draft[(size_t)b * a.G + i] : -1;
+  if (x >= 0 && x < V) {
+    rec.px = prob(0, Key<ET>::load_key(row[0], x));
+    rec.qx = prob(1, Key<ET>::load_key(row[1], x));
+  }
+  // min{v : C(v) > u Z}, a tile of ids at a time; else the last weight above 0.
+  const double target = (double)a.u[(size_t)b * (a.G + 1) + a.G] * Z;
+  constexpr int PER = Key<ET>::VEC;
+  double base = 0.0;
+  uint32_t last = 0, hit = NONE;
+  for (int t0 = 0; t0 < V && hit == NONE; t0 += NTHR * PER) {
+    const int v0 = t0 + (int)threadIdx.x * PER;
+    double w[PER], loc = 0.0, tot;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      w[e] = 0.0;
+      if (v0 + e < V) {
+        const double p = prob(0, Key<ET>::load_key(row[0], v0 + e));
+        if (p > 0.0) w[e] = resid ? fmax(p - prob(1, Key<ET>::load_key(row[1], v0 + e)), 0.0) : p;
+      }
+      loc += w[e];
+      if (w[e] > 0.0) last = (uint32_t)(v0 + e + 1);
+    }
+    double c = base + mp_scan<NTHR>(loc, s.red, &tot);
+    uint32_t mine = NONE;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      c += w[e];
+      if (mine == NONE && w[e] > 0.0 && c > target) mine = (uint32_t)(v0 + e);
+    }
+    hit = mp_reduce_u32<NTHR>(mine, NONE, s.red_u, [](uint32_t p, uint32_t q) { return p < q ? p : q; });
+    base += tot;
+  }
+  last = mp_reduce_u32<NTHR>(last, 0u, s.red_u, [](uint32_t p, uint32_t q) { return p > q ? p : q; });
+  rec.tok = hit != NONE ? (int)hit : (int)last - 1;
+  if (ma.a.sampler) rec.px = prob(0, Key<ET>::load_key(row[0], rec.tok));
+  return rec;
+}
+
+// What one thread does with a position's result: the record, or a sampled row's outputs.
+__device__ __forceinline__ void mp_put(const MinpArgs& ma, int b, int i, const PosRec& rec) {
+  const Args& a = ma.a;
+  if (!a.sampler) {
+    a.pos[(size_t)b * (a.G + 1) + i] = rec;
+    return;
+  }
+  const float u = a.u[b];
+  const bool ok = rec.bad == 0u && u >= 0.0f && u < 1.0f;
+  a.out_tokens[b] = ok ? rec.tok : -1;
+  if (ma.out_prob) ma.out_prob[b] = ok ? (float)rec.px : __int_as_float(0x7FC00000);
+}
+
+// The positions that the position kernel left.
+template <typename ET>
+__global__ __launch_bounds__(MP_ROW_NT) void minp_row_kernel(MinpArgs ma) {
+  __shared__ MinpScratch s;
+  const uint32_t n = ma.a.dense_count[0];
+  for (uint32_t j = blockIdx.x; j < n; j += gridDim.x) {
+    const int id = ma.a.dense_list[j], b = id / (ma.a.G + 1), i = id % (ma.a.G + 1);
+    const MinpMode mm = minp_mode(ma, b);
+    const PosRec rec = mp_position_from_rows<ET, MP_ROW_NT>(ma, mm, b, i, s);
+    if (threadIdx.x == 0) mp_put(ma, b, i, rec);
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// One position from the lists.
+// ---------------------------------------------------------------------------
+struct MinpSmem {
+  MinpScratch s;
+  uint32_t key[2][MP_CAP], id[2][MP_CAP];
+  double w[2][MP_CAP];    // probabilities
+  uint32_t base[MP_NT];   // entries before each of some parts
+};
+
+enum { MP_OK = 0, MP_IS_BAD = 1, MP_TOO_LONG = 2 };
+
+// The values of one row that min-p keeps, in ascending id, into key[h] and id[h].
+template <typename ET>
+__device__ __forceinline__ int mp_gather(const MinpArgs& ma, const MinpMode& mm, long long rowid, int h, MinpSmem& s, int* n,
+                                         MinpRow& r, uint32_t* kmax_out) {
+  typedef MinpEntry<ET> E;
+  const int NP = ma.a.NP, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const uint32_t* pm = ma.part_max + rowid * NP;
+  const uint32_t* pc = ma.part_count + rowid * NP;
+  uint32_t kmax = 0, flags = 0;
+  for (int p = tid; p < NP; p += MP_NT) {
+    kmax = max(kmax, pm[p]);
+    flags |= pc[p] & (MP_BAD | MP_OVER);
+  }
+  kmax = mp_reduce_u32<MP_NT>(kmax, 0u, s.s.red_u, [](uint32_t x, uint32_t y) { return x > y ? x : y; });
+  flags = mp_reduce_u32<MP_NT>(flags, 0u, s.s.red_u, [](uint32_t x, uint32_t y) { return x | y; });
+  if ((flags & MP_BAD) || kmax <= Key<ET>::NEG_INF) return MP_IS_BAD;
+  if (flags & MP_OVER) return MP_TOO_LONG;
+  r.zmax = Key<ET>::value(kmax);
+  r.thr = mm.kind == MP_GREEDY ? kmax : min(mp_key_from<ET>((double)r.zmax + (double)mm.m.T * log((double)mm.mp)), kmax);
+  *kmax_out = kmax;
+  int have = 0;
+  for (int p0 = 0; p0 < NP; p0 += MP_NT) {   // MP_NT parts at a time
+    uint32_t total;
+    const uint32_t c = p0 + tid < NP ? pc[p0 + tid] : 0u;
+    const uint32_t before = mp_scan_u32<MP_NT>(c, s.s.red_u, &total);
+    s.base[tid] = before;
+    __syncthreads();
+    const int np = min(NP - p0, MP_NT);
+    for (uint32_t i0 = 0; i0 < total; i0 += MP_NT) {
+      const uint32_t i = i0 + (uint32_t)tid;
+      uint32_t key = 0, id = 0;
+      if (i < total) {
+        int lo = 0, hi = np - 1;   // the last part whose base is at most i
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) / 2;
+          if (s.base[mid] <= i) lo = mid;
+          else hi = mid - 1;
+        }
+        const typename E::type e = reinterpret_cast<const typename E::type*>(ma.part_list)[((size_t)rowid * NP + p0 + lo) * MP_PART_CAP + (i - s.base[lo])];
+        key = Key<ET>::of_bits(E::bits(e));
+        id = (uint32_t)((p0 + lo) * ma.a.PL) + E::index(e);
+      }
+      const bool keep = key >= r.thr;
+      const unsigned long long mask = __ballot(keep);
+      __syncthreads();
+      if (lane == 0) s.s.red_u[wave] = (uint32_t)__popcll(mask);
+      __syncthreads();
+      int at = have, all = 0;
+#pragma unroll
+      for (int q = 0; q < MP_WAVES; ++q) {
+        if (q < wave) at += (int)s.s.red_u[q];
+        all += (int)s.s.red_u[q];
+      }
+      at += __popcll(mask & ((1ull << lane) - 1));
+      if (keep && at < MP_CAP) {
+        s.key[h][at] = key;
+        s.id[h][at] = id;
+      }
+      have += all;
+    }
+    __syncthreads();
+  }
+  if (mm.kind == MP_GREEDY) have = 1;   // the lowest id
+  *n = have;
+  return have > MP_CAP ? MP_TOO_LONG : MP_OK;
+}
+
+// q(v) by v's place among the ascending ids of row 1.
+__device__ __forceinline__ double mp_find(const MinpSmem& s, int n, uint32_t v) {
+  int lo = 0, hi = n;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (s.id[1][mid] < v) lo = mid + 1;
+    else hi = mid;
+  }
+  return lo < n && s.id[1][lo] == v ? s.w[1][lo] : 0.0;
+}
+
+// ROWS: a position that its lists cannot give is computed here, from the
+// logits; else it is left to the row kernel.
+template <typename ET, bool ROWS>
+__global__ __launch_bounds__(MP_NT) void minp_position_kernel(MinpArgs ma) {
+  __shared__ MinpSmem s;
+  const Args& a = ma.a;
+  const int b = (int)(blockIdx.x / (unsigned)(a.G + 1)), i = (int)(blockIdx.x % (unsigned)(a.G + 1)), tid = threadIdx.x;
+  const MinpMode mm = minp_mode(ma, b);
+  if (i == 0 && tid == 0 && !a.sampler) a.seq_flags[b] = 0;
+  PosRec rec{0.0, 0.0, 0.0, -1, 0u};
+  if (mm.kind == MP_INVALID) {
+    rec.bad = 1u;
+    if (tid == 0) mp_put(ma, b, i, rec);
+    return;
+  }
+  if (i > mm.m.g) return;
+  const bool two = i < mm.m.g;
+  int n[2] = {0, 0}, how = mm.kind == MP_ROW ? MP_TOO_LONG : MP_OK;
+  uint32_t kmax[2];
+  MinpRow r[2];
+  for (int h = 0; h < (two ? 2 : 1) && how == MP_OK; ++h)
+    how = mp_gather<ET>(ma, mm, (long long)b * a.RS + (h ? a.G + 1 + i : i), h, s, &n[h], r[h], &kmax[h]);
+  if (how == MP_TOO_LONG) {
+    if constexpr (ROWS) {
+      rec = mp_position_from_rows<ET, MP_NT>(ma, mm, b, i, s.s);
+      if (tid == 0) mp_put(ma, b, i, rec);
+    } else if (tid == 0) {
+      a.dense_list[atomicAdd(&a.dense_count[0], 1u)] = (int)blockIdx.x;
+    }
+    return;
+  }
+  if (how == MP_IS_BAD) {
+    rec.bad = 1u;
+    if (tid == 0) mp_put(ma, b, i, rec);
+    return;
+  }
+  const double invT = mm.kind == MP_GREEDY ? 0.0 : 1.0 / (double)mm.m.T;
+  for (int h = 0; h < (two ? 2 : 1); ++h) {
+    if (mm.kind == MP_GREEDY) {
+      r[h].invS = 1.0;
+    } else {
+      mp_filter<ET, MP_NT>([&](auto fn) {
+        for (int j = tid; j < n[h]; j += MP_NT) fn(s.key[h][j]);
+      }, mm, kmax[h], invT, s.s, r[h]);
+    }
+    for (int j = tid; j < n[h]; j += MP_NT) {
+      const uint32_t key = s.key[h][j];
+      s.w[h][j] = key >= r[h].thr ? mp_exp(((double)Key<ET>::value(key) - (double)r[h].zmax) * invT) * r[h].invS : 0.0;
+    }
+  }
+  __syncthreads();
+  // A thread's run of consecutive entries of the target's row.
+  constexpr int PER = MP_CAP / MP_NT;
+  const int per = (n[0] + MP_NT - 1) / MP_NT, j0 = tid * per;
+  const uint32_t x = two ? (uint32_t)a.draft[(size_t)b * a.G + i] : NONE;
+  double al = 0.0, z = 0.0, px = 0.0, w[PER];
+#pragma unroll
+  for (int e = 0; e < PER; ++e) {
+    w[e] = 0.0;
+    if (e < per && j0 + e < n[0]) {
+      const double p = s.w[0][j0 + e], q = two ? mp_find(s, n[1], s.id[0][j0 + e]) : 0.0;
+      al += fmin(p, q);
+      w[e] = fmax(p - q, 0.0);
+      if (s.id[0][j0 + e] == x) px = p;
+    }
+    z += w[e];
+  }
+  rec.alpha = mp_sum<MP_NT>(al, s.s.red);
+  rec.px = mp_sum<MP_NT>(px, s.s.red);   // one thread's
+  double Z, before = mp_scan<MP_NT>(z, s.s.red, &Z);
+  if (!(Z > 0.0)) {   // no residual is left: draw from p
+    z = 0.0;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      w[e] = e < per && j0 + e < n[0] ? s.w[0][j0 + e] : 0.0;
+      z += w[e];
+    }
+    before = mp_scan<MP_NT>(z, s.s.red, &Z);
+  }
+  rec.qx = two ? mp_find(s, n[1], x) : 0.0;
+  const double target = (double)a.u[(size_t)b * (a.G + 1) + a.G] * Z;
+  uint32_t mine = NONE, last = 0;
+#pragma unroll
+  for (int e = 0; e < PER; ++e) {
+    before += w[e];
+    if (w[e] > 0.0) {
+      last = (uint32_t)(j0 + e + 1);
+      if (mine == NONE && before > target) mine = (uint32_t)(j0 + e);
+    }
+  }
+  uint32_t hit = mp_reduce_u32<MP_NT>(mine, NONE, s.s.red_u, [](uint32_t p, uint32_t q) { return p < q ? p : q; });
+  last = mp_reduce_u32<MP_NT>(last, 0u, s.s.red_u, [](uint32_t p, uint32_t q) { return p > q ? p : q; });
+  if (hit == NONE) hit = last - 1;
+  if (tid == 0) {
+    rec.tok = (int)s.id[0][hit];
+    if (a.sampler) rec.px = s.w[0][hit];
+    mp_put(ma, b, i, rec);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Acceptance: one wavefront per sequence.
+// ---------------------------------------------------------------------------
+constexpr int MP_FIN_NT = 256;
+__global__ __launch_bounds__(MP_FIN_NT) void minp_finish_kernel(MinpArgs ma) {
+  const int b = (int)(blockIdx.x * (MP_FIN_NT / 64) + (threadIdx.x >> 6));
+  if (b >= ma.a.B) return;
+  finish_from_pairs_wave(ma.a, b, seq_mode(ma.a, b));
+}
+
+}  // namespace sv
