@@ -79,9 +79,9 @@ int spec_logits_w4(const void* hidden, int hidden_dtype, const uint8_t* weights,
  * 8-bit floating-point codes (e4m3: 4 exponent and 3 fraction bits, largest value 448, no
  * infinities) of x, with a scale for each block of SL_F8_BLOCK values along k:
  *
- *   scale = max(max |x| of the block / 448, 2^-126),  code = e4m3(x / scale)
+ *   scale = max(max |x| of the block * float(1 / 448), 2^-126),  code = e4m3(x / scale)
  *
- * in float32, the quotient rounded to float32 and then to nearest even.
+ * in float32: the product and the quotient are rounded to float32, the code to nearest even.
  *
  *  x        [R][K] bf16 or fp32 (x_dtype), aligned to its element (16-byte alignment and K a
  *           multiple of 8 take the wide path).

@@ -41,7 +41,7 @@ def quantize(x, rows=1):
     pad = np.zeros((RB * rows, KB * BLOCK), dtype=np.float32)
     pad[:R, :K] = x
     blocks = pad.reshape(RB, rows, KB, BLOCK)
-    s = np.maximum(np.abs(blocks).max((1, 3)) / np.float32(448), TINY).astype(np.float32)
+    s = np.maximum(np.abs(blocks).max((1, 3)) * (np.float32(1) / np.float32(448)), TINY).astype(np.float32)
     q = blocks / s[:, None, :, None]
     return encode(q).reshape(pad.shape)[:R, :K], s
 

@@ -1,7 +1,7 @@
 // 8-bit floating point (e4m3, 4 exponent bits, largest finite value 448) with a
 // scale for each block of 128, and logits from a head of such weights:
 //
-//   q = e4m3(x / s),  s = max(max |x| of the block / 448, 2^-126)
+//   q = e4m3(x / s),  s = max(max |x| of the block * float(1 / 448), 2^-126)
 //   out[r][n] = sum_b sx[r][b] * sw[n / 128][b] * sum_{k in b} qx[r][k] * qw[n][k]
 //
 // The matrix cores multiply such codes at twice the rate of bf16, but they align
@@ -72,9 +72,9 @@ __device__ __forceinline__ float f8_amax(const float (&v)[8]) {
   return m;
 }
 
-__device__ __forceinline__ float f8_scale(float amax) { return fmaxf(amax / 448.0f, F8_TINY); }
+__device__ __forceinline__ float f8_scale(float amax) { return fmaxf(amax * (1.0f / 448.0f), F8_TINY); }
 
-// Eight codes.  The quotients are at most 448 (1 + 2^-23), which rounds to 448.
+// Eight codes.  The quotients are at most 448 (1 + 2^-22), which rounds to 448.
 __device__ __forceinline__ uint2 f8_codes(const float (&v)[8], float s) {
   uint2 c;
   int a = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] / s, v[1] / s, 0, false);
