@@ -366,67 +366,75 @@ __global__ __launch_bounds__(512) void f8_order_kernel(F8Args a) {
   if (u == 0) a.xsc[(size_t)blockIdx.x * 32 + r] = s;
 }
 
-// 16 bytes a lane from memory into consecutive LDS, past the registers.
-__device__ __forceinline__ void f8_to_lds(const void* g, char* lds) {
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)g,
-                                   (__attribute__((address_space(3))) void*)lds, 16, 0, 0);
+// 16 bytes a lane from memory (base + a lane's offset) into consecutive LDS, past
+// the registers.  In assembly, because the compiler lets any later read of LDS
+// wait for such a load: who uses this waits himself (f8_landed), before he reads
+// what it brings, and has read what lay there before.
+__device__ __forceinline__ void f8_to_lds(const void* base, uint32_t off, const char* lds) {
+  const uint32_t at = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)lds);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(off), "s"(base) : "memory");   // (nothing else here uses m0)
 }
+// The same with 4 bytes a lane.
+__device__ __forceinline__ void f8_word_to_lds(const void* base, uint32_t off, const char* lds) {
+  const uint32_t at = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)lds);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(at), "v"(off), "s"(base) : "memory");
+}
+__device__ __forceinline__ void f8_landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
-// Four wavefronts side by side along the weight rows, 64 of them each, by
-// MT * 32 rows of x.  Weight rows are the products' rows, rows of x their
-// columns: a lane's results share a row of x, hence one scale a block.  Both
-// come from memory into LDS without registers in between.  The weights of a
-// wavefront pass through its own part of LDS (loaded in whole lines, read in
-// operand order; position q of a row holds its 16-byte unit q ^ (row % 8), so
-// that the reads do not conflict): a block is read into registers, then the
-// next one is loaded in its place.  The operands of x are shared, in two
-// buffers.
-constexpr int F8T_NT = 256;
-constexpr int F8T_N = 256;   // weight rows of a workgroup
+// Eight wavefronts, four along the weight rows (32 CN of them each) by two along
+// the rows of x (32 MT each).  Weight rows are the products' rows, rows of x
+// their columns: a lane's results share a row of x, hence one scale a block.
+// Both come from memory into LDS without registers in between, a block ahead,
+// in two buffers with one barrier a block.  The weights are loaded in whole
+// lines and read in operand order; position q of a row holds its 16-byte unit
+// q ^ (row % 8), so that the reads do not conflict.
+constexpr int F8T_NT = 512;
 
-template <int MT, bool F8>
+template <int CN, int MT, bool F8>
+__host__ __device__ constexpr int f8_tile_lds() { return 2 * (4 * CN * 4096 + 2 * MT * (f8_block_bytes<F8>() + 128)); }
+
+template <int CN, int MT, bool F8>
 __global__ __launch_bounds__(F8T_NT, 2) void f8_tile_kernel(F8Args a) {
-  constexpr int XB = f8_block_bytes<F8>();
-  __shared__ __align__(16) char wlds[4][8192];
-  __shared__ __align__(16) char xlds[2][MT * XB];
-  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, l32 = lane & 31,
-            half = lane >> 5;
+  constexpr int XB = f8_block_bytes<F8>(), N = 128 * CN;   // weight rows of a workgroup
+  constexpr int WL = N * 128, XL = 2 * MT * XB;            // bytes of a block
+  constexpr int WI = WL / 8192, XI = XL / 8192;            // 1 KB loads a wavefront
+  constexpr int SL = 2 * MT * 128, XAT = 2 * WL, SAT = XAT + 2 * XL;
+  extern __shared__ __align__(16) char lds[];              // [2] weights, [2] operands of x, [2] their scales
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), wn = wave & 3, wr = wave >> 2;
+  int lane = tid & 63;
   const int KB = a.KB;
-  const long long sets = (long long)((a.N + F8T_N - 1) / F8T_N) * a.row_tiles;
+  const long long sets = (long long)((a.N + N - 1) / N) * a.row_tiles;
   // The row tiles of a column tile run on one XCD, one after the other.
   const long long set = (long long)(blockIdx.x & 7) * a.per_xcd + (blockIdx.x >> 3);
   if (set >= sets) return;
-  const int rt = (int)(set % a.row_tiles) * MT;
-  const int n0 = (int)(set / a.row_tiles) * F8T_N + wave * 64;
+  const int rt = (int)(set % a.row_tiles) * 2 * MT;        // of 32 rows
+  const int n0 = (int)(set / a.row_tiles) * N;
   const char* xop = a.xop + (size_t)rt * KB * XB;
-  const float* xsc = a.xsc + (size_t)rt * KB * 32;
-  // Behind the last weight row it is repeated.
-  const int nb = min(n0, a.N - 1);
-  const float* sw = a.s + (size_t)(nb / 128) * KB;
-  const uint8_t* wbase = a.w + (size_t)nb * a.K;
-  uint32_t wrow[8];
+  const char* xsc = reinterpret_cast<const char*>(a.xsc + (size_t)rt * KB * 32);
+  const float* sw = a.s + (size_t)(min(n0 + wn * 32 * CN, a.N - 1) / 128) * KB;
+  const uint8_t* wbase = a.w + (size_t)n0 * a.K;
+  // What lies behind the last weight row repeats it; what lies beyond K repeats
+  // the row's end, and meets zeros of x.
+  const int wlast = a.N - 1 - n0;
+  const uint32_t xlen = (uint32_t)KB * XB;   // bytes of a row tile
+  auto load = [&](int b) __attribute__((always_inline)) {
+    const uint32_t k = (uint32_t)min(b * 128 + ((lane & 7) ^ (lane >> 3)) * 16, a.K - 16);
+    const char* wl = lds + (b & 1) * WL + wave * 1024 * WI;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) wrow[i] = (uint32_t)min(i * 8 + (lane >> 3), a.N - 1 - nb) * (uint32_t)a.K;
-  const int wk = ((lane & 7) ^ (lane >> 3)) * 16;
-  char* wl = wlds[wave];
-
-  // What lies beyond K repeats the row's end: it meets zeros of x.
-  auto load_w = [&](int b) __attribute__((always_inline)) {
-    const uint32_t k = (uint32_t)min(b * 128 + wk, a.K - 16);
+    for (int i = 0; i < WI; ++i) f8_to_lds(wbase, (uint32_t)min((wave * WI + i) * 8 + (lane >> 3), wlast) * (uint32_t)a.K + k, wl + i * 1024);
+    const char* from = xop + (size_t)b * XB;
+    const char* xl = lds + XAT + (b & 1) * XL;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f8_to_lds(wbase + (wrow[i] + k), wl + i * 1024);
-  };
-  auto load_x = [&](int b) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < MT * XB / 4096; ++i) {
-      const int at = i * 4096 + wave * 1024, m = at / XB;   // XB is a multiple of 4096: m does not depend on the wavefront
-      f8_to_lds(xop + ((size_t)m * KB + b) * XB + (at % XB + lane * 16), xlds[b & 1] + at);
+    for (int i = 0; i < XI; ++i) {
+      const int at = (i * 8 + wave) * 1024, m = at / XB;
+      f8_to_lds(from + ((size_t)m * xlen + at % XB), lane * 16, xl + at);
     }
+    if (wave < MT)   // the scales of two row tiles
+      f8_word_to_lds(xsc + ((size_t)wave * 2 * KB + b) * 128, (uint32_t)(lane >> 5) * (uint32_t)KB * 128 + (lane & 31) * 4, lds + SAT + (b & 1) * SL + wave * 256);
   };
-
-  f32x16 tot[2][MT];
+  f32x16 tot[CN][MT];
 #pragma unroll
-  for (int c = 0; c < 2; ++c)
+  for (int c = 0; c < CN; ++c)
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -435,73 +443,115 @@ __global__ __launch_bounds__(F8T_NT, 2) void f8_tile_kernel(F8Args a) {
 #pragma unroll
   for (int r = 0; r < 16; ++r) zero[r] = 0.0f;
 
-  load_w(0);
-  load_x(0);
+  float swn = sw[0];
+  load(0);
   for (int b = 0; b < KB; ++b) {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // this wavefront's loads into LDS have landed
-    __syncthreads();                                   // and everyone's
-    i32x4 wv[2][4];
-#pragma unroll
-    for (int c = 0; c < 2; ++c)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        wv[c][q] = *reinterpret_cast<const i32x4*>(wl + (c * 32 + l32) * 128 + (((half * 4 + q) ^ (l32 & 7)) << 4));
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the block is in registers: its place is free
-    float sx[MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) sx[m] = xsc[((size_t)m * KB + b) * 32 + l32] * sw[b];
+    f8_landed();       // this wavefront's loads of the block
+    __syncthreads();   // and everyone's; the other buffers have been read
+    const float swb = swn;
+    asm volatile("" : "+v"(lane));   // what follows from it is formed again in each block: registers are short
     if (b + 1 < KB) {
-      load_w(b + 1);
-      load_x(b + 1);
+      swn = sw[b + 1];
+      load(b + 1);
     }
-    const char* xl = xlds[b & 1] + lane * 16;
+    const int l32 = lane & 31, half = lane >> 5;
+    // Unit 4 half + q of a row, q = 0..3, lies at position (4 half ^ row % 8) ^ q.
+    const uint32_t wl = (uint32_t)((b & 1) * WL + (wn * 32 * CN + l32) * 128 + (((half * 4) ^ (l32 & 7)) << 4));
+    const char* xl = lds + XAT + (b & 1) * XL + wr * MT * XB + lane * 16;
+    const float* sl = reinterpret_cast<const float*>(lds + SAT + (b & 1) * SL + wr * MT * 128) + l32;
+    i32x4 wv[CN][4];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      if constexpr (F8) {
-        i32x8 xv[2];
+    for (int c = 0; c < CN; ++c)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          xv[j] = f8_join(*reinterpret_cast<const i32x4*>(xl + m * XB + j * 2048), *reinterpret_cast<const i32x4*>(xl + m * XB + j * 2048 + 1024));
+      for (int q = 0; q < 4; ++q) wv[c][q] = *reinterpret_cast<const i32x4*>(lds + (wl ^ (q << 4)) + c * 4096);
+    if constexpr (F8) {
+      // Step (m, c): two products, and in their shade the scaling of the step before.
+      f32x16 p[2];
+      i32x8 xv[2];
+      float sx = 0.0f, next = sl[0] * swb;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          f32x16 p = zero;
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            p = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f8_join(wv[c][2 * j], wv[c][2 * j + 1]), xv[j], p, 0, 0, 0, 0, 0, 0);
-#pragma unroll
-          for (int r = 0; r < 16; ++r) tot[c][m][r] = __builtin_fmaf(sx[m], p[r], tot[c][m][r]);
+      for (int q = 0; q <= CN * MT; ++q) {
+        const int m = q / CN, c = q % CN, mb = (q - 1) / CN, cb = (q - 1) % CN;
+        if (q > 0 && cb == 0) {   // the first step that scales row tile mb
+          sx = next;
+          if (mb + 1 < MT) next = sl[(mb + 1) * 32] * swb;
         }
-      } else {
-        f32x16 p[2] = {zero, zero};
+        if (q < CN * MT) {
+          if (c == 0) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              xv[j] = f8_join(*reinterpret_cast<const i32x4*>(xl + m * XB + j * 2048), *reinterpret_cast<const i32x4*>(xl + m * XB + j * 2048 + 1024));
+          }
+          p[q & 1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f8_join(wv[c][0], wv[c][1]), xv[0], zero, 0, 0, 0, 0, 0, 0);
+          p[q & 1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f8_join(wv[c][2], wv[c][3]), xv[1], p[q & 1], 0, 0, 0, 0, 0, 0);
+        }
+        if (q > 0) {
+#pragma unroll
+          for (int r = 0; r < 16; ++r) tot[cb][mb][r] = __builtin_fmaf(sx, p[(q - 1) & 1][r], tot[cb][mb][r]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    } else {
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        f32x16 p[CN];
+#pragma unroll
+        for (int c = 0; c < CN; ++c) p[c] = zero;
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
           const bf16x8 xv = *reinterpret_cast<const bf16x8*>(xl + m * XB + t * 1024);
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
+          for (int c = 0; c < CN; ++c)
             p[c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f8_expand((uint32_t)wv[c][t >> 1][2 * (t & 1)], (uint32_t)wv[c][t >> 1][2 * (t & 1) + 1]), xv, p[c], 0, 0, 0);
         }
+        const float sx = sl[m * 32] * swb;
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+        for (int c = 0; c < CN; ++c)
 #pragma unroll
-          for (int r = 0; r < 16; ++r) tot[c][m][r] = __builtin_fmaf(sx[m], p[c][r], tot[c][m][r]);
+          for (int r = 0; r < 16; ++r) tot[c][m][r] = __builtin_fmaf(sx, p[c][r], tot[c][m][r]);
       }
     }
   }
 
+  // The results through LDS, so that whole lines are written: a wavefront's
+  // 32 rows of 32 CN values at a time.
+  __syncthreads();
+  const int l32 = lane & 31, half = lane >> 5;
+  const int nw = n0 + wn * 32 * CN, cols = min(a.N - nw, 32 * CN);
+  const int es = a.out_bf16 ? 2 : 4, pitch = 32 * CN * es + 16;
+  char* mine = lds + wave * (32 * (32 * CN * 4 + 16));
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
-    const int row = (rt + m) * 32 + l32;
-    if (row >= a.R) continue;
+    char* put = mine + l32 * pitch;
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
+    for (int c = 0; c < CN; ++c)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int n = n0 + c * 32 + 8 * (r / 4) + 4 * half + r % 4;
-        if (n >= a.N) continue;
-        const size_t o = (size_t)row * a.N + n;
-        if (a.out_bf16) store_out(reinterpret_cast<uint16_t*>(a.out) + o, tot[c][m][r]);
-        else store_out(reinterpret_cast<float*>(a.out) + o, tot[c][m][r]);
+      for (int g = 0; g < 4; ++g) {
+        const int n = c * 32 + 8 * g + 4 * half;
+        const f32x4 v = {tot[c][m][4 * g], tot[c][m][4 * g + 1], tot[c][m][4 * g + 2], tot[c][m][4 * g + 3]};
+        if (a.out_bf16) {
+          const uint2 h = make_uint2(to_bf16(v[0]) | (uint32_t)to_bf16(v[1]) << 16, to_bf16(v[2]) | (uint32_t)to_bf16(v[3]) << 16);
+          *reinterpret_cast<uint2*>(put + n * 2) = h;
+        } else {
+          *reinterpret_cast<f32x4*>(put + n * 4) = v;
+        }
       }
+    const int row0 = (rt + wr * MT + m) * 32, unit = 16 / es, per = 32 * CN / unit;   // 16-byte units of a row
+    char* out = reinterpret_cast<char*>(a.out);
+    for (int u = lane; u < 32 * per; u += 64) {
+      const int r = u / per, n = u % per * unit;
+      if (row0 + r >= a.R) continue;
+      const char* from = mine + r * pitch + n * es;
+      char* to = out + ((size_t)(row0 + r) * a.N + nw + n) * es;
+      if (n + unit <= cols) {
+        __builtin_memcpy(to, from, 16);
+      } else {
+        for (int e = 0; n + e < cols; ++e) {
+          if (a.out_bf16) reinterpret_cast<uint16_t*>(to)[e] = reinterpret_cast<const uint16_t*>(from)[e];
+          else reinterpret_cast<float*>(to)[e] = reinterpret_cast<const float*>(from)[e];
+        }
+      }
+    }
   }
 }
 

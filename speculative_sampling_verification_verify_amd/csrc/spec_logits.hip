@@ -8,6 +8,8 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <mutex>
+
 namespace sl {
 
 static thread_local char g_errbuf[256];
@@ -182,6 +184,27 @@ extern "C" int spec_logits_w4(const void* hidden, int hidden_dtype, const uint8_
 // ---------------------------------------------------------------------------
 namespace sl {
 
+// Raises a kernel's dynamic-LDS limit on the current device, once for each
+// kernel and device: what is known of it is kept in a small table.
+constexpr int MAX_DEVICES = 64;
+static hipError_t lds_limit(const void* kernel, int bytes) {
+  static std::mutex mu;
+  static struct { const void* kernel; uint64_t devices; } done[16];
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  if (dev < 0 || dev >= MAX_DEVICES) return hipErrorInvalidDevice;
+  std::lock_guard<std::mutex> lk(mu);
+  int i = 0;
+  while (i < 15 && done[i].kernel && done[i].kernel != kernel) ++i;
+  if (done[i].kernel == kernel && (done[i].devices >> dev & 1)) return hipSuccess;
+  if ((e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes)) != hipSuccess) return e;
+  if (done[i].kernel != kernel) done[i].devices = 0;
+  done[i].kernel = kernel;
+  done[i].devices |= 1ull << dev;
+  return hipSuccess;
+}
+
 static int f8_sizes(int R, int K) {
   if (R > SL_MAX_ROWS || K > SL_MAX_K) return SV_ERR_UNSUPPORTED;
   if (R < 0 || K < 1) return SV_ERR_ARG;
@@ -203,7 +226,7 @@ static int launch_quantize(const F8QuantArgs& a, int rows, hipStream_t st) {
 constexpr int F8_EXACT_ROWS = 64;
 
 struct F8Plan {
-  int stream, rp, mt, f8, row_tiles;
+  int stream, rp, mt, f8, row_tiles;   // mt: tiles of 32 rows of a wavefront, half of a workgroup's
   size_t op_bytes, bytes;
 };
 static F8Plan f8_plan(int out_dtype, int R, int K) {
@@ -217,18 +240,28 @@ static F8Plan f8_plan(int out_dtype, int R, int K) {
     return p;
   }
   p.f8 = out_dtype == SV_BF16 && R > F8_EXACT_ROWS;
-  p.mt = p.f8 ? 4 : R <= 32 ? 1 : 2;
-  p.row_tiles = (R + 32 * p.mt - 1) / (32 * p.mt);
-  p.op_bytes = (size_t)p.row_tiles * p.mt * KB * (p.f8 ? f8_block_bytes<true>() : f8_block_bytes<false>());
-  p.bytes = p.op_bytes + (size_t)p.row_tiles * p.mt * KB * 128;
+  // The widest tile that wastes the fewest rows.
+  const int most = p.f8 ? 5 : 2;
+  p.mt = 1;
+  for (int mt = 2; mt <= most; ++mt)
+    if ((R + 64 * mt - 1) / (64 * mt) * mt <= (R + 64 * p.mt - 1) / (64 * p.mt) * p.mt) p.mt = mt;
+  p.row_tiles = (R + 64 * p.mt - 1) / (64 * p.mt);
+  const size_t blocks = (size_t)p.row_tiles * 2 * p.mt * KB;
+  p.op_bytes = blocks * (p.f8 ? f8_block_bytes<true>() : f8_block_bytes<false>());
+  p.bytes = p.op_bytes + blocks * 128;
   return p;
 }
 
-template <int MT, bool F8>
+// The kernel's LDS limit is raised once per device, whatever call comes first.
+template <int CN, int MT, bool F8>
 static hipError_t launch_f8_tile(F8Args a, hipStream_t st) {
-  const long long sets = (long long)((a.N + F8T_N - 1) / F8T_N) * a.row_tiles;
+  constexpr int least = 8 * 32 * (32 * CN * 4 + 16), lds = f8_tile_lds<CN, MT, F8>() > least ? f8_tile_lds<CN, MT, F8>() : least;
+  static_assert(lds <= 160 * 1024, "a workgroup's LDS");
+  const hipError_t e = lds_limit(reinterpret_cast<const void*>(&f8_tile_kernel<CN, MT, F8>), lds);
+  if (e != hipSuccess) return e;
+  const long long sets = (long long)((a.N + 128 * CN - 1) / (128 * CN)) * a.row_tiles;
   a.per_xcd = (int)((sets + 7) / 8);
-  hipLaunchKernelGGL((f8_tile_kernel<MT, F8>), dim3((unsigned)a.per_xcd * 8), dim3(F8T_NT), 0, st, a);
+  hipLaunchKernelGGL((f8_tile_kernel<CN, MT, F8>), dim3((unsigned)a.per_xcd * 8), dim3(F8T_NT), lds, st, a);
   return hipGetLastError();
 }
 
@@ -241,13 +274,21 @@ static hipError_t launch_f8(F8Args a, const F8Plan& p, hipStream_t st) {
     hipLaunchKernelGGL((f8_stream_kernel<XT>), dim3((unsigned)(tiles < W4S_GRID ? tiles : W4S_GRID)), dim3(F8S_NT), 0, st, a);
     return hipGetLastError();
   }
-  const dim3 grid((unsigned)(p.row_tiles * p.mt * a.KB));
+  const dim3 grid((unsigned)(p.row_tiles * 2 * p.mt * a.KB));
   if (p.f8) hipLaunchKernelGGL((f8_order_kernel<XT, true>), grid, dim3(512), 0, st, a);
   else hipLaunchKernelGGL((f8_order_kernel<XT, false>), grid, dim3(512), 0, st, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (p.f8) return launch_f8_tile<4, true>(a, st);
-  return p.mt == 1 ? launch_f8_tile<1, false>(a, st) : launch_f8_tile<2, false>(a, st);
+  if (p.f8) {
+    switch (p.mt) {
+      case 1: return launch_f8_tile<2, 1, true>(a, st);
+      case 2: return launch_f8_tile<2, 2, true>(a, st);
+      case 3: return launch_f8_tile<2, 3, true>(a, st);
+      case 4: return launch_f8_tile<2, 4, true>(a, st);
+      default: return launch_f8_tile<2, 5, true>(a, st);
+    }
+  }
+  return p.mt == 1 ? launch_f8_tile<2, 1, false>(a, st) : launch_f8_tile<2, 2, false>(a, st);
 }
 
 }  // namespace sl
