@@ -450,48 +450,70 @@ __global__ __launch_bounds__(F8T_NT, 2) void f8_tile_kernel(F8Args a) {
     __syncthreads();   // and everyone's; the other buffers have been read
     const float swb = swn;
     asm volatile("" : "+v"(lane));   // what follows from it is formed again in each block: registers are short
-    if (b + 1 < KB) {
-      swn = sw[b + 1];
-      load(b + 1);
-    }
     const int l32 = lane & 31, half = lane >> 5;
     // Unit 4 half + q of a row, q = 0..3, lies at position (4 half ^ row % 8) ^ q.
     const uint32_t wl = (uint32_t)((b & 1) * WL + (wn * 32 * CN + l32) * 128 + (((half * 4) ^ (l32 & 7)) << 4));
     const char* xl = lds + XAT + (b & 1) * XL + wr * MT * XB + lane * 16;
     const float* sl = reinterpret_cast<const float*>(lds + SAT + (b & 1) * SL + wr * MT * 128) + l32;
     i32x4 wv[CN][4];
-#pragma unroll
-    for (int c = 0; c < CN; ++c)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) wv[c][q] = *reinterpret_cast<const i32x4*>(lds + (wl ^ (q << 4)) + c * 4096);
+    auto read_w = [&](int c, int q) __attribute__((always_inline)) {
+      wv[c][q] = *reinterpret_cast<const i32x4*>(lds + (wl ^ (q << 4)) + c * 4096);
+    };
+    auto next = [&]() __attribute__((always_inline)) {   // the next block's loads
+      if (b + 1 < KB) {
+        swn = sw[b + 1];
+        load(b + 1);
+      }
+    };
     if constexpr (F8) {
-      // Step (m, c): two products, and in their shade the scaling of the step before.
+      // What the first products need is read first, then the next block's loads
+      // go out.  Step (m, c): two products, and in their shade the scaling of the
+      // step before.
+      constexpr int XD = MT < 5 ? 2 : 1;   // the operands of a row tile are read while those of the last one are in use
       f32x16 p[2];
-      i32x8 xv[2];
-      float sx = 0.0f, next = sl[0] * swb;
+      i32x8 xv[XD][2];
+      auto read_x = [&](int m) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          xv[m % XD][j] = f8_join(*reinterpret_cast<const i32x4*>(xl + m * XB + j * 2048), *reinterpret_cast<const i32x4*>(xl + m * XB + j * 2048 + 1024));
+      };
+      read_w(0, 0);
+      read_w(0, 1);
+      read_x(0);
+      read_w(0, 2);
+      read_w(0, 3);
+      float sx[MT];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) sx[m] = sl[m * 32];
+      __builtin_amdgcn_sched_barrier(0);
+      next();
+#pragma unroll
+      for (int c = 1; c < CN; ++c)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) read_w(c, q);
 #pragma unroll
       for (int q = 0; q <= CN * MT; ++q) {
         const int m = q / CN, c = q % CN, mb = (q - 1) / CN, cb = (q - 1) % CN;
-        if (q > 0 && cb == 0) {   // the first step that scales row tile mb
-          sx = next;
-          if (mb + 1 < MT) next = sl[(mb + 1) * 32] * swb;
-        }
+        if (q > 0 && cb == 0) sx[mb] *= swb;
         if (q < CN * MT) {
-          if (c == 0) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-              xv[j] = f8_join(*reinterpret_cast<const i32x4*>(xl + m * XB + j * 2048), *reinterpret_cast<const i32x4*>(xl + m * XB + j * 2048 + 1024));
-          }
-          p[q & 1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f8_join(wv[c][0], wv[c][1]), xv[0], zero, 0, 0, 0, 0, 0, 0);
-          p[q & 1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f8_join(wv[c][2], wv[c][3]), xv[1], p[q & 1], 0, 0, 0, 0, 0, 0);
+          if (XD == 1 && c == 0 && m > 0) read_x(m);
+          p[q & 1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f8_join(wv[c][0], wv[c][1]), xv[m % XD][0], zero, 0, 0, 0, 0, 0, 0);
+          p[q & 1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(f8_join(wv[c][2], wv[c][3]), xv[m % XD][1], p[q & 1], 0, 0, 0, 0, 0, 0);
+          __builtin_amdgcn_sched_barrier(0);
+          if (XD == 2 && c == 0 && m + 1 < MT) read_x(m + 1);
         }
         if (q > 0) {
 #pragma unroll
-          for (int r = 0; r < 16; ++r) tot[cb][mb][r] = __builtin_fmaf(sx, p[(q - 1) & 1][r], tot[cb][mb][r]);
+          for (int r = 0; r < 16; ++r) tot[cb][mb][r] = __builtin_fmaf(sx[mb], p[(q - 1) & 1][r], tot[cb][mb][r]);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
     } else {
+      next();
+#pragma unroll
+      for (int c = 0; c < CN; ++c)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) read_w(c, q);
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         f32x16 p[CN];
