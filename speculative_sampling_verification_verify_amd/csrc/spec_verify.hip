@@ -961,7 +961,7 @@ namespace sv {
 struct MinpPlan {
   int vpl;    // 16-byte units a thread of the cut kernel
   int NP, PL;
-  size_t flags_off, pos_off, redo_off, max_off, count_off, list_off, total;
+  size_t flags_off, pos_off, rows_off, redo_off, max_off, count_off, list_off, total;
 };
 
 // Row parts of 32 KB; of 8 KB in calls of few, which then spread over the chip.
@@ -979,7 +979,8 @@ static MinpPlan minp_plan(int B, int G, int V, int dtype) {
   const auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   p.flags_off = 256;
   p.pos_off = up(p.flags_off + (size_t)B * 4);
-  p.redo_off = up(p.pos_off + np * sizeof(PosRec));
+  p.rows_off = up(p.pos_off + np * sizeof(PosRec));
+  p.redo_off = up(p.rows_off + 2 * np * sizeof(MinpRow));
   p.max_off = up(p.redo_off + np * 4);
   p.count_off = up(p.max_off + units * 4);
   p.list_off = up(p.count_off + units * 4);
@@ -1007,6 +1008,8 @@ static hipError_t launch_minp(const MinpArgs& ma, const MinpPlan& p, int hints, 
     hipLaunchKernelGGL((minp_position_kernel<ET, false>), positions, dim3(MP_NT), 0, st, ma);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     hipLaunchKernelGGL((minp_row_kernel<ET>), dim3(MP_ROW_GRID), dim3(MP_ROW_NT), 0, st, ma);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    hipLaunchKernelGGL((minp_row_position_kernel<ET>), dim3(MP_ROW_GRID), dim3(MP_ROW_NT), 0, st, ma);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   if (a.sampler) return hipSuccess;
@@ -1057,6 +1060,7 @@ static int run_minp(const void* p_logits, const void* q_logits, int dtype, const
   a.pos = reinterpret_cast<PosRec*>(ws + p.pos_off);
   a.dense_list = reinterpret_cast<int32_t*>(ws + p.redo_off);
   ma.min_p = min_p;
+  ma.rows = reinterpret_cast<MinpRow*>(ws + p.rows_off);
   ma.part_max = reinterpret_cast<uint32_t*>(ws + p.max_off);
   ma.part_count = reinterpret_cast<uint32_t*>(ws + p.count_off);
   ma.part_list = ws + p.list_off;

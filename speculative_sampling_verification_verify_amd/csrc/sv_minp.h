@@ -12,7 +12,8 @@
 //                         values of the position's target and draft row,
 //                         gathered in LDS, give p(x), q(x), the overlap and the
 //                         draw as if the first rejection were there
-//   minp_row_kernel       the same from the logits, for rows without min-p and
+//   minp_row_kernel, minp_row_position_kernel
+//                         the same from the logits, for rows without min-p and
 //                         rows that keep more than the lists hold
 //   minp_finish_kernel    one wavefront per sequence: acceptance and outputs
 //
@@ -32,11 +33,20 @@ constexpr int MP_PART_CAP = 512;  // list entries of a row part
 constexpr int MP_CAP = 1024;      // kept values of a row that the position kernel holds
 constexpr int MP_ROW_NT = 1024;   // threads of a row workgroup
 constexpr int MP_ROW_GRID = 512;
+constexpr int MP_FEW_KEYS = 8192; // keys of one bin that a row workgroup holds
+constexpr int MP_BINS = 512;      // bins of a row's masses, 1/8 wide in (zmax - z) / T; at least 256
 constexpr int MP_FIX = 42;        // fraction bits of a mass: at most 2^20 masses of at most 1
 
 // Flags in a part's count.
 constexpr uint32_t MP_BAD = 1u << 30;    // NaN or +inf
 constexpr uint32_t MP_OVER = 1u << 31;   // more than MP_PART_CAP entries
+
+// A row's processed distribution: its values with keys >= thr, exp((z - zmax) / T) / S each.
+struct MinpRow {
+  uint32_t thr;
+  float zmax;
+  double invS;
+};
 
 struct MinpArgs {
   Args a;                 // rows, parameters, outputs; a.pos the records, a.dense_count[0] the number of
@@ -46,6 +56,7 @@ struct MinpArgs {
   uint32_t* part_count;   // [rows][NP] entries, or flags
   void* part_list;        // [rows][NP][MP_PART_CAP] MinpEntry
   float* out_prob;        // sampler: [R] or null
+  MinpRow* rows;          // [B * (G + 1)][2] distributions of the positions left to the row kernels
 };
 
 template <typename ET> struct MinpEntry;
@@ -76,10 +87,10 @@ __device__ __forceinline__ MinpMode minp_mode(const MinpArgs& ma, int b) {
   const int k = ma.a.topk ? ma.a.topk[b] : 0;
   r.k = k > 0 && k < ma.a.V ? k : 0;
   r.mp = ma.min_p ? ma.min_p[b] : 0.0f;
-  r.cut = 0.0;
   const int gl = ma.a.gamma_len ? ma.a.gamma_len[b] : ma.a.G;
   const bool ok = r.m.mode != MODE_INVALID && r.m.tp == r.m.tp && r.mp <= 1.0f && (ma.a.sampler || (gl >= 1 && gl <= ma.a.G));
   r.kind = !ok ? MP_INVALID : r.m.mode == MODE_GREEDY ? MP_GREEDY : r.mp > 0.0f ? MP_LIST : MP_ROW;
+  r.cut = r.kind >= MP_LIST && r.mp > 0.0f ? (double)r.m.T * log((double)r.mp) : 0.0;
   return r;
 }
 
@@ -109,7 +120,8 @@ __device__ __forceinline__ uint32_t mp_key_from(double c) {
 // exp(x) for x <= 0 in 64 bits: 2^k times the Taylor polynomial of exp on
 // [-ln 2 / 2, ln 2 / 2], whose 13th term is below 2^-53.
 __device__ __forceinline__ double mp_exp(double x) {
-  if (!(x > -745.0)) return x == x ? 0.0 : x;
+  const double y = x;
+  x = fmax(x, -746.0);   // (no branch: -inf, too, takes this way)
   const double k = rint(x * 1.4426950408889634);
   const double r = fma(k, -0x1.cf79abc9e3b3ap-40, fma(k, -0x1.62e42fefap-1, x));   // ln 2 in two parts, the first of 36 bits
   double p = 1.0 / 6227020800.0;
@@ -126,7 +138,7 @@ __device__ __forceinline__ double mp_exp(double x) {
   p = fma(p, r, 0.5);
   p = fma(p, r, 1.0);
   p = fma(p, r, 1.0);
-  return ldexp(p, (int)k);
+  return y > -745.0 ? ldexp(p, (int)k) : 0.0;
 }
 
 // ---------------------------------------------------------------------------
@@ -356,26 +368,27 @@ __device__ __forceinline__ uint32_t mp_reduce_u32(uint32_t v, uint32_t neutral, 
 }
 
 struct MinpScratch {
-  unsigned long long hist[256];
+  unsigned long long hist[MP_BINS];
   double red[MP_ROW_NT / 64];
   uint32_t red_u[MP_ROW_NT / 64];
   uint32_t bc[8];
 };
 
+__device__ __forceinline__ unsigned long long mp_fixed(double e) { return (unsigned long long)(e * (double)(1ull << MP_FIX)); }
+
 // The largest key t with mass(key >= t) >= tau, of the keys that feed gives
-// (with their masses), a radix select from the top digit down; 0 if there is
-// none.
+// (with their masses; `above`: the mass of those it leaves out, all larger), a
+// radix select from the top digit down; 0 if there is none.
 template <int LEVELS, int NTHR, class Feed>
-__device__ __forceinline__ uint32_t mp_nucleus(Feed feed, double tau, MinpScratch& s) {
+__device__ __forceinline__ uint32_t mp_nucleus(Feed feed, unsigned long long above, double tau, MinpScratch& s) {
   uint32_t prefix = 0, pmask = 0;
-  unsigned long long above = 0;
   for (int lvl = 0; lvl < LEVELS; ++lvl) {
     const int shift = 8 * (LEVELS - 1 - lvl);
     __syncthreads();
     for (int i = threadIdx.x; i < 256; i += NTHR) s.hist[i] = 0ull;
     __syncthreads();
     feed([&](uint32_t key, double e) {
-      if ((key & pmask) == prefix) atomicAdd(&s.hist[(key >> shift) & 255u], (unsigned long long)(e * (double)(1ull << MP_FIX)));
+      if ((key & pmask) == prefix) atomicAdd(&s.hist[(key >> shift) & 255u], mp_fixed(e));
     });
     __syncthreads();
     if (threadIdx.x < 64) {
@@ -423,27 +436,23 @@ __device__ __forceinline__ uint32_t mp_nucleus(Feed feed, double tau, MinpScratc
   return prefix;
 }
 
-// A row's processed distribution: its values with keys >= thr, exp((z - zmax) / T) / S each.
-struct MinpRow {
-  uint32_t thr;
-  float zmax;
-  double invS;
-};
+// top-k, of the keys >= thr that feed gives (with any others below): raises thr.
+template <typename ET, int NTHR, class Feed>
+__device__ __forceinline__ void mp_top_k(Feed feed, const MinpMode& mm, MinpScratch& s, uint32_t* thr) {
+  if (!mm.k) return;
+  __syncthreads();
+  const uint32_t t = block_kth_largest<Key<ET>::LEVELS, NTHR>(
+      [&](auto fn) { feed([&](uint32_t key) { fn(key >= *thr ? key : 0u); }); }, (uint32_t)mm.k,
+      reinterpret_cast<uint32_t*>(s.hist), s.bc);
+  *thr = max(*thr, t);
+}
 
-// top-k and top-p of the keys >= thr that feed gives (with any others below),
-// then their sum.
+// top-k and top-p of the keys >= thr that feed gives, then their sum.
 template <typename ET, int NTHR, class Feed>
 __device__ __forceinline__ void mp_filter(Feed feed, const MinpMode& mm, uint32_t kmax, double invT, MinpScratch& s, MinpRow& r) {
-  constexpr int LEVELS = Key<ET>::LEVELS;
   const double z0 = (double)r.zmax;
   const auto weight = [&](uint32_t key) { return mp_exp(((double)Key<ET>::value(key) - z0) * invT); };
-  if (mm.k) {
-    __syncthreads();
-    const uint32_t t = block_kth_largest<LEVELS, NTHR>(
-        [&](auto fn) { feed([&](uint32_t key) { fn(key >= r.thr ? key : 0u); }); }, (uint32_t)mm.k,
-        reinterpret_cast<uint32_t*>(s.hist), s.bc);
-    r.thr = max(r.thr, t);
-  }
+  mp_top_k<ET, NTHR>(feed, mm, s, &r.thr);
   const auto total = [&]() {
     double x = 0.0;
     feed([&](uint32_t key) {
@@ -453,12 +462,13 @@ __device__ __forceinline__ void mp_filter(Feed feed, const MinpMode& mm, uint32_
   };
   double S = total();
   if (mm.m.tp < 1.0f) {
-    const uint32_t t = mm.m.tp <= 0.0f ? kmax
-                                       : mp_nucleus<LEVELS, NTHR>([&](auto fn) {
-                                           feed([&](uint32_t key) {
-                                             if (key >= r.thr) fn(key, weight(key));
-                                           });
-                                         }, (double)mm.m.tp * S * (double)(1ull << MP_FIX), s);
+    uint32_t t = kmax;
+    if (mm.m.tp > 0.0f)
+      t = mp_nucleus<Key<ET>::LEVELS, NTHR>([&](auto fn) {
+        feed([&](uint32_t key) {
+          if (key >= r.thr) fn(key, weight(key));
+        });
+      }, 0ull, (double)mm.m.tp * S * (double)(1ull << MP_FIX), s);
     if (t > r.thr) {
       r.thr = t;
       S = total();
@@ -468,104 +478,250 @@ __device__ __forceinline__ void mp_filter(Feed feed, const MinpMode& mm, uint32_
 }
 
 // ---------------------------------------------------------------------------
-// One position from the logits.
+// One position from the logits.  `few` holds `cap` keys.
 // ---------------------------------------------------------------------------
-template <typename ET, int NTHR, class F>
-__device__ __forceinline__ void mp_for_row(const ET* row, int V, F fn) {
-  constexpr int VEC = Key<ET>::VEC, PER = 4 / sizeof(ET);
-  for (int e = (int)threadIdx.x * VEC; e < V; e += NTHR * VEC) {
-    const u32x4 raw = mp_load(row, e, V);
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      const uint32_t bits = sizeof(ET) == 2 ? (raw[i / PER] >> (16 * (i % PER))) & 0xFFFFu : raw[i / PER];
-      if (e + i < V) fn(Key<ET>::of_bits(bits), e + i);
+template <typename ET>
+__device__ __forceinline__ uint32_t mp_key_of(const u32x4& raw, int i) {   // of value i of a unit
+  return Key<ET>::of_bits(sizeof(ET) == 2 ? (raw[i / 2] >> (16 * (i % 2))) & 0xFFFFu : raw[i]);
+}
+
+// fn(key, index) for a unit's values, a word at a time: 16 wavefronts hide what
+// one copy of fn's code waits for, and eight copies neither fit the registers nor
+// the instruction cache.
+template <typename ET, class F>
+__device__ __forceinline__ void mp_for_words(u32x4 raw, int e, F fn) {
+#pragma unroll 1
+  for (int w = 0; w < 4; ++w) {
+    const uint32_t x = raw.x;
+    raw = u32x4{raw.y, raw.z, raw.w, x};
+    if (sizeof(ET) == 2) {
+      fn(Key<ET>::of_bits(x & 0xFFFFu), e + 2 * w);
+      fn(Key<ET>::of_bits(x >> 16), e + 2 * w + 1);
+    } else {
+      fn(Key<ET>::of_bits(x), e + w);
     }
   }
 }
 
+// fn(16 bytes, first element) for units `step` elements apart from e on, -inf
+// behind the row's end; the next one is under way meanwhile.
+template <typename ET, class F>
+__device__ __forceinline__ void mp_for_units(const ET* row, int e, int end, int step, int V, F fn) {
+  u32x4 next = {0, 0, 0, 0};
+  if (e < end) next = mp_load(row, e, V);
+#pragma unroll 1
+  for (; e < end; e += step) {
+    const u32x4 raw = next;
+    if (e + step < end) next = mp_load(row, e + step, V);
+    fn(raw, e);
+  }
+}
+
+template <typename ET, int NTHR, class F>
+__device__ __forceinline__ void mp_for_row(const ET* row, int V, F fn) {
+  constexpr int VEC = Key<ET>::VEC;
+  mp_for_units(row, (int)threadIdx.x * VEC, V, NTHR * VEC, V, [&](const u32x4& raw, int e) { mp_for_words<ET>(raw, e, fn); });
+}
+
+// A row's distribution; false: it has no valid one.  Passes over the row: its
+// maximum; the sum, with the masses by bins of the value; the keys of the bin in
+// which the nucleus ends; the sum of what is kept.
 template <typename ET, int NTHR>
-__device__ __forceinline__ PosRec mp_position_from_rows(const MinpArgs& ma, const MinpMode& mm, int b, int i, MinpScratch& s) {
+__device__ __forceinline__ bool mp_row_stats(const ET* row, int V, const MinpMode& mm, MinpScratch& s, uint32_t* few, int cap, MinpRow* out) {
+  constexpr int VEC = Key<ET>::VEC;
+  const double invT = 1.0 / (double)mm.m.T;
+  uint32_t kmax = 0, bad = 0;
+  mp_for_units(row, (int)threadIdx.x * VEC, V, NTHR * VEC, V, [&](const u32x4& raw, int) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      const uint32_t key = mp_key_of<ET>(raw, i);
+      kmax = max(kmax, key);
+      bad |= key_valid<ET>(key) ? 0u : 1u;
+    }
+  });
+  kmax = mp_reduce_u32<NTHR>(kmax, 0u, s.red_u, [](uint32_t x, uint32_t y) { return x > y ? x : y; });
+  bad = mp_reduce_u32<NTHR>(bad, 0u, s.red_u, [](uint32_t x, uint32_t y) { return x | y; });
+  if (bad || kmax <= Key<ET>::NEG_INF) return false;
+  const float zmax = Key<ET>::value(kmax);
+  const double z0 = (double)zmax;
+  uint32_t thr = mm.mp > 0.0f ? min(mp_key_from<ET>(z0 + mm.cut), kmax) : Key<ET>::NEG_INF + 1;
+  const auto keys = [&](auto fn) { mp_for_row<ET, NTHR>(row, V, [&](uint32_t key, int) { fn(key); }); };
+  const auto exponent = [&](uint32_t key) { return ((double)Key<ET>::value(key) - z0) * invT; };
+  mp_top_k<ET, NTHR>(keys, mm, s, &thr);
+  const bool nucleus = mm.m.tp < 1.0f && mm.m.tp > 0.0f;
+  const auto bin = [](double x) { return (uint32_t)fmin(-8.0 * x, (double)(MP_BINS - 1)); };
+  __syncthreads();
+  for (int i = threadIdx.x; i < MP_BINS; i += NTHR) s.hist[i] = 0ull;
+  __syncthreads();
+  double sum = 0.0;
+  if (mm.m.tp < 1.0f && !nucleus) thr = kmax;   // top_p <= 0
+  keys([&](uint32_t key) {
+    if (key >= thr) {
+      const double x = exponent(key), e = mp_exp(x);
+      sum += e;
+      if (nucleus) atomicAdd(&s.hist[bin(x)], mp_fixed(e));
+    }
+  });
+  double S = mp_sum<NTHR>(sum, s.red);   // (the bins are complete)
+  if (nucleus) {
+    const double tau = (double)mm.m.tp * S * (double)(1ull << MP_FIX);
+    if (threadIdx.x < 64) {
+      constexpr int PER = MP_BINS / 64;
+      unsigned long long c = 0;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) c += s.hist[threadIdx.x * PER + i];
+      unsigned long long incl = c;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const unsigned long long u = shfl_up_u64(incl, o);
+        if ((int)threadIdx.x >= o) incl += u;
+      }
+      const unsigned long long reach = __ballot((double)incl >= tau);
+      if (reach == 0ull) {
+        if (threadIdx.x == 0) s.bc[4] = NONE;
+      } else if ((int)threadIdx.x == __ffsll((long long)reach) - 1) {
+        unsigned long long run = incl - c;
+        int i = 0;
+        while (i < PER - 1 && (double)(run + s.hist[threadIdx.x * PER + i]) < tau) run += s.hist[threadIdx.x * PER + i++];
+        s.bc[4] = threadIdx.x * PER + i;
+        s.bc[5] = (uint32_t)run;
+        s.bc[6] = (uint32_t)(run >> 32);
+      }
+      if (threadIdx.x == 0) s.bc[3] = 0;
+    }
+    __syncthreads();
+    const uint32_t cross = s.bc[4];
+    const unsigned long long above = ((unsigned long long)s.bc[6] << 32) | s.bc[5];
+    if (cross != NONE) {   // (else rounding: everything is kept)
+      const auto of_bin = [&](uint32_t key) { return key >= thr && bin(exponent(key)) == cross; };
+      keys([&](uint32_t key) {
+        if (of_bin(key)) {
+          const uint32_t at = atomicAdd(&s.bc[3], 1u);
+          if (at < (uint32_t)cap) few[at] = key;   // in any order: their masses are whole numbers
+        }
+      });
+      __syncthreads();
+      const uint32_t found = s.bc[3];
+      uint32_t t;
+      if (found <= (uint32_t)cap) {
+        t = mp_nucleus<Key<ET>::LEVELS, NTHR>([&](auto fn) {
+          for (uint32_t j = threadIdx.x; j < found; j += NTHR) fn(few[j], mp_exp(exponent(few[j])));
+        }, above, tau, s);
+      } else {
+        t = mp_nucleus<Key<ET>::LEVELS, NTHR>([&](auto fn) {
+          keys([&](uint32_t key) {
+            if (of_bin(key)) fn(key, mp_exp(exponent(key)));
+          });
+        }, above, tau, s);
+      }
+      if (t > thr) {
+        thr = t;
+        sum = 0.0;
+        keys([&](uint32_t key) {
+          if (key >= thr) sum += mp_exp(exponent(key));
+        });
+        S = mp_sum<NTHR>(sum, s.red);
+      }
+    }
+  }
+  out->thr = thr;
+  out->zmax = zmax;
+  out->invS = 1.0 / S;
+  return true;
+}
+
+// The position's record from its two rows' distributions (the second is used
+// where the position has a draft).
+template <typename ET, int NTHR>
+__device__ __forceinline__ PosRec mp_position_from_rows(const MinpArgs& ma, const MinpMode& mm, int b, int i, const MinpRow& r0,
+                                                        const MinpRow& r1, MinpScratch& s) {
   const Args& a = ma.a;
   const int V = a.V;
   const bool two = i < mm.m.g;
   PosRec rec{0.0, 0.0, 0.0, -1, 0u};
   const double invT = 1.0 / (double)mm.m.T;
-  const ET* row[2] = {row_ptr<ET>(a, b, true, i), two ? row_ptr<ET>(a, b, false, i) : nullptr};
-  MinpRow r[2];
-  r[1].thr = 0xFFFFFFFFu;
-  r[1].zmax = 0.0f;
-  r[1].invS = 0.0;
-  for (int h = 0; h < (two ? 2 : 1); ++h) {
-    uint32_t kmax = 0, bad = 0;
-    mp_for_row<ET, NTHR>(row[h], V, [&](uint32_t key, int) {
-      kmax = max(kmax, key);
-      bad |= key_valid<ET>(key) ? 0u : 1u;
-    });
-    kmax = mp_reduce_u32<NTHR>(kmax, 0u, s.red_u, [](uint32_t x, uint32_t y) { return x > y ? x : y; });
-    bad = mp_reduce_u32<NTHR>(bad, 0u, s.red_u, [](uint32_t x, uint32_t y) { return x | y; });
-    if (bad || kmax <= Key<ET>::NEG_INF) {
-      rec.bad = 1u;
-      return rec;
-    }
-    r[h].zmax = Key<ET>::value(kmax);
-    r[h].thr = mm.mp > 0.0f ? min(mp_key_from<ET>((double)r[h].zmax + (double)mm.m.T * log((double)mm.mp)), kmax) : Key<ET>::NEG_INF + 1;
-    mp_filter<ET, NTHR>([&](auto fn) { mp_for_row<ET, NTHR>(row[h], V, [&](uint32_t key, int) { fn(key); }); }, mm, kmax, invT, s, r[h]);
-  }
+  const ET* row[2] = {row_ptr<ET>(a, b, true, i), row_ptr<ET>(a, b, !two, i)};
+  const MinpRow r[2] = {r0, two ? r1 : MinpRow{0xFFFFFFFFu, 0.0f, 0.0}};
   const auto prob = [&](int h, uint32_t key) {
     return key >= r[h].thr ? mp_exp(((double)Key<ET>::value(key) - (double)r[h].zmax) * invT) * r[h].invS : 0.0;
   };
-  double al = 0.0, z = 0.0;
-  mp_for_row<ET, NTHR>(row[0], V, [&](uint32_t key, int v) {
-    const double p = prob(0, key);
-    if (p > 0.0) {
-      const double q = two ? prob(1, Key<ET>::load_key(row[1], v)) : 0.0;
-      al += fmin(p, q);
-      z += fmax(p - q, 0.0);
-    }
-  });
-  rec.alpha = mp_sum<NTHR>(al, s.red);
-  double Z = mp_sum<NTHR>(z, s.red);
+  // A wavefront's run of consecutive ids: the draw then looks for its token in
+  // one run.
+  constexpr int NW = NTHR / 64, PER = Key<ET>::VEC;
+  const int run = ((V + NW - 1) / NW + PER - 1) / PER * PER, wave = (int)threadIdx.x >> 6, lane = (int)threadIdx.x & 63;
+  const int v1 = min(V, (wave + 1) * run);
   bool resid = two;
-  if (!(Z > 0.0)) {   // no residual is left: draw from p
-    resid = false;
+  double al = 0.0, z = 0.0;
+  const auto weight = [&](uint32_t kp, uint32_t kq, double* overlap) {
+    const double p = prob(0, kp);
+    if (!(p > 0.0) || !resid) return p;
+    const double q = prob(1, kq);
+    *overlap += fmin(p, q);
+    return fmax(p - q, 0.0);
+  };
+  // fn(key of the target's row, of the draft's, id) for the unit at id v.
+  const auto both = [&](const u32x4& raw, int v, auto fn) {
+    u32x4 other = two ? mp_load(row[1], v, V) : raw;
+    mp_for_words<ET>(raw, v, [&](uint32_t key, int id) {
+      fn(key, mp_key_of<ET>(other, sizeof(ET) == 2 ? (id - v) & 1 : 0), id);
+      if (sizeof(ET) == 4 || ((id - v) & 1)) other = u32x4{other.y, other.z, other.w, other.x};
+    });
+  };
+  const auto sums = [&]() {   // of the runs, in s.red; their total
     z = 0.0;
-    mp_for_row<ET, NTHR>(row[0], V, [&](uint32_t key, int) { z += prob(0, key); });
-    Z = mp_sum<NTHR>(z, s.red);
+    mp_for_units(row[0], wave * run + lane * PER, v1, 64 * PER, V, [&](const u32x4& raw, int e) {
+      both(raw, e, [&](uint32_t kp, uint32_t kq, int) { z += weight(kp, kq, &al); });   // (runs end with a unit or the row)
+    });
+    return mp_sum<NTHR>(z, s.red);
+  };
+  double Z = sums();
+  if (two && !(Z > 0.0)) {   // no residual is left: draw from p
+    resid = false;
+    Z = sums();
   }
+  // min{v : C(v) > u Z}: first the run, then a tile of ids at a time; else the
+  // last weight above 0.
+  const double target = (double)a.u[(size_t)b * (a.G + 1) + a.G] * Z;
+  double base = 0.0;
+  int t0 = 0;
+  for (int w = 0; w + 1 < NW && !(base + s.red[w] > target); ++w) {
+    base += s.red[w];
+    t0 += run;
+  }
+  rec.alpha = mp_sum<NTHR>(al, s.red);
   const int x = two ? a.draft[(size_t)b * a.G + i] : -1;
   if (x >= 0 && x < V) {
     rec.px = prob(0, Key<ET>::load_key(row[0], x));
     rec.qx = prob(1, Key<ET>::load_key(row[1], x));
   }
-  // min{v : C(v) > u Z}, a tile of ids at a time; else the last weight above 0.
-  const double target = (double)a.u[(size_t)b * (a.G + 1) + a.G] * Z;
-  constexpr int PER = Key<ET>::VEC;
-  double base = 0.0;
   uint32_t last = 0, hit = NONE;
-  for (int t0 = 0; t0 < V && hit == NONE; t0 += NTHR * PER) {
-    const int v0 = t0 + (int)threadIdx.x * PER;
-    double w[PER], loc = 0.0, tot;
-#pragma unroll
-    for (int e = 0; e < PER; ++e) {
-      w[e] = 0.0;
-      if (v0 + e < V) {
-        const double p = prob(0, Key<ET>::load_key(row[0], v0 + e));
-        if (p > 0.0) w[e] = resid ? fmax(p - prob(1, Key<ET>::load_key(row[1], v0 + e)), 0.0) : p;
-      }
-      loc += w[e];
-      if (w[e] > 0.0) last = (uint32_t)(v0 + e + 1);
+  for (int again = 0; again < 2; ++again) {
+    for (; t0 < V && hit == NONE; t0 += NTHR * PER) {
+      const int v0 = t0 + (int)threadIdx.x * PER;
+      double loc = 0.0, tot, none = 0.0;
+      u32x4 raw = {0, 0, 0, 0};
+      if (v0 < V) raw = mp_load(row[0], v0, V);
+      const bool some = v0 < V;
+      if (some) both(raw, v0, [&](uint32_t kp, uint32_t kq, int v) {
+        const double w = weight(kp, kq, &none);
+        loc += w;
+        if (w > 0.0) last = (uint32_t)(v + 1);
+      });
+      double c = base + mp_scan<NTHR>(loc, s.red, &tot);
+      uint32_t mine = NONE;
+      if (some && c + loc > target) both(raw, v0, [&](uint32_t kp, uint32_t kq, int v) {
+        const double w = weight(kp, kq, &none);
+        c += w;
+        if (mine == NONE && w > 0.0 && c > target) mine = (uint32_t)v;
+      });
+      hit = mp_reduce_u32<NTHR>(mine, NONE, s.red_u, [](uint32_t p, uint32_t q) { return p < q ? p : q; });
+      base += tot;
     }
-    double c = base + mp_scan<NTHR>(loc, s.red, &tot);
-    uint32_t mine = NONE;
-#pragma unroll
-    for (int e = 0; e < PER; ++e) {
-      c += w[e];
-      if (mine == NONE && w[e] > 0.0 && c > target) mine = (uint32_t)(v0 + e);
-    }
-    hit = mp_reduce_u32<NTHR>(mine, NONE, s.red_u, [](uint32_t p, uint32_t q) { return p < q ? p : q; });
-    base += tot;
+    last = mp_reduce_u32<NTHR>(last, 0u, s.red_u, [](uint32_t p, uint32_t q) { return p > q ? p : q; });
+    if (hit != NONE || last != 0) break;
+    t0 = 0;   // no weight from that run on: from the first id
+    base = 0.0;
   }
-  last = mp_reduce_u32<NTHR>(last, 0u, s.red_u, [](uint32_t p, uint32_t q) { return p > q ? p : q; });
   rec.tok = hit != NONE ? (int)hit : (int)last - 1;
   if (ma.a.sampler) rec.px = prob(0, Key<ET>::load_key(row[0], rec.tok));
   return rec;
@@ -584,15 +740,37 @@ __device__ __forceinline__ void mp_put(const MinpArgs& ma, int b, int i, const P
   if (ma.out_prob) ma.out_prob[b] = ok ? (float)rec.px : __int_as_float(0x7FC00000);
 }
 
-// The positions that the position kernel left.
+// The positions that the position kernel left, in two launches: the distributions
+// of their rows, one workgroup a row, then the positions.
 template <typename ET>
 __global__ __launch_bounds__(MP_ROW_NT) void minp_row_kernel(MinpArgs ma) {
   __shared__ MinpScratch s;
-  const uint32_t n = ma.a.dense_count[0];
+  __shared__ uint32_t few[MP_FEW_KEYS];
+  const Args& a = ma.a;
+  const uint32_t n = 2 * a.dense_count[0];
   for (uint32_t j = blockIdx.x; j < n; j += gridDim.x) {
-    const int id = ma.a.dense_list[j], b = id / (ma.a.G + 1), i = id % (ma.a.G + 1);
+    const int id = a.dense_list[j / 2], b = id / (a.G + 1), i = id % (a.G + 1), h = (int)(j & 1);
     const MinpMode mm = minp_mode(ma, b);
-    const PosRec rec = mp_position_from_rows<ET, MP_ROW_NT>(ma, mm, b, i, s);
+    if (h && i >= mm.m.g) continue;
+    MinpRow r;
+    const bool ok = mp_row_stats<ET, MP_ROW_NT>(row_ptr<ET>(a, b, !h, i), a.V, mm, s, few, MP_FEW_KEYS, &r);
+    if (!ok) r.thr = 0;   // no key
+    if (threadIdx.x == 0) ma.rows[2 * (size_t)id + h] = r;
+    __syncthreads();
+  }
+}
+
+template <typename ET>
+__global__ __launch_bounds__(MP_ROW_NT) void minp_row_position_kernel(MinpArgs ma) {
+  __shared__ MinpScratch s;
+  const Args& a = ma.a;
+  const uint32_t n = a.dense_count[0];
+  for (uint32_t j = blockIdx.x; j < n; j += gridDim.x) {
+    const int id = a.dense_list[j], b = id / (a.G + 1), i = id % (a.G + 1);
+    const MinpMode mm = minp_mode(ma, b);
+    const MinpRow r0 = ma.rows[2 * (size_t)id], r1 = i < mm.m.g ? ma.rows[2 * (size_t)id + 1] : r0;
+    PosRec rec{0.0, 0.0, 0.0, -1, 1u};
+    if (r0.thr && r1.thr) rec = mp_position_from_rows<ET, MP_ROW_NT>(ma, mm, b, i, r0, r1, s);
     if (threadIdx.x == 0) mp_put(ma, b, i, rec);
     __syncthreads();
   }
@@ -628,7 +806,7 @@ __device__ __forceinline__ int mp_gather(const MinpArgs& ma, const MinpMode& mm,
   if ((flags & MP_BAD) || kmax <= Key<ET>::NEG_INF) return MP_IS_BAD;
   if (flags & MP_OVER) return MP_TOO_LONG;
   r.zmax = Key<ET>::value(kmax);
-  r.thr = mm.kind == MP_GREEDY ? kmax : min(mp_key_from<ET>((double)r.zmax + (double)mm.m.T * log((double)mm.mp)), kmax);
+  r.thr = mm.kind == MP_GREEDY ? kmax : min(mp_key_from<ET>((double)r.zmax + mm.cut), kmax);
   *kmax_out = kmax;
   int have = 0;
   for (int p0 = 0; p0 < NP; p0 += MP_NT) {   // MP_NT parts at a time
@@ -712,7 +890,14 @@ __global__ __launch_bounds__(MP_NT) void minp_position_kernel(MinpArgs ma) {
     how = mp_gather<ET>(ma, mm, (long long)b * a.RS + (h ? a.G + 1 + i : i), h, s, &n[h], r[h], &kmax[h]);
   if (how == MP_TOO_LONG) {
     if constexpr (ROWS) {
-      rec = mp_position_from_rows<ET, MP_NT>(ma, mm, b, i, s.s);
+      uint32_t* few = &s.key[0][0];   // key and id
+      bool ok = mp_row_stats<ET, MP_NT>(row_ptr<ET>(a, b, true, i), a.V, mm, s.s, few, 4 * MP_CAP, &r[0]);
+      __syncthreads();
+      r[1] = r[0];
+      if (ok && two) ok = mp_row_stats<ET, MP_NT>(row_ptr<ET>(a, b, false, i), a.V, mm, s.s, few, 4 * MP_CAP, &r[1]);
+      __syncthreads();
+      rec.bad = 1u;
+      if (ok) rec = mp_position_from_rows<ET, MP_NT>(ma, mm, b, i, r[0], r[1], s.s);
       if (tid == 0) mp_put(ma, b, i, rec);
     } else if (tid == 0) {
       a.dense_list[atomicAdd(&a.dense_count[0], 1u)] = (int)blockIdx.x;
@@ -729,9 +914,10 @@ __global__ __launch_bounds__(MP_NT) void minp_position_kernel(MinpArgs ma) {
     if (mm.kind == MP_GREEDY) {
       r[h].invS = 1.0;
     } else {
-      mp_filter<ET, MP_NT>([&](auto fn) {
+      const auto keys = [&](auto fn) {
         for (int j = tid; j < n[h]; j += MP_NT) fn(s.key[h][j]);
-      }, mm, kmax[h], invT, s.s, r[h]);
+      };
+      mp_filter<ET, MP_NT>(keys, mm, kmax[h], invT, s.s, r[h]);
     }
     for (int j = tid; j < n[h]; j += MP_NT) {
       const uint32_t key = s.key[h][j];
