@@ -971,7 +971,8 @@ static MinpPlan minp_plan(int B, int G, int V, int dtype) {
   MinpPlan p;
   const int vec = dtype == SV_BF16 ? 8 : 4;
   const size_t rows = (size_t)B * (2 * G + 1), np = (size_t)B * (G + 1);
-  const auto parts = [&](int vpl) { return (V + MP_NT * vpl * vec - 1) / (MP_NT * vpl * vec); };
+  // (a row may begin up to a unit behind the first part's start)
+  const auto parts = [&](int vpl) { return (V + vec - 1 + MP_NT * vpl * vec - 1) / (MP_NT * vpl * vec); };
   p.vpl = (long long)rows * parts(8) < MP_FEW ? 2 : 8;
   p.NP = parts(p.vpl);
   p.PL = MP_NT * p.vpl * vec;
@@ -996,23 +997,21 @@ static size_t minp_bytes(int B, int G, int V, int dtype) {
 template <typename ET>
 static hipError_t launch_minp(const MinpArgs& ma, const MinpPlan& p, int hints, hipStream_t st) {
   const Args& a = ma.a;
-  const dim3 units((unsigned)((long long)a.B * a.RS * a.NP)), positions((unsigned)((long long)a.B * (a.G + 1)));
+  const dim3 units((unsigned)((long long)a.B * a.RS * a.NP)), groups((unsigned)(a.sampler ? (a.B + MP_POS_WAVES - 1) / MP_POS_WAVES : a.B));
   hipError_t e;
   if (p.vpl == 8) hipLaunchKernelGGL((minp_cut_kernel<ET, 8>), units, dim3(MP_NT), 0, st, ma);
   else hipLaunchKernelGGL((minp_cut_kernel<ET, 2>), units, dim3(MP_NT), 0, st, ma);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   if (hints & SV_HINT_ALL_MIN_P) {
-    hipLaunchKernelGGL((minp_position_kernel<ET, true>), positions, dim3(MP_NT), 0, st, ma);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-  } else {
-    hipLaunchKernelGGL((minp_position_kernel<ET, false>), positions, dim3(MP_NT), 0, st, ma);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    hipLaunchKernelGGL((minp_row_kernel<ET>), dim3(MP_ROW_GRID), dim3(MP_ROW_NT), 0, st, ma);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    hipLaunchKernelGGL((minp_row_position_kernel<ET>), dim3(MP_ROW_GRID), dim3(MP_ROW_NT), 0, st, ma);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+    hipLaunchKernelGGL((minp_position_kernel<ET, true>), groups, dim3(MP_POS_NT), 0, st, ma);
+    return hipGetLastError();
   }
-  if (a.sampler) return hipSuccess;
+  hipLaunchKernelGGL((minp_position_kernel<ET, false>), groups, dim3(MP_POS_NT), 0, st, ma);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  hipLaunchKernelGGL((minp_row_kernel<ET>), dim3(MP_ROW_GRID), dim3(MP_ROW_NT), 0, st, ma);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  hipLaunchKernelGGL((minp_row_position_kernel<ET>), dim3(MP_ROW_GRID), dim3(MP_ROW_NT), 0, st, ma);
+  if ((e = hipGetLastError()) != hipSuccess || a.sampler) return e;
   constexpr int per = MP_FIN_NT / 64;
   hipLaunchKernelGGL(minp_finish_kernel, dim3((unsigned)((a.B + per - 1) / per)), dim3(MP_FIN_NT), 0, st, ma);
   return hipGetLastError();
@@ -1056,10 +1055,10 @@ static int run_minp(const void* p_logits, const void* q_logits, int dtype, const
   a.out_alpha = out_alpha;
   a.out_pq = out_pq;
   a.dense_count = reinterpret_cast<uint32_t*>(ws);
-  a.seq_flags = reinterpret_cast<uint32_t*>(ws + p.flags_off);
   a.pos = reinterpret_cast<PosRec*>(ws + p.pos_off);
   a.dense_list = reinterpret_cast<int32_t*>(ws + p.redo_off);
   ma.min_p = min_p;
+  ma.left = reinterpret_cast<uint32_t*>(ws + p.flags_off);
   ma.rows = reinterpret_cast<MinpRow*>(ws + p.rows_off);
   ma.part_max = reinterpret_cast<uint32_t*>(ws + p.max_off);
   ma.part_count = reinterpret_cast<uint32_t*>(ws + p.count_off);

@@ -8,14 +8,14 @@
 //   minp_cut_kernel       one workgroup per (logit row, row part): the part is
 //                         read once, into registers; its maximum and the
 //                         values that may be kept go to the workspace
-//   minp_position_kernel  one workgroup per (sequence, position): the kept
-//                         values of the position's target and draft row,
-//                         gathered in LDS, give p(x), q(x), the overlap and the
-//                         draw as if the first rejection were there
-//   minp_row_kernel, minp_row_position_kernel
+//   minp_position_kernel  one workgroup per sequence, one wavefront per position:
+//                         the kept values of the position's target and draft
+//                         row, gathered in LDS, give p(x), q(x), the overlap
+//                         and the draw as if the first rejection were there;
+//                         then the acceptance
+//   minp_row_kernel, minp_row_position_kernel, minp_finish_kernel
 //                         the same from the logits, for rows without min-p and
 //                         rows that keep more than the lists hold
-//   minp_finish_kernel    one wavefront per sequence: acceptance and outputs
 //
 // Probabilities, normalisers and nucleus masses are held in 64 bits (the masses
 // as fixed-point numbers, whose sum does not depend on its order), so that a
@@ -23,18 +23,19 @@
 #pragma once
 
 #include "sv_common.h"
-#include "sv_finish.h"
+#include "sv_finish.h"   // shfl_up_u64
 
 namespace sv {
 
-constexpr int MP_NT = 256;        // threads of a cut or position workgroup
+constexpr int MP_NT = 256;        // threads of a cut workgroup
 constexpr int MP_WAVES = MP_NT / 64;
+constexpr int MP_POS_NT = 512;    // threads of a position workgroup
+constexpr int MP_POS_WAVES = MP_POS_NT / 64;
 constexpr int MP_PART_CAP = 512;  // list entries of a row part
-constexpr int MP_CAP = 1024;      // kept values of a row that the position kernel holds
 constexpr int MP_ROW_NT = 1024;   // threads of a row workgroup
 constexpr int MP_ROW_GRID = 512;
 constexpr int MP_FEW_KEYS = 8192; // keys of one bin that a row workgroup holds
-constexpr int MP_BINS = 512;      // bins of a row's masses, 1/8 wide in (zmax - z) / T; at least 256
+constexpr int MP_BINS = 256;      // bins of a row's masses, 1/8 wide in (zmax - z) / T; also a digit's
 constexpr int MP_FIX = 42;        // fraction bits of a mass: at most 2^20 masses of at most 1
 
 // Flags in a part's count.
@@ -56,6 +57,7 @@ struct MinpArgs {
   uint32_t* part_count;   // [rows][NP] entries, or flags
   void* part_list;        // [rows][NP][MP_PART_CAP] MinpEntry
   float* out_prob;        // sampler: [R] or null
+  uint32_t* left;         // [B] 1: the row kernels finish the sequence
   MinpRow* rows;          // [B * (G + 1)][2] distributions of the positions left to the row kernels
 };
 
@@ -145,26 +147,30 @@ __device__ __forceinline__ double mp_exp(double x) {
 // The cut: one workgroup per (row, part).
 // ---------------------------------------------------------------------------
 
-// The 16 bytes of a row from element e on; -inf behind its end.
+// Elements that a row begins behind a 16-byte boundary.
+template <typename ET>
+__device__ __forceinline__ int mp_lead(const ET* row) { return (int)((uintptr_t)row % 16 / sizeof(ET)); }
+
+// The 16 bytes of a row from element e on; -inf before it and behind its end.
 __device__ __forceinline__ u32x4 mp_load(const uint16_t* row, int e, int V) {
   u32x4 v = {0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u};
-  if (e + 8 <= V) {
+  if (e >= 0 && e + 8 <= V) {
     __builtin_memcpy(&v, row + e, 16);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (e + i < V) v[i / 2] = i & 1 ? (v[i / 2] & 0xFFFFu) | (uint32_t)row[e + i] << 16 : (v[i / 2] & 0xFFFF0000u) | row[e + i];
+      if (e + i >= 0 && e + i < V) v[i / 2] = i & 1 ? (v[i / 2] & 0xFFFFu) | (uint32_t)row[e + i] << 16 : (v[i / 2] & 0xFFFF0000u) | row[e + i];
   }
   return v;
 }
 __device__ __forceinline__ u32x4 mp_load(const float* row, int e, int V) {
   u32x4 v = {0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u};
-  if (e + 4 <= V) {
+  if (e >= 0 && e + 4 <= V) {
     __builtin_memcpy(&v, row + e, 16);
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (e + i < V) v[i] = __float_as_uint(row[e + i]);
+      if (e + i >= 0 && e + i < V) v[i] = __float_as_uint(row[e + i]);
   }
   return v;
 }
@@ -234,10 +240,16 @@ __global__ __launch_bounds__(MP_NT) void minp_cut_kernel(MinpArgs ma) {
   if ((mm.kind != MP_LIST && mm.kind != MP_GREEDY) || pos > mm.m.g || (!isP && pos >= mm.m.g)) return;   // not used
   const ET* row = row_ptr<ET>(a, b, isP, pos);
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int e0 = part * a.PL, w0 = (wave * VPL * 64 + lane) * VEC;   // the lane's first value in the part
+  // Parts begin at a 16-byte boundary, the first one up to a unit before the row.
+  const int e0 = part * a.PL - mp_lead(row), w0 = (wave * VPL * 64 + lane) * VEC;   // the lane's first value in the part
   u32x4 raw[VPL];
+  if (e0 >= 0 && e0 + MP_NT * VPL * VEC <= a.V) {
 #pragma unroll
-  for (int j = 0; j < VPL; ++j) raw[j] = mp_load(row, e0 + w0 + j * 64 * VEC, a.V);
+    for (int j = 0; j < VPL; ++j) raw[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(row + e0 + w0 + j * 64 * VEC));
+  } else {
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) raw[j] = mp_load(row, e0 + w0 + j * 64 * VEC, a.V);
+  }
   T v[VPL][4], hi, lo;
 #pragma unroll
   for (int j = 0; j < VPL; ++j)
@@ -311,31 +323,44 @@ __global__ __launch_bounds__(MP_NT) void minp_cut_kernel(MinpArgs ma) {
 }
 
 // ---------------------------------------------------------------------------
-// Block-wide pieces for workgroups of NTHR threads; `red` is NTHR / 64 slots.
+// Pieces for a group of NTHR threads: a workgroup, or (64) one wavefront of it,
+// which needs no barrier.  `red` is NTHR / 64 slots.
 // ---------------------------------------------------------------------------
+template <int NTHR>
+__device__ __forceinline__ void mp_sync() {
+  if (NTHR == 64) wave_lds_sync();
+  else __syncthreads();
+}
+template <int NTHR> __device__ __forceinline__ int mp_tid() { return (int)threadIdx.x & (NTHR - 1); }
+
+// Every wavefront's value from its last lane, to all: fn(wavefront, value).
+template <int NTHR, typename T, class F>
+__device__ __forceinline__ void mp_gather_waves(T v, bool mine, T* red, F fn) {
+  __syncthreads();
+  if (mine) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < NTHR / 64; ++i) fn(i, red[i]);
+}
 template <int NTHR>
 __device__ __forceinline__ double mp_sum(double v, double* red) {
   v = wave_sum_dpp(v);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
+  if (NTHR == 64) return v;
   double r = 0.0;
-#pragma unroll
-  for (int i = 0; i < NTHR / 64; ++i) r += red[i];
+  mp_gather_waves<NTHR>(v, (threadIdx.x & 63) == 0, red, [&](int, double x) { r += x; });
   return r;
 }
 // The exclusive prefix of v in thread order, and the total.
 template <int NTHR>
 __device__ __forceinline__ double mp_scan(double v, double* red, double* total) {
   const double incl = wave_incl_scan_f64(v);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 63) red[threadIdx.x >> 6] = incl;
-  __syncthreads();
-  double base = 0.0, all = 0.0;
-#pragma unroll
-  for (int i = 0; i < NTHR / 64; ++i) {
-    if (i < (int)(threadIdx.x >> 6)) base += red[i];
-    all += red[i];
+  double base = 0.0, all = readlane_f64(incl, 63);
+  if (NTHR > 64) {
+    all = 0.0;
+    mp_gather_waves<NTHR>(incl, (threadIdx.x & 63) == 63, red, [&](int i, double x) {
+      if (i < (int)(threadIdx.x >> 6)) base += x;
+      all += x;
+    });
   }
   *total = all;
   return base + incl - v;
@@ -343,14 +368,13 @@ __device__ __forceinline__ double mp_scan(double v, double* red, double* total) 
 template <int NTHR>
 __device__ __forceinline__ uint32_t mp_scan_u32(uint32_t v, uint32_t* red, uint32_t* total) {
   const uint32_t incl = wave_incl_scan_dpp(v);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 63) red[threadIdx.x >> 6] = incl;
-  __syncthreads();
-  uint32_t base = 0, all = 0;
-#pragma unroll
-  for (int i = 0; i < NTHR / 64; ++i) {
-    if (i < (int)(threadIdx.x >> 6)) base += red[i];
-    all += red[i];
+  uint32_t base = 0, all = (uint32_t)__builtin_amdgcn_readlane((int)incl, 63);
+  if (NTHR > 64) {
+    all = 0;
+    mp_gather_waves<NTHR>(incl, (threadIdx.x & 63) == 63, red, [&](int i, uint32_t x) {
+      if (i < (int)(threadIdx.x >> 6)) base += x;
+      all += x;
+    });
   }
   *total = all;
   return base + incl - v;
@@ -358,12 +382,9 @@ __device__ __forceinline__ uint32_t mp_scan_u32(uint32_t v, uint32_t* red, uint3
 template <int NTHR, class Op>
 __device__ __forceinline__ uint32_t mp_reduce_u32(uint32_t v, uint32_t neutral, uint32_t* red, Op op) {
   v = wave_reduce_dpp_u32(v, neutral, op);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
+  if (NTHR == 64) return v;
   uint32_t r = neutral;
-#pragma unroll
-  for (int i = 0; i < NTHR / 64; ++i) r = op(r, red[i]);
+  mp_gather_waves<NTHR>(v, (threadIdx.x & 63) == 0, red, [&](int, uint32_t x) { r = op(r, x); });
   return r;
 }
 
@@ -384,15 +405,15 @@ __device__ __forceinline__ uint32_t mp_nucleus(Feed feed, unsigned long long abo
   uint32_t prefix = 0, pmask = 0;
   for (int lvl = 0; lvl < LEVELS; ++lvl) {
     const int shift = 8 * (LEVELS - 1 - lvl);
-    __syncthreads();
-    for (int i = threadIdx.x; i < 256; i += NTHR) s.hist[i] = 0ull;
-    __syncthreads();
+    mp_sync<NTHR>();
+    for (int i = mp_tid<NTHR>(); i < 256; i += NTHR) s.hist[i] = 0ull;
+    mp_sync<NTHR>();
     feed([&](uint32_t key, double e) {
       if ((key & pmask) == prefix) atomicAdd(&s.hist[(key >> shift) & 255u], mp_fixed(e));
     });
-    __syncthreads();
-    if (threadIdx.x < 64) {
-      const int lane = threadIdx.x, first = 255 - 4 * lane;   // four digits a lane, from the top
+    mp_sync<NTHR>();
+    if (mp_tid<NTHR>() < 64) {
+      const int lane = threadIdx.x & 63, first = 255 - 4 * lane;   // four digits a lane, from the top
       unsigned long long c[4], sum = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -426,7 +447,7 @@ __device__ __forceinline__ uint32_t mp_nucleus(Feed feed, unsigned long long abo
       }
       if (lane == 0 && hit < 0) s.bc[0] = NONE;
     }
-    __syncthreads();
+    mp_sync<NTHR>();
     const uint32_t d = s.bc[0];
     above = ((unsigned long long)s.bc[2] << 32) | s.bc[1];
     if (d == NONE) return 0;
@@ -440,10 +461,12 @@ __device__ __forceinline__ uint32_t mp_nucleus(Feed feed, unsigned long long abo
 template <typename ET, int NTHR, class Feed>
 __device__ __forceinline__ void mp_top_k(Feed feed, const MinpMode& mm, MinpScratch& s, uint32_t* thr) {
   if (!mm.k) return;
-  __syncthreads();
-  const uint32_t t = block_kth_largest<Key<ET>::LEVELS, NTHR>(
-      [&](auto fn) { feed([&](uint32_t key) { fn(key >= *thr ? key : 0u); }); }, (uint32_t)mm.k,
-      reinterpret_cast<uint32_t*>(s.hist), s.bc);
+  const auto some = [&](auto fn) { feed([&](uint32_t key) { fn(key >= *thr ? key : 0u); }); };
+  uint32_t* hist = reinterpret_cast<uint32_t*>(s.hist);
+  uint32_t t;
+  mp_sync<NTHR>();
+  if constexpr (NTHR == 64) t = wave_kth<Key<ET>::LEVELS>(some, (uint32_t)mm.k, hist);
+  else t = block_kth_largest<Key<ET>::LEVELS, NTHR>(some, (uint32_t)mm.k, hist, s.bc);
   *thr = max(*thr, t);
 }
 
@@ -727,13 +750,9 @@ __device__ __forceinline__ PosRec mp_position_from_rows(const MinpArgs& ma, cons
   return rec;
 }
 
-// What one thread does with a position's result: the record, or a sampled row's outputs.
-__device__ __forceinline__ void mp_put(const MinpArgs& ma, int b, int i, const PosRec& rec) {
+// A sampled row's outputs, by one thread.
+__device__ __forceinline__ void mp_put_sample(const MinpArgs& ma, int b, const PosRec& rec) {
   const Args& a = ma.a;
-  if (!a.sampler) {
-    a.pos[(size_t)b * (a.G + 1) + i] = rec;
-    return;
-  }
   const float u = a.u[b];
   const bool ok = rec.bad == 0u && u >= 0.0f && u < 1.0f;
   a.out_tokens[b] = ok ? rec.tok : -1;
@@ -771,52 +790,63 @@ __global__ __launch_bounds__(MP_ROW_NT) void minp_row_position_kernel(MinpArgs m
     const MinpRow r0 = ma.rows[2 * (size_t)id], r1 = i < mm.m.g ? ma.rows[2 * (size_t)id + 1] : r0;
     PosRec rec{0.0, 0.0, 0.0, -1, 1u};
     if (r0.thr && r1.thr) rec = mp_position_from_rows<ET, MP_ROW_NT>(ma, mm, b, i, r0, r1, s);
-    if (threadIdx.x == 0) mp_put(ma, b, i, rec);
+    if (threadIdx.x == 0) {
+      if (a.sampler) mp_put_sample(ma, b, rec);
+      else a.pos[id] = rec;
+    }
     __syncthreads();
   }
 }
 
 // ---------------------------------------------------------------------------
-// One position from the lists.
+// One position from the lists, by a wavefront or a workgroup; PER entries of a
+// row a thread.
 // ---------------------------------------------------------------------------
+template <int NTHR, int PER>
 struct MinpSmem {
+  static constexpr int CAP = NTHR * PER;
   MinpScratch s;
-  uint32_t key[2][MP_CAP], id[2][MP_CAP];
-  double w[2][MP_CAP];    // probabilities
-  uint32_t base[MP_NT];   // entries before each of some parts
+  uint32_t key[2][CAP], id[2][CAP];
+  double w[2][CAP];      // probabilities
+  uint32_t base[NTHR];   // entries before each of some parts
 };
+typedef MinpSmem<64, 3> MinpWave;
+typedef MinpSmem<MP_POS_NT, 2> MinpBlock;
 
 enum { MP_OK = 0, MP_IS_BAD = 1, MP_TOO_LONG = 2 };
 
 // The values of one row that min-p keeps, in ascending id, into key[h] and id[h].
-template <typename ET>
-__device__ __forceinline__ int mp_gather(const MinpArgs& ma, const MinpMode& mm, long long rowid, int h, MinpSmem& s, int* n,
-                                         MinpRow& r, uint32_t* kmax_out) {
+template <typename ET, int NTHR, int PER>
+__device__ __forceinline__ int mp_gather(const MinpArgs& ma, const MinpMode& mm, long long rowid, const ET* row, int h,
+                                         MinpSmem<NTHR, PER>& s, int* n, MinpRow& r, uint32_t* kmax_out) {
   typedef MinpEntry<ET> E;
-  const int NP = ma.a.NP, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  constexpr int CAP = NTHR * PER;
+  const int NP = ma.a.NP, tid = mp_tid<NTHR>(), lane = tid & 63;
   const uint32_t* pm = ma.part_max + rowid * NP;
   const uint32_t* pc = ma.part_count + rowid * NP;
   uint32_t kmax = 0, flags = 0;
-  for (int p = tid; p < NP; p += MP_NT) {
+  for (int p = tid; p < NP; p += NTHR) {
     kmax = max(kmax, pm[p]);
     flags |= pc[p] & (MP_BAD | MP_OVER);
   }
-  kmax = mp_reduce_u32<MP_NT>(kmax, 0u, s.s.red_u, [](uint32_t x, uint32_t y) { return x > y ? x : y; });
-  flags = mp_reduce_u32<MP_NT>(flags, 0u, s.s.red_u, [](uint32_t x, uint32_t y) { return x | y; });
+  kmax = mp_reduce_u32<NTHR>(kmax, 0u, s.s.red_u, [](uint32_t x, uint32_t y) { return x > y ? x : y; });
+  flags = mp_reduce_u32<NTHR>(flags, 0u, s.s.red_u, [](uint32_t x, uint32_t y) { return x | y; });
   if ((flags & MP_BAD) || kmax <= Key<ET>::NEG_INF) return MP_IS_BAD;
   if (flags & MP_OVER) return MP_TOO_LONG;
   r.zmax = Key<ET>::value(kmax);
   r.thr = mm.kind == MP_GREEDY ? kmax : min(mp_key_from<ET>((double)r.zmax + mm.cut), kmax);
   *kmax_out = kmax;
+  const int lead = mp_lead(row);
   int have = 0;
-  for (int p0 = 0; p0 < NP; p0 += MP_NT) {   // MP_NT parts at a time
+  for (int p0 = 0; p0 < NP; p0 += NTHR) {   // NTHR parts at a time
     uint32_t total;
-    const uint32_t c = p0 + tid < NP ? pc[p0 + tid] : 0u;
-    const uint32_t before = mp_scan_u32<MP_NT>(c, s.s.red_u, &total);
+    // A part whose maximum is not kept has nothing that is.
+    const uint32_t c = p0 + tid < NP && pm[p0 + tid] >= r.thr ? pc[p0 + tid] : 0u;
+    const uint32_t before = mp_scan_u32<NTHR>(c, s.s.red_u, &total);
     s.base[tid] = before;
-    __syncthreads();
-    const int np = min(NP - p0, MP_NT);
-    for (uint32_t i0 = 0; i0 < total; i0 += MP_NT) {
+    mp_sync<NTHR>();
+    const int np = min(NP - p0, NTHR);
+    for (uint32_t i0 = 0; i0 < total; i0 += NTHR) {
       const uint32_t i = i0 + (uint32_t)tid;
       uint32_t key = 0, id = 0;
       if (i < total) {
@@ -828,122 +858,88 @@ __device__ __forceinline__ int mp_gather(const MinpArgs& ma, const MinpMode& mm,
         }
         const typename E::type e = reinterpret_cast<const typename E::type*>(ma.part_list)[((size_t)rowid * NP + p0 + lo) * MP_PART_CAP + (i - s.base[lo])];
         key = Key<ET>::of_bits(E::bits(e));
-        id = (uint32_t)((p0 + lo) * ma.a.PL) + E::index(e);
+        id = (uint32_t)((p0 + lo) * ma.a.PL - lead) + E::index(e);
       }
-      const bool keep = key >= r.thr;
-      const unsigned long long mask = __ballot(keep);
-      __syncthreads();
-      if (lane == 0) s.s.red_u[wave] = (uint32_t)__popcll(mask);
-      __syncthreads();
-      int at = have, all = 0;
-#pragma unroll
-      for (int q = 0; q < MP_WAVES; ++q) {
-        if (q < wave) at += (int)s.s.red_u[q];
-        all += (int)s.s.red_u[q];
-      }
-      at += __popcll(mask & ((1ull << lane) - 1));
-      if (keep && at < MP_CAP) {
+      uint32_t all;
+      const uint32_t keep = key >= r.thr ? 1u : 0u, at = (uint32_t)have + mp_scan_u32<NTHR>(keep, s.s.red_u, &all);
+      if (keep && at < (uint32_t)CAP) {
         s.key[h][at] = key;
         s.id[h][at] = id;
       }
-      have += all;
+      have += (int)all;
     }
-    __syncthreads();
+    mp_sync<NTHR>();
   }
   if (mm.kind == MP_GREEDY) have = 1;   // the lowest id
   *n = have;
-  return have > MP_CAP ? MP_TOO_LONG : MP_OK;
+  return have > CAP ? MP_TOO_LONG : MP_OK;
 }
 
-// q(v) by v's place among the ascending ids of row 1.
-__device__ __forceinline__ double mp_find(const MinpSmem& s, int n, uint32_t v) {
+// q(v) by v's place among the n ascending ids of row 1.
+__device__ __forceinline__ double mp_find(const uint32_t* id, const double* w, int n, uint32_t v) {
   int lo = 0, hi = n;
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
-    if (s.id[1][mid] < v) lo = mid + 1;
+    if (id[mid] < v) lo = mid + 1;
     else hi = mid;
   }
-  return lo < n && s.id[1][lo] == v ? s.w[1][lo] : 0.0;
+  return lo < n && id[lo] == v ? w[lo] : 0.0;
 }
 
-// ROWS: a position that its lists cannot give is computed here, from the
-// logits; else it is left to the row kernel.
-template <typename ET, bool ROWS>
-__global__ __launch_bounds__(MP_NT) void minp_position_kernel(MinpArgs ma) {
-  __shared__ MinpSmem s;
+// MP_OK: the record is the position's.
+template <typename ET, int NTHR, int PER>
+__device__ __forceinline__ int mp_position_from_lists(const MinpArgs& ma, const MinpMode& mm, int b, int i, MinpSmem<NTHR, PER>& s,
+                                                      PosRec* out) {
   const Args& a = ma.a;
-  const int b = (int)(blockIdx.x / (unsigned)(a.G + 1)), i = (int)(blockIdx.x % (unsigned)(a.G + 1)), tid = threadIdx.x;
-  const MinpMode mm = minp_mode(ma, b);
-  if (i == 0 && tid == 0 && !a.sampler) a.seq_flags[b] = 0;
-  PosRec rec{0.0, 0.0, 0.0, -1, 0u};
-  if (mm.kind == MP_INVALID) {
-    rec.bad = 1u;
-    if (tid == 0) mp_put(ma, b, i, rec);
-    return;
-  }
-  if (i > mm.m.g) return;
+  const int tid = mp_tid<NTHR>();
   const bool two = i < mm.m.g;
-  int n[2] = {0, 0}, how = mm.kind == MP_ROW ? MP_TOO_LONG : MP_OK;
+  PosRec rec{0.0, 0.0, 0.0, -1, 1u};
+  *out = rec;
+  if (mm.kind == MP_INVALID) return MP_OK;
+  if (mm.kind == MP_ROW) return MP_TOO_LONG;
+  int n[2] = {0, 0};
   uint32_t kmax[2];
   MinpRow r[2];
-  for (int h = 0; h < (two ? 2 : 1) && how == MP_OK; ++h)
-    how = mp_gather<ET>(ma, mm, (long long)b * a.RS + (h ? a.G + 1 + i : i), h, s, &n[h], r[h], &kmax[h]);
-  if (how == MP_TOO_LONG) {
-    if constexpr (ROWS) {
-      uint32_t* few = &s.key[0][0];   // key and id
-      bool ok = mp_row_stats<ET, MP_NT>(row_ptr<ET>(a, b, true, i), a.V, mm, s.s, few, 4 * MP_CAP, &r[0]);
-      __syncthreads();
-      r[1] = r[0];
-      if (ok && two) ok = mp_row_stats<ET, MP_NT>(row_ptr<ET>(a, b, false, i), a.V, mm, s.s, few, 4 * MP_CAP, &r[1]);
-      __syncthreads();
-      rec.bad = 1u;
-      if (ok) rec = mp_position_from_rows<ET, MP_NT>(ma, mm, b, i, r[0], r[1], s.s);
-      if (tid == 0) mp_put(ma, b, i, rec);
-    } else if (tid == 0) {
-      a.dense_list[atomicAdd(&a.dense_count[0], 1u)] = (int)blockIdx.x;
-    }
-    return;
+  for (int h = 0; h < (two ? 2 : 1); ++h) {
+    const int how = mp_gather(ma, mm, (long long)b * a.RS + (h ? a.G + 1 + i : i), row_ptr<ET>(a, b, !h, i), h, s, &n[h], r[h], &kmax[h]);
+    if (how == MP_IS_BAD) return MP_OK;
+    if (how != MP_OK) return how;
   }
-  if (how == MP_IS_BAD) {
-    rec.bad = 1u;
-    if (tid == 0) mp_put(ma, b, i, rec);
-    return;
-  }
+  rec.bad = 0u;
   const double invT = mm.kind == MP_GREEDY ? 0.0 : 1.0 / (double)mm.m.T;
   for (int h = 0; h < (two ? 2 : 1); ++h) {
     if (mm.kind == MP_GREEDY) {
       r[h].invS = 1.0;
     } else {
       const auto keys = [&](auto fn) {
-        for (int j = tid; j < n[h]; j += MP_NT) fn(s.key[h][j]);
+        for (int j = tid; j < n[h]; j += NTHR) fn(s.key[h][j]);
       };
-      mp_filter<ET, MP_NT>(keys, mm, kmax[h], invT, s.s, r[h]);
+      mp_filter<ET, NTHR>(keys, mm, kmax[h], invT, s.s, r[h]);
     }
-    for (int j = tid; j < n[h]; j += MP_NT) {
+    for (int j = tid; j < n[h]; j += NTHR) {
       const uint32_t key = s.key[h][j];
       s.w[h][j] = key >= r[h].thr ? mp_exp(((double)Key<ET>::value(key) - (double)r[h].zmax) * invT) * r[h].invS : 0.0;
     }
   }
-  __syncthreads();
+  mp_sync<NTHR>();
   // A thread's run of consecutive entries of the target's row.
-  constexpr int PER = MP_CAP / MP_NT;
-  const int per = (n[0] + MP_NT - 1) / MP_NT, j0 = tid * per;
+  const int per = (n[0] + NTHR - 1) / NTHR, j0 = tid * per;
   const uint32_t x = two ? (uint32_t)a.draft[(size_t)b * a.G + i] : NONE;
   double al = 0.0, z = 0.0, px = 0.0, w[PER];
 #pragma unroll
   for (int e = 0; e < PER; ++e) {
     w[e] = 0.0;
     if (e < per && j0 + e < n[0]) {
-      const double p = s.w[0][j0 + e], q = two ? mp_find(s, n[1], s.id[0][j0 + e]) : 0.0;
+      const double p = s.w[0][j0 + e], q = two ? mp_find(s.id[1], s.w[1], n[1], s.id[0][j0 + e]) : 0.0;
       al += fmin(p, q);
       w[e] = fmax(p - q, 0.0);
       if (s.id[0][j0 + e] == x) px = p;
     }
     z += w[e];
   }
-  rec.alpha = mp_sum<MP_NT>(al, s.s.red);
-  rec.px = mp_sum<MP_NT>(px, s.s.red);   // one thread's
-  double Z, before = mp_scan<MP_NT>(z, s.s.red, &Z);
+  rec.alpha = mp_sum<NTHR>(al, s.s.red);
+  rec.px = mp_sum<NTHR>(px, s.s.red);   // one thread's
+  double Z, before = mp_scan<NTHR>(z, s.s.red, &Z);
   if (!(Z > 0.0)) {   // no residual is left: draw from p
     z = 0.0;
 #pragma unroll
@@ -951,9 +947,9 @@ __global__ __launch_bounds__(MP_NT) void minp_position_kernel(MinpArgs ma) {
       w[e] = e < per && j0 + e < n[0] ? s.w[0][j0 + e] : 0.0;
       z += w[e];
     }
-    before = mp_scan<MP_NT>(z, s.s.red, &Z);
+    before = mp_scan<NTHR>(z, s.s.red, &Z);
   }
-  rec.qx = two ? mp_find(s, n[1], x) : 0.0;
+  rec.qx = two ? mp_find(s.id[1], s.w[1], n[1], x) : 0.0;
   const double target = (double)a.u[(size_t)b * (a.G + 1) + a.G] * Z;
   uint32_t mine = NONE, last = 0;
 #pragma unroll
@@ -964,24 +960,128 @@ __global__ __launch_bounds__(MP_NT) void minp_position_kernel(MinpArgs ma) {
       if (mine == NONE && before > target) mine = (uint32_t)(j0 + e);
     }
   }
-  uint32_t hit = mp_reduce_u32<MP_NT>(mine, NONE, s.s.red_u, [](uint32_t p, uint32_t q) { return p < q ? p : q; });
-  last = mp_reduce_u32<MP_NT>(last, 0u, s.s.red_u, [](uint32_t p, uint32_t q) { return p > q ? p : q; });
+  uint32_t hit = mp_reduce_u32<NTHR>(mine, NONE, s.s.red_u, [](uint32_t p, uint32_t q) { return p < q ? p : q; });
+  last = mp_reduce_u32<NTHR>(last, 0u, s.s.red_u, [](uint32_t p, uint32_t q) { return p > q ? p : q; });
   if (hit == NONE) hit = last - 1;
-  if (tid == 0) {
-    rec.tok = (int)s.id[0][hit];
-    if (a.sampler) rec.px = s.w[0][hit];
-    mp_put(ma, b, i, rec);
-  }
+  rec.tok = (int)s.id[0][hit];
+  if (a.sampler) rec.px = s.w[0][hit];
+  *out = rec;
+  return MP_OK;
 }
 
 // ---------------------------------------------------------------------------
-// Acceptance: one wavefront per sequence.
+// Acceptance of sequence b from its records, by one wavefront.
 // ---------------------------------------------------------------------------
+__device__ __forceinline__ void mp_finish(const MinpArgs& ma, int b, const Mode& m, const PosRec* rec) {
+  const Args& a = ma.a;
+  const int lane = threadIdx.x & 63, G = a.G, g = m.g;
+  const float* ub = a.u + (size_t)b * (G + 1);
+  PosRec r{0.0, 0.0, 0.0, -1, 0u};
+  int32_t x = 0;
+  float u = 0.5f;
+  if (lane < g) {
+    r = rec[lane];
+    x = a.draft[(size_t)b * G + lane];
+    u = ub[lane];
+  }
+  const float ures = ub[G], lv = a.lenience ? a.lenience[b] : 1.0f;
+  const bool bad = lane < g && (x < 0 || x >= a.V || !(u >= 0.0f && u < 1.0f) || r.bad);
+  const bool ok = lv >= 0.0f && lv <= 1.0f && ures >= 0.0f && ures < 1.0f && !rec[g].bad && __ballot(bad) == 0ull;
+  // The first rejection; if there is none, the bonus position.
+  const unsigned long long rejected = __ballot(lane < g && !((double)u * (double)lv * r.qx < r.px));
+  const int n = rejected ? __ffsll((long long)rejected) - 1 : g;
+  const int tok = rec[n].tok;
+  const float qnan = __int_as_float(0x7FC00000);
+  const auto value = [&](double v) { return ok ? (lane < g ? (float)v : 0.0f) : qnan; };
+  for (int i = lane; i <= G; i += 64)
+    a.out_tokens[(size_t)b * (G + 1) + i] = !ok || i > n ? -1 : i < n ? x : tok;   // (i < n <= 64: i is the lane)
+  if (lane < G) {
+    a.out_alpha[(size_t)b * G + lane] = value(r.alpha);
+    if (a.out_pq) {
+      a.out_pq[((size_t)b * G + lane) * 2] = value(r.px);
+      a.out_pq[((size_t)b * G + lane) * 2 + 1] = value(r.qx);
+    }
+  }
+  if (lane == 0) a.out_n[b] = ok ? n : -1;
+}
+
+// One workgroup per sequence, or per MP_POS_WAVES rows to sample.  A wavefront
+// takes a position whose rows keep at most MinpWave::CAP values each; the whole
+// workgroup takes the longer ones after that, up to MinpBlock::CAP; what then is
+// left it computes from the logits (ROWS), or leaves to the row kernels, which
+// also finish the sequence.
+template <typename ET, bool ROWS>
+__global__ __launch_bounds__(MP_POS_NT, 4) void minp_position_kernel(MinpArgs ma) {
+  __shared__ union {
+    MinpWave wave[MP_POS_WAVES];
+    MinpBlock block;
+  } s;
+  __shared__ PosRec rec[SV_MAX_GAMMA + 1];
+  __shared__ uint32_t later[SV_MAX_GAMMA + 1];
+  const Args& a = ma.a;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int b0 = a.sampler ? (int)blockIdx.x * MP_POS_WAVES : (int)blockIdx.x;
+  const Mode m0 = seq_mode(ma.a, b0);
+  const int count = a.sampler ? min(MP_POS_WAVES, a.B - b0) : m0.g + 1;
+  for (int j = wave; j < count; j += MP_POS_WAVES) {
+    const int b = a.sampler ? b0 + j : b0, i = a.sampler ? 0 : j;
+    PosRec r;
+    const int how = mp_position_from_lists<ET>(ma, minp_mode(ma, b), b, i, s.wave[wave], &r);
+    if (lane == 0) {
+      rec[j] = r;
+      later[j] = how != MP_OK;
+    }
+  }
+  __syncthreads();
+  bool left = false;
+  for (int j = 0; j < count; ++j) {
+    if (!later[j]) continue;
+    const int b = a.sampler ? b0 + j : b0, i = a.sampler ? 0 : j;
+    const MinpMode mm = minp_mode(ma, b);
+    PosRec r;
+    int how = mp_position_from_lists<ET>(ma, mm, b, i, s.block, &r);
+    __syncthreads();
+    if (how != MP_OK) {
+      if constexpr (ROWS) {
+        uint32_t* few = &s.block.key[0][0];   // key and id
+        MinpRow r0, r1;
+        bool ok = mp_row_stats<ET, MP_POS_NT>(row_ptr<ET>(a, b, true, i), a.V, mm, s.block.s, few, 4 * MinpBlock::CAP, &r0);
+        __syncthreads();
+        r1 = r0;
+        if (ok && i < mm.m.g) ok = mp_row_stats<ET, MP_POS_NT>(row_ptr<ET>(a, b, false, i), a.V, mm, s.block.s, few, 4 * MinpBlock::CAP, &r1);
+        __syncthreads();
+        if (ok) r = mp_position_from_rows<ET, MP_POS_NT>(ma, mm, b, i, r0, r1, s.block.s);
+        how = MP_OK;
+      } else {
+        if (threadIdx.x == 0) a.dense_list[atomicAdd(&a.dense_count[0], 1u)] = b * (a.G + 1) + i;
+        left = true;
+      }
+    }
+    if (threadIdx.x == 0) {
+      if (how == MP_OK) later[j] = 0;
+      rec[j] = r;
+    }
+    __syncthreads();
+  }
+  if (a.sampler) {
+    if ((int)threadIdx.x < count && !later[threadIdx.x]) mp_put_sample(ma, b0 + (int)threadIdx.x, rec[threadIdx.x]);
+    return;
+  }
+  if (threadIdx.x == 0) ma.left[b0] = left;
+  if (left) {
+    for (int j = threadIdx.x; j < count; j += MP_POS_NT)
+      if (!later[j]) a.pos[(size_t)b0 * (a.G + 1) + j] = rec[j];
+  } else if (wave == 0) {
+    mp_finish(ma, b0, m0, rec);
+  }
+}
+
+// The sequences that the position kernel did not finish: one wavefront each.
 constexpr int MP_FIN_NT = 256;
 __global__ __launch_bounds__(MP_FIN_NT) void minp_finish_kernel(MinpArgs ma) {
   const int b = (int)(blockIdx.x * (MP_FIN_NT / 64) + (threadIdx.x >> 6));
-  if (b >= ma.a.B) return;
-  finish_from_pairs_wave(ma.a, b, seq_mode(ma.a, b));
+  if (b >= ma.a.B || !ma.left[b]) return;
+  mp_finish(ma, b, seq_mode(ma.a, b), ma.a.pos + (size_t)b * (ma.a.G + 1));
 }
 
 }  // namespace sv
