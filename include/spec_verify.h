@@ -374,7 +374,7 @@ int spec_verify_spectr(const void* p_logits, const void* q_logits, int dtype, co
  *  min_p        [B] or [R] float: above 0 and at most 1; 0 or less: no min-p; above 1 or NaN makes
  *               the sequence invalid.  NULL: none has min-p.  T = 0 is argmax, whatever min_p is.
  *  hints        0, or SV_HINT_ALL_MIN_P: the caller knows that every sequence has min_p > 0 or
- *               T = 0, and the launch that takes the other sequences is left out.  One that breaks
+ *               T = 0, and the launches that take the other sequences, row by row, are replaced by one.  One that breaks
  *               the promise, or keeps more than the call's lists hold (1024 values of a row), still
  *               gets its exact result, from a slower path.
  *  out_prob     [R] float or NULL: the processed probability of the token drawn (NaN for an invalid

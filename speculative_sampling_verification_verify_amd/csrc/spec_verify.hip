@@ -997,13 +997,15 @@ static size_t minp_bytes(int B, int G, int V, int dtype) {
 template <typename ET>
 static hipError_t launch_minp(const MinpArgs& ma, const MinpPlan& p, int hints, hipStream_t st) {
   const Args& a = ma.a;
-  const dim3 units((unsigned)((long long)a.B * a.RS * a.NP)), groups((unsigned)(a.sampler ? (a.B + MP_POS_WAVES - 1) / MP_POS_WAVES : a.B));
+  const dim3 units((unsigned)((long long)a.B * a.RS * a.NP)), groups((unsigned)(a.sampler ? (a.B + a.split - 1) / a.split : a.B));
   hipError_t e;
   if (p.vpl == 8) hipLaunchKernelGGL((minp_cut_kernel<ET, 8>), units, dim3(MP_NT), 0, st, ma);
   else hipLaunchKernelGGL((minp_cut_kernel<ET, 2>), units, dim3(MP_NT), 0, st, ma);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   if (hints & SV_HINT_ALL_MIN_P) {
     hipLaunchKernelGGL((minp_position_kernel<ET, true>), groups, dim3(MP_POS_NT), 0, st, ma);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    hipLaunchKernelGGL((minp_left_kernel<ET>), dim3(MP_LEFT_GRID), dim3(MP_POS_NT), 0, st, ma);
     return hipGetLastError();
   }
   hipLaunchKernelGGL((minp_position_kernel<ET, false>), groups, dim3(MP_POS_NT), 0, st, ma);
@@ -1050,6 +1052,10 @@ static int run_minp(const void* p_logits, const void* q_logits, int dtype, const
   a.RS = 2 * G + 1;
   a.NP = p.NP;
   a.PL = p.PL;
+  // Rows to sample of a workgroup: one where they fit the chip at once (its long
+  // lists then wait for nobody), up to one a wavefront.
+  a.split = (B + 511) / 512;
+  a.split = a.split > MP_POS_WAVES ? MP_POS_WAVES : a.split;
   a.out_tokens = out_tokens;
   a.out_n = out_n;
   a.out_alpha = out_alpha;

@@ -15,7 +15,10 @@
 //                         then the acceptance
 //   minp_row_kernel, minp_row_position_kernel, minp_finish_kernel
 //                         the same from the logits, for rows without min-p and
-//                         rows that keep more than the lists hold
+//                         rows that keep more than the lists hold, one
+//                         workgroup a row; where the caller says that there are
+//                         none of the first, minp_left_kernel in place of the
+//                         three, one workgroup a sequence
 //
 // Probabilities, normalisers and nucleus masses are held in 64 bits (the masses
 // as fixed-point numbers, whose sum does not depend on its order), so that a
@@ -34,6 +37,7 @@ constexpr int MP_POS_WAVES = MP_POS_NT / 64;
 constexpr int MP_PART_CAP = 512;  // list entries of a row part
 constexpr int MP_ROW_NT = 1024;   // threads of a row workgroup
 constexpr int MP_ROW_GRID = 512;
+constexpr int MP_LEFT_GRID = 256;
 constexpr int MP_FEW_KEYS = 8192; // keys of one bin that a row workgroup holds
 constexpr int MP_BINS = 256;      // bins of a row's masses, 1/8 wide in (zmax - z) / T; also a digit's
 constexpr int MP_FIX = 42;        // fraction bits of a mass: at most 2^20 masses of at most 1
@@ -51,7 +55,8 @@ struct MinpRow {
 
 struct MinpArgs {
   Args a;                 // rows, parameters, outputs; a.pos the records, a.dense_count[0] the number of
-                          // positions left to the row kernel, a.dense_list those positions
+                          // positions left to the row kernel, a.dense_list those positions; a.split
+                          // rows to sample of a position workgroup
   const float* min_p;     // [B] or null (0)
   uint32_t* part_max;     // [rows][NP] largest key
   uint32_t* part_count;   // [rows][NP] entries, or flags
@@ -81,7 +86,6 @@ struct MinpMode {
   Mode m;
   int kind, k;     // k: top-k, 0: off
   float mp;
-  double cut;      // T ln(min_p)
 };
 __device__ __forceinline__ MinpMode minp_mode(const MinpArgs& ma, int b) {
   MinpMode r;
@@ -92,7 +96,6 @@ __device__ __forceinline__ MinpMode minp_mode(const MinpArgs& ma, int b) {
   const int gl = ma.a.gamma_len ? ma.a.gamma_len[b] : ma.a.G;
   const bool ok = r.m.mode != MODE_INVALID && r.m.tp == r.m.tp && r.mp <= 1.0f && (ma.a.sampler || (gl >= 1 && gl <= ma.a.G));
   r.kind = !ok ? MP_INVALID : r.m.mode == MODE_GREEDY ? MP_GREEDY : r.mp > 0.0f ? MP_LIST : MP_ROW;
-  r.cut = r.kind >= MP_LIST && r.mp > 0.0f ? (double)r.m.T * log((double)r.mp) : 0.0;
   return r;
 }
 
@@ -470,34 +473,31 @@ __device__ __forceinline__ void mp_top_k(Feed feed, const MinpMode& mm, MinpScra
   *thr = max(*thr, t);
 }
 
-// top-k and top-p of the keys >= thr that feed gives, then their sum.
+// top-k and top-p of the keys that feed gives with their weights, the largest
+// kmax; returns the sum of those >= thr.
 template <typename ET, int NTHR, class Feed>
-__device__ __forceinline__ void mp_filter(Feed feed, const MinpMode& mm, uint32_t kmax, double invT, MinpScratch& s, MinpRow& r) {
-  const double z0 = (double)r.zmax;
-  const auto weight = [&](uint32_t key) { return mp_exp(((double)Key<ET>::value(key) - z0) * invT); };
-  mp_top_k<ET, NTHR>(feed, mm, s, &r.thr);
-  const auto total = [&]() {
-    double x = 0.0;
-    feed([&](uint32_t key) {
-      if (key >= r.thr) x += weight(key);
-    });
-    return mp_sum<NTHR>(x, s.red);
-  };
-  double S = total();
-  if (mm.m.tp < 1.0f) {
-    uint32_t t = kmax;
-    if (mm.m.tp > 0.0f)
-      t = mp_nucleus<Key<ET>::LEVELS, NTHR>([&](auto fn) {
-        feed([&](uint32_t key) {
-          if (key >= r.thr) fn(key, weight(key));
+__device__ __forceinline__ double mp_filter(Feed feed, const MinpMode& mm, uint32_t kmax, MinpScratch& s, uint32_t* thr) {
+  mp_top_k<ET, NTHR>([&](auto fn) { feed([&](uint32_t key, double) { fn(key); }); }, mm, s, thr);
+  const bool nucleus = mm.m.tp < 1.0f && mm.m.tp > 0.0f;
+  if (mm.m.tp <= 0.0f) *thr = kmax;
+  double S = 0.0;
+#pragma unroll 1
+  for (int pass = 0; pass < (nucleus ? 2 : 1); ++pass) {
+    if (pass == 1) {
+      const uint32_t t = mp_nucleus<Key<ET>::LEVELS, NTHR>([&](auto fn) {
+        feed([&](uint32_t key, double e) {
+          if (key >= *thr) fn(key, e);
         });
       }, 0ull, (double)mm.m.tp * S * (double)(1ull << MP_FIX), s);
-    if (t > r.thr) {
-      r.thr = t;
-      S = total();
+      *thr = max(*thr, t);
     }
+    double x = 0.0;
+    feed([&](uint32_t key, double e) {
+      if (key >= *thr) x += e;
+    });
+    S = mp_sum<NTHR>(x, s.red);
   }
-  r.invS = 1.0 / S;
+  return S;
 }
 
 // ---------------------------------------------------------------------------
@@ -567,7 +567,7 @@ __device__ __forceinline__ bool mp_row_stats(const ET* row, int V, const MinpMod
   if (bad || kmax <= Key<ET>::NEG_INF) return false;
   const float zmax = Key<ET>::value(kmax);
   const double z0 = (double)zmax;
-  uint32_t thr = mm.mp > 0.0f ? min(mp_key_from<ET>(z0 + mm.cut), kmax) : Key<ET>::NEG_INF + 1;
+  uint32_t thr = mm.mp > 0.0f ? min(mp_key_from<ET>(z0 + (double)mm.m.T * log((double)mm.mp)), kmax) : Key<ET>::NEG_INF + 1;
   const auto keys = [&](auto fn) { mp_for_row<ET, NTHR>(row, V, [&](uint32_t key, int) { fn(key); }); };
   const auto exponent = [&](uint32_t key) { return ((double)Key<ET>::value(key) - z0) * invT; };
   mp_top_k<ET, NTHR>(keys, mm, s, &thr);
@@ -807,7 +807,8 @@ struct MinpSmem {
   static constexpr int CAP = NTHR * PER;
   MinpScratch s;
   uint32_t key[2][CAP], id[2][CAP];
-  double w[2][CAP];      // probabilities
+  double w[2][CAP];      // weights, then probabilities
+  int n[2];
   uint32_t base[NTHR];   // entries before each of some parts
 };
 typedef MinpSmem<64, 3> MinpWave;
@@ -815,37 +816,53 @@ typedef MinpSmem<MP_POS_NT, 2> MinpBlock;
 
 enum { MP_OK = 0, MP_IS_BAD = 1, MP_TOO_LONG = 2 };
 
-// The values of one row that min-p keeps, in ascending id, into key[h] and id[h].
+// A thread's part of a row: its maximum and count.
+struct MinpPart {
+  uint32_t top, count;
+};
+__device__ __forceinline__ MinpPart mp_part(const MinpArgs& ma, long long rowid, int p) {
+  const long long at = rowid * ma.a.NP + p;
+  return p < ma.a.NP ? MinpPart{ma.part_max[at], ma.part_count[at]} : MinpPart{0u, 0u};
+}
+
+// One row's processed distribution from its lists: the values that min-p keeps, in
+// ascending id, into key[h], id[h] and w[h], exp((z - zmax) / T) >= min_p each; then
+// the probabilities of what top-k and top-p leave, 0 for the others.  first: the
+// thread's part among the first NTHR.  (All of this is executed about once in a
+// launch, from memory: its time is that of fetching the instructions, so there is
+// one copy of it for both rows.)
 template <typename ET, int NTHR, int PER>
-__device__ __forceinline__ int mp_gather(const MinpArgs& ma, const MinpMode& mm, long long rowid, const ET* row, int h,
-                                         MinpSmem<NTHR, PER>& s, int* n, MinpRow& r, uint32_t* kmax_out) {
+__device__ __forceinline__ int mp_list_row(const MinpArgs& ma, const MinpMode& mm, long long rowid, const ET* row, int h, MinpPart first,
+                                           MinpSmem<NTHR, PER>& s) {
   typedef MinpEntry<ET> E;
   constexpr int CAP = NTHR * PER;
-  const int NP = ma.a.NP, tid = mp_tid<NTHR>(), lane = tid & 63;
-  const uint32_t* pm = ma.part_max + rowid * NP;
-  const uint32_t* pc = ma.part_count + rowid * NP;
-  uint32_t kmax = 0, flags = 0;
-  for (int p = tid; p < NP; p += NTHR) {
-    kmax = max(kmax, pm[p]);
-    flags |= pc[p] & (MP_BAD | MP_OVER);
+  const int NP = ma.a.NP, tid = mp_tid<NTHR>();
+  uint32_t kmax = first.top, flags = first.count;
+#pragma unroll 1
+  for (int p = NTHR + tid; p < NP; p += NTHR) {
+    const MinpPart q = mp_part(ma, rowid, p);
+    kmax = max(kmax, q.top);
+    flags |= q.count;
   }
   kmax = mp_reduce_u32<NTHR>(kmax, 0u, s.s.red_u, [](uint32_t x, uint32_t y) { return x > y ? x : y; });
   flags = mp_reduce_u32<NTHR>(flags, 0u, s.s.red_u, [](uint32_t x, uint32_t y) { return x | y; });
   if ((flags & MP_BAD) || kmax <= Key<ET>::NEG_INF) return MP_IS_BAD;
   if (flags & MP_OVER) return MP_TOO_LONG;
-  r.zmax = Key<ET>::value(kmax);
-  r.thr = mm.kind == MP_GREEDY ? kmax : min(mp_key_from<ET>((double)r.zmax + mm.cut), kmax);
-  *kmax_out = kmax;
+  const bool greedy = mm.kind == MP_GREEDY;
+  const double z0 = (double)Key<ET>::value(kmax), invT = greedy ? 0.0 : 1.0 / (double)mm.m.T, least = (double)mm.mp;
+  // A part whose maximum is well below what is kept has nothing that is.
+  const float near = Key<ET>::value(kmax) + mm.m.T * (__logf(mm.mp) - 0.001f);
+  const float floor_ = greedy ? Key<ET>::value(kmax) : near - 1e-5f * fabsf(near);
   const int lead = mp_lead(row);
   int have = 0;
+#pragma unroll 1
   for (int p0 = 0; p0 < NP; p0 += NTHR) {   // NTHR parts at a time
     uint32_t total;
-    // A part whose maximum is not kept has nothing that is.
-    const uint32_t c = p0 + tid < NP && pm[p0 + tid] >= r.thr ? pc[p0 + tid] : 0u;
-    const uint32_t before = mp_scan_u32<NTHR>(c, s.s.red_u, &total);
-    s.base[tid] = before;
+    const MinpPart q = p0 == 0 ? first : mp_part(ma, rowid, p0 + tid);
+    s.base[tid] = mp_scan_u32<NTHR>(q.top != 0u && !(Key<ET>::value(q.top) < floor_) ? q.count : 0u, s.s.red_u, &total);
     mp_sync<NTHR>();
     const int np = min(NP - p0, NTHR);
+#pragma unroll 1
     for (uint32_t i0 = 0; i0 < total; i0 += NTHR) {
       const uint32_t i = i0 + (uint32_t)tid;
       uint32_t key = 0, id = 0;
@@ -860,19 +877,39 @@ __device__ __forceinline__ int mp_gather(const MinpArgs& ma, const MinpMode& mm,
         key = Key<ET>::of_bits(E::bits(e));
         id = (uint32_t)((p0 + lo) * ma.a.PL - lead) + E::index(e);
       }
-      uint32_t all;
-      const uint32_t keep = key >= r.thr ? 1u : 0u, at = (uint32_t)have + mp_scan_u32<NTHR>(keep, s.s.red_u, &all);
+      const double w = mp_exp(((double)Key<ET>::value(key) - z0) * invT);
+      const bool keep = i < total && (greedy ? key == kmax : w >= least);
+      uint32_t all, at = (uint32_t)have;
+      if constexpr (NTHR == 64) {
+        const unsigned long long mask = __ballot(keep);
+        at += (uint32_t)__popcll(mask & ((1ull << tid) - 1));
+        all = (uint32_t)__popcll(mask);
+      } else {
+        at += mp_scan_u32<NTHR>(keep ? 1u : 0u, s.s.red_u, &all);
+      }
       if (keep && at < (uint32_t)CAP) {
         s.key[h][at] = key;
         s.id[h][at] = id;
+        s.w[h][at] = w;
       }
       have += (int)all;
     }
     mp_sync<NTHR>();
   }
-  if (mm.kind == MP_GREEDY) have = 1;   // the lowest id
-  *n = have;
-  return have > CAP ? MP_TOO_LONG : MP_OK;
+  if (greedy) have = 1;   // the lowest id
+  if (have > CAP) return MP_TOO_LONG;
+  if (tid == 0) s.n[h] = have;
+  if (!greedy) {
+    uint32_t thr = 0;
+    const double S = mp_filter<ET, NTHR>([&](auto fn) {
+#pragma unroll 1
+      for (int j = tid; j < have; j += NTHR) fn(s.key[h][j], s.w[h][j]);
+    }, mm, kmax, s.s, &thr);
+#pragma unroll 1
+    for (int j = tid; j < have; j += NTHR) s.w[h][j] = s.key[h][j] >= thr ? s.w[h][j] / S : 0.0;
+  }
+  mp_sync<NTHR>();
+  return MP_OK;
 }
 
 // q(v) by v's place among the n ascending ids of row 1.
@@ -897,34 +934,20 @@ __device__ __forceinline__ int mp_position_from_lists(const MinpArgs& ma, const 
   *out = rec;
   if (mm.kind == MP_INVALID) return MP_OK;
   if (mm.kind == MP_ROW) return MP_TOO_LONG;
-  int n[2] = {0, 0};
-  uint32_t kmax[2];
-  MinpRow r[2];
+  const long long rowid[2] = {(long long)b * a.RS + i, (long long)b * a.RS + (two ? a.G + 1 + i : i)};
+  const MinpPart first[2] = {mp_part(ma, rowid[0], tid), mp_part(ma, rowid[1], tid)};
+  const uint32_t x = two ? (uint32_t)a.draft[(size_t)b * a.G + i] : NONE;
+  const float u = a.u[(size_t)b * (a.G + 1) + a.G];
+#pragma unroll 1
   for (int h = 0; h < (two ? 2 : 1); ++h) {
-    const int how = mp_gather(ma, mm, (long long)b * a.RS + (h ? a.G + 1 + i : i), row_ptr<ET>(a, b, !h, i), h, s, &n[h], r[h], &kmax[h]);
+    const int how = mp_list_row(ma, mm, h ? rowid[1] : rowid[0], row_ptr<ET>(a, b, !h, i), h, h ? first[1] : first[0], s);
     if (how == MP_IS_BAD) return MP_OK;
     if (how != MP_OK) return how;
   }
   rec.bad = 0u;
-  const double invT = mm.kind == MP_GREEDY ? 0.0 : 1.0 / (double)mm.m.T;
-  for (int h = 0; h < (two ? 2 : 1); ++h) {
-    if (mm.kind == MP_GREEDY) {
-      r[h].invS = 1.0;
-    } else {
-      const auto keys = [&](auto fn) {
-        for (int j = tid; j < n[h]; j += NTHR) fn(s.key[h][j]);
-      };
-      mp_filter<ET, NTHR>(keys, mm, kmax[h], invT, s.s, r[h]);
-    }
-    for (int j = tid; j < n[h]; j += NTHR) {
-      const uint32_t key = s.key[h][j];
-      s.w[h][j] = key >= r[h].thr ? mp_exp(((double)Key<ET>::value(key) - (double)r[h].zmax) * invT) * r[h].invS : 0.0;
-    }
-  }
-  mp_sync<NTHR>();
+  const int n[2] = {s.n[0], two ? s.n[1] : 0};
   // A thread's run of consecutive entries of the target's row.
   const int per = (n[0] + NTHR - 1) / NTHR, j0 = tid * per;
-  const uint32_t x = two ? (uint32_t)a.draft[(size_t)b * a.G + i] : NONE;
   double al = 0.0, z = 0.0, px = 0.0, w[PER];
 #pragma unroll
   for (int e = 0; e < PER; ++e) {
@@ -950,7 +973,7 @@ __device__ __forceinline__ int mp_position_from_lists(const MinpArgs& ma, const 
     before = mp_scan<NTHR>(z, s.s.red, &Z);
   }
   rec.qx = two ? mp_find(s.id[1], s.w[1], n[1], x) : 0.0;
-  const double target = (double)a.u[(size_t)b * (a.G + 1) + a.G] * Z;
+  const double target = (double)u * Z;
   uint32_t mine = NONE, last = 0;
 #pragma unroll
   for (int e = 0; e < PER; ++e) {
@@ -1005,12 +1028,14 @@ __device__ __forceinline__ void mp_finish(const MinpArgs& ma, int b, const Mode&
   if (lane == 0) a.out_n[b] = ok ? n : -1;
 }
 
-// One workgroup per sequence, or per MP_POS_WAVES rows to sample.  A wavefront
+// One workgroup per sequence, or per a.split rows to sample.  A wavefront
 // takes a position whose rows keep at most MinpWave::CAP values each; the whole
 // workgroup takes the longer ones after that, up to MinpBlock::CAP; what then is
-// left it computes from the logits (ROWS), or leaves to the row kernels, which
-// also finish the sequence.
-template <typename ET, bool ROWS>
+// left goes to other launches, which also finish the sequence: listed by
+// position, or (WHOLE) by sequence, with REC_REDO in the records.  (Computed here,
+// with the registers that takes, it made the kernel spill: 19 instead of 6 us for
+// 1000 rows of 1000.)
+template <typename ET, bool WHOLE>
 __global__ __launch_bounds__(MP_POS_NT, 4) void minp_position_kernel(MinpArgs ma) {
   __shared__ union {
     MinpWave wave[MP_POS_WAVES];
@@ -1020,9 +1045,9 @@ __global__ __launch_bounds__(MP_POS_NT, 4) void minp_position_kernel(MinpArgs ma
   __shared__ uint32_t later[SV_MAX_GAMMA + 1];
   const Args& a = ma.a;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int b0 = a.sampler ? (int)blockIdx.x * MP_POS_WAVES : (int)blockIdx.x;
+  const int b0 = a.sampler ? (int)blockIdx.x * a.split : (int)blockIdx.x;
   const Mode m0 = seq_mode(ma.a, b0);
-  const int count = a.sampler ? min(MP_POS_WAVES, a.B - b0) : m0.g + 1;
+  const int count = a.sampler ? min(a.split, a.B - b0) : m0.g + 1;
   for (int j = wave; j < count; j += MP_POS_WAVES) {
     const int b = a.sampler ? b0 + j : b0, i = a.sampler ? 0 : j;
     PosRec r;
@@ -1039,26 +1064,15 @@ __global__ __launch_bounds__(MP_POS_NT, 4) void minp_position_kernel(MinpArgs ma
     const int b = a.sampler ? b0 + j : b0, i = a.sampler ? 0 : j;
     const MinpMode mm = minp_mode(ma, b);
     PosRec r;
-    int how = mp_position_from_lists<ET>(ma, mm, b, i, s.block, &r);
+    const int how = mp_position_from_lists<ET>(ma, mm, b, i, s.block, &r);
     __syncthreads();
     if (how != MP_OK) {
-      if constexpr (ROWS) {
-        uint32_t* few = &s.block.key[0][0];   // key and id
-        MinpRow r0, r1;
-        bool ok = mp_row_stats<ET, MP_POS_NT>(row_ptr<ET>(a, b, true, i), a.V, mm, s.block.s, few, 4 * MinpBlock::CAP, &r0);
-        __syncthreads();
-        r1 = r0;
-        if (ok && i < mm.m.g) ok = mp_row_stats<ET, MP_POS_NT>(row_ptr<ET>(a, b, false, i), a.V, mm, s.block.s, few, 4 * MinpBlock::CAP, &r1);
-        __syncthreads();
-        if (ok) r = mp_position_from_rows<ET, MP_POS_NT>(ma, mm, b, i, r0, r1, s.block.s);
-        how = MP_OK;
-      } else {
-        if (threadIdx.x == 0) a.dense_list[atomicAdd(&a.dense_count[0], 1u)] = b * (a.G + 1) + i;
-        left = true;
-      }
+      if (!WHOLE && threadIdx.x == 0) a.dense_list[atomicAdd(&a.dense_count[0], 1u)] = b * (a.G + 1) + i;
+      if (WHOLE && a.sampler && threadIdx.x == 0) a.dense_list[atomicAdd(&a.dense_count[0], 1u)] = b;
+      left = true;
     }
-    if (threadIdx.x == 0) {
-      if (how == MP_OK) later[j] = 0;
+    if (threadIdx.x == 0 && how == MP_OK) {
+      later[j] = 0;
       rec[j] = r;
     }
     __syncthreads();
@@ -1067,12 +1081,52 @@ __global__ __launch_bounds__(MP_POS_NT, 4) void minp_position_kernel(MinpArgs ma
     if ((int)threadIdx.x < count && !later[threadIdx.x]) mp_put_sample(ma, b0 + (int)threadIdx.x, rec[threadIdx.x]);
     return;
   }
-  if (threadIdx.x == 0) ma.left[b0] = left;
+  if (threadIdx.x == 0) {
+    if (WHOLE && left) a.dense_list[atomicAdd(&a.dense_count[0], 1u)] = b0;
+    if (!WHOLE) ma.left[b0] = left;
+  }
   if (left) {
-    for (int j = threadIdx.x; j < count; j += MP_POS_NT)
-      if (!later[j]) a.pos[(size_t)b0 * (a.G + 1) + j] = rec[j];
+    for (int j = threadIdx.x; j < count; j += MP_POS_NT) {
+      if (later[j]) rec[j].bad = REC_REDO;
+      if (WHOLE || !later[j]) a.pos[(size_t)b0 * (a.G + 1) + j] = rec[j];   // (else the row kernels write it)
+    }
   } else if (wave == 0) {
     mp_finish(ma, b0, m0, rec);
+  }
+}
+
+// The sequences (or rows to sample) that the position kernel left whole: one
+// workgroup each (of 512 threads: 1024 do not get the registers that it needs).
+template <typename ET>
+__global__ __launch_bounds__(MP_POS_NT) void minp_left_kernel(MinpArgs ma) {
+  __shared__ MinpScratch s;
+  __shared__ uint32_t few[MP_FEW_KEYS];
+  const Args& a = ma.a;
+  const uint32_t n = a.dense_count[0];
+  for (uint32_t j = blockIdx.x; j < n; j += gridDim.x) {
+    const int b = a.dense_list[j];
+    const MinpMode mm = minp_mode(ma, b);
+    PosRec* pos = a.pos + (size_t)b * (a.G + 1);
+    for (int i = 0; i <= (a.sampler ? 0 : mm.m.g); ++i) {
+      if (!a.sampler && pos[i].bad != REC_REDO) continue;
+      __syncthreads();
+      MinpRow r0, r1;
+      bool ok = mp_row_stats<ET, MP_POS_NT>(row_ptr<ET>(a, b, true, i), a.V, mm, s, few, MP_FEW_KEYS, &r0);
+      __syncthreads();
+      r1 = r0;
+      if (ok && i < mm.m.g) ok = mp_row_stats<ET, MP_POS_NT>(row_ptr<ET>(a, b, false, i), a.V, mm, s, few, MP_FEW_KEYS, &r1);
+      __syncthreads();
+      PosRec rec{0.0, 0.0, 0.0, -1, 1u};
+      if (ok) rec = mp_position_from_rows<ET, MP_POS_NT>(ma, mm, b, i, r0, r1, s);
+      __syncthreads();   // (everyone has read pos[i])
+      if (threadIdx.x == 0) {
+        if (a.sampler) mp_put_sample(ma, b, rec);
+        else pos[i] = rec;
+      }
+    }
+    __syncthreads();
+    if (!a.sampler && threadIdx.x < 64) mp_finish(ma, b, mm.m, pos);
+    __syncthreads();
   }
 }
 
