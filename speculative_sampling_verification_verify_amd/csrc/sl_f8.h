@@ -366,40 +366,47 @@ __global__ __launch_bounds__(512) void f8_order_kernel(F8Args a) {
   if (u == 0) a.xsc[(size_t)blockIdx.x * 32 + r] = s;
 }
 
-// 16 bytes a lane from memory (base + a lane's offset) into consecutive LDS, past
-// the registers.  In assembly, because the compiler lets any later read of LDS
-// wait for such a load: who uses this waits himself (f8_landed), before he reads
-// what it brings, and has read what lay there before.
-__device__ __forceinline__ void f8_to_lds(const void* base, uint32_t off, const char* lds) {
-  const uint32_t at = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)lds);
+// 16 (or 4) bytes a lane from memory (base + a lane's offset) into consecutive LDS
+// from byte `at` on, past the registers.  In assembly, because the compiler lets
+// any later read of LDS wait for such a load: who uses this waits himself
+// (f8_landed), before he reads what it brings, and has read what lay there before.
+__device__ __forceinline__ void f8_to_lds(const void* base, uint32_t off, uint32_t at) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(off), "s"(base) : "memory");   // (nothing else here uses m0)
 }
-// The same with 4 bytes a lane.
-__device__ __forceinline__ void f8_word_to_lds(const void* base, uint32_t off, const char* lds) {
-  const uint32_t at = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)lds);
+__device__ __forceinline__ void f8_word_to_lds(const void* base, uint32_t off, uint32_t at) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(at), "v"(off), "s"(base) : "memory");
 }
-__device__ __forceinline__ void f8_landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// All but the last N of this wavefront's loads have landed.
+template <int N> __device__ __forceinline__ void f8_landed() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
 
 // Eight wavefronts, four along the weight rows (32 CN of them each) by two along
 // the rows of x (32 MT each).  Weight rows are the products' rows, rows of x
 // their columns: a lane's results share a row of x, hence one scale a block.
-// Both come from memory into LDS without registers in between, a block ahead,
-// in two buffers with one barrier a block.  The weights are loaded in whole
-// lines and read in operand order; position q of a row holds its 16-byte unit
-// q ^ (row % 8), so that the reads do not conflict.
+// Both come from memory into LDS without registers in between, in as many
+// buffers as fit, all but one block ahead, with one barrier a block.  The weights
+// are loaded in whole lines and read in operand order; position q of a row holds
+// its 16-byte unit q ^ (row / 2 % 8), so that the reads do not conflict (4 cycles a
+// 16-byte read of a wavefront, measured alone; with row % 8, 8).
 constexpr int F8T_NT = 512;
+constexpr int F8T_SW = 4096;   // bytes of the weights' scales: SL_MAX_K / 128 blocks, twice
 
-template <int CN, int MT, bool F8>
-__host__ __device__ constexpr int f8_tile_lds() { return 2 * (4 * CN * 4096 + 2 * MT * (f8_block_bytes<F8>() + 128)); }
+template <int CN, int MT, bool F8> struct F8Tile {
+  static constexpr int N = 128 * CN;                                       // weight rows of a workgroup
+  static constexpr int WL = N * 128, XB = f8_block_bytes<F8>(), XL = 2 * MT * XB, SL = F8T_NT * 4;
+  static constexpr int STAGE = WL + XL + SL;                               // weights, operands of x, their scales
+  static constexpr int FIT = (160 * 1024 - F8T_SW) / STAGE, STAGES = FIT > 6 ? 6 : FIT;
+  static constexpr int WI = WL / 8192, XI = XL / 8192, LOADS = WI + XI + 1;   // of 1 KB; loads a wavefront and block
+  static constexpr int PITCH = 32 * CN * 4 + 16, OUT = 8 * 32 * PITCH;     // results on their way out
+  static constexpr int LDS = F8T_SW + (STAGES * STAGE > OUT ? STAGES * STAGE : OUT);
+  static_assert(STAGES >= 2 && LDS <= 160 * 1024 && LOADS * (STAGES - 2) < 64, "a workgroup's LDS, the count of loads");
+};
 
 template <int CN, int MT, bool F8>
 __global__ __launch_bounds__(F8T_NT, 2) void f8_tile_kernel(F8Args a) {
-  constexpr int XB = f8_block_bytes<F8>(), N = 128 * CN;   // weight rows of a workgroup
-  constexpr int WL = N * 128, XL = 2 * MT * XB;            // bytes of a block
-  constexpr int WI = WL / 8192, XI = XL / 8192;            // 1 KB loads a wavefront
-  constexpr int SL = 2 * MT * 128, XAT = 2 * WL, SAT = XAT + 2 * XL;
-  extern __shared__ __align__(16) char lds[];              // [2] weights, [2] operands of x, [2] their scales
+  typedef F8Tile<CN, MT, F8> T;
+  constexpr int N = T::N, WL = T::WL, XB = T::XB, WI = T::WI, XI = T::XI, AHEAD = T::STAGES - 1;
+  extern __shared__ __align__(16) char lds[];              // the weights' scales, then the stages
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), wn = wave & 3, wr = wave >> 2;
   int lane = tid & 63;
   const int KB = a.KB;
@@ -411,26 +418,28 @@ __global__ __launch_bounds__(F8T_NT, 2) void f8_tile_kernel(F8Args a) {
   const int n0 = (int)(set / a.row_tiles) * N;
   const char* xop = a.xop + (size_t)rt * KB * XB;
   const char* xsc = reinterpret_cast<const char*>(a.xsc + (size_t)rt * KB * 32);
-  const float* sw = a.s + (size_t)(min(n0 + wn * 32 * CN, a.N - 1) / 128) * KB;
   const uint8_t* wbase = a.w + (size_t)n0 * a.K;
   // What lies behind the last weight row repeats it; what lies beyond K repeats
   // the row's end, and meets zeros of x.
   const int wlast = a.N - 1 - n0;
   const uint32_t xlen = (uint32_t)KB * XB;   // bytes of a row tile
-  auto load = [&](int b) __attribute__((always_inline)) {
-    const uint32_t k = (uint32_t)min(b * 128 + ((lane & 7) ^ (lane >> 3)) * 16, a.K - 16);
-    const char* wl = lds + (b & 1) * WL + wave * 1024 * WI;
+  auto load = [&](int b, int stage) __attribute__((always_inline)) {
+    const uint32_t to = lds0 + F8T_SW + (uint32_t)(stage * T::STAGE);
 #pragma unroll
-    for (int i = 0; i < WI; ++i) f8_to_lds(wbase, (uint32_t)min((wave * WI + i) * 8 + (lane >> 3), wlast) * (uint32_t)a.K + k, wl + i * 1024);
+    for (int i = 0; i < WI; ++i) {
+      const int unit = (lane & 7) ^ (((i & 1) << 2) + (lane >> 4));   // rows (wave WI + i) 8 + lane / 8
+      f8_to_lds(wbase, (uint32_t)min((wave * WI + i) * 8 + (lane >> 3), wlast) * (uint32_t)a.K + (uint32_t)min(b * 128 + unit * 16, a.K - 16),
+                to + (wave * WI + i) * 1024);
+    }
     const char* from = xop + (size_t)b * XB;
-    const char* xl = lds + XAT + (b & 1) * XL;
 #pragma unroll
     for (int i = 0; i < XI; ++i) {
       const int at = (i * 8 + wave) * 1024, m = at / XB;
-      f8_to_lds(from + ((size_t)m * xlen + at % XB), lane * 16, xl + at);
+      f8_to_lds(from + ((size_t)m * xlen + at % XB), lane * 16, to + WL + at);
     }
-    if (wave < MT)   // the scales of two row tiles
-      f8_word_to_lds(xsc + ((size_t)wave * 2 * KB + b) * 128, (uint32_t)(lane >> 5) * (uint32_t)KB * 128 + (lane & 31) * 4, lds + SAT + (b & 1) * SL + wave * 256);
+    // The scales of two row tiles (every wavefront loads some, so that all wait for the same number of loads).
+    const int st = min(wave, MT - 1) * 2;
+    f8_word_to_lds(xsc + ((size_t)st * KB + b) * 128, (uint32_t)(lane >> 5) * (uint32_t)KB * 128 + (lane & 31) * 4, to + WL + T::XL + wave * 256);
   };
   f32x16 tot[CN][MT];
 #pragma unroll
@@ -443,27 +452,35 @@ __global__ __launch_bounds__(F8T_NT, 2) void f8_tile_kernel(F8Args a) {
 #pragma unroll
   for (int r = 0; r < 16; ++r) zero[r] = 0.0f;
 
-  float swn = sw[0];
-  load(0);
+  // The weights' scales of the workgroup's one or two blocks of 128 rows.
+  float* sws = reinterpret_cast<float*>(lds);
+  for (int i = tid; i < CN * KB; i += F8T_NT) sws[i] = a.s[(size_t)min(n0 / 128 + i / KB, (a.N - 1) / 128) * KB + i % KB];
+  f8_landed<0>();
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i)
+    if (i < KB) load(i, i);
+  int stage = 0;
   for (int b = 0; b < KB; ++b) {
-    f8_landed();       // this wavefront's loads of the block
-    __syncthreads();   // and everyone's; the other buffers have been read
-    const float swb = swn;
+    // This wavefront's loads of the block have landed, and everyone's; the buffer
+    // of the block before has been read.
+    if (b + AHEAD <= KB) f8_landed<T::LOADS * (AHEAD - 1)>();
+    else f8_landed<0>();
+    __syncthreads();
+    const float swb = sws[(CN > 1 ? wn >> 1 : 0) * KB + b];
     asm volatile("" : "+v"(lane));   // what follows from it is formed again in each block: registers are short
     const int l32 = lane & 31, half = lane >> 5;
-    // Unit 4 half + q of a row, q = 0..3, lies at position (4 half ^ row % 8) ^ q.
-    const uint32_t wl = (uint32_t)((b & 1) * WL + (wn * 32 * CN + l32) * 128 + (((half * 4) ^ (l32 & 7)) << 4));
-    const char* xl = lds + XAT + (b & 1) * XL + wr * MT * XB + lane * 16;
-    const float* sl = reinterpret_cast<const float*>(lds + SAT + (b & 1) * SL + wr * MT * 128) + l32;
+    const uint32_t at = (uint32_t)(F8T_SW + stage * T::STAGE);
+    // Unit 4 half + q of a row, q = 0..3, lies at position (4 half ^ row / 2 % 8) ^ q.
+    const uint32_t wl = at + (uint32_t)((wn * 32 * CN + l32) * 128), wq = (uint32_t)(((half * 4) ^ (l32 >> 1 & 7)) << 4);
+    const char* xl = lds + at + WL + wr * MT * XB + lane * 16;
+    const float* sl = reinterpret_cast<const float*>(lds + at + WL + T::XL + wr * MT * 128) + l32;
     i32x4 wv[CN][4];
     auto read_w = [&](int c, int q) __attribute__((always_inline)) {
-      wv[c][q] = *reinterpret_cast<const i32x4*>(lds + (wl ^ (q << 4)) + c * 4096);
+      wv[c][q] = *reinterpret_cast<const i32x4*>(lds + wl + (wq ^ (q << 4)) + c * 4096);
     };
-    auto next = [&]() __attribute__((always_inline)) {   // the next block's loads
-      if (b + 1 < KB) {
-        swn = sw[b + 1];
-        load(b + 1);
-      }
+    auto next = [&]() __attribute__((always_inline)) {   // the loads of the block furthest ahead
+      if (b + AHEAD < KB) load(b + AHEAD, stage == 0 ? AHEAD : stage - 1);
+      stage = stage == AHEAD ? 0 : stage + 1;
     };
     if constexpr (F8) {
       // What the first products need is read first, then the next block's loads
@@ -541,7 +558,7 @@ __global__ __launch_bounds__(F8T_NT, 2) void f8_tile_kernel(F8Args a) {
   const int l32 = lane & 31, half = lane >> 5;
   const int nw = n0 + wn * 32 * CN, cols = min(a.N - nw, 32 * CN);
   const int es = a.out_bf16 ? 2 : 4, pitch = 32 * CN * es + 16;
-  char* mine = lds + wave * (32 * (32 * CN * 4 + 16));
+  char* mine = lds + F8T_SW + wave * 32 * T::PITCH;
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     char* put = mine + l32 * pitch;

@@ -189,14 +189,14 @@ namespace sl {
 constexpr int MAX_DEVICES = 64;
 static hipError_t lds_limit(const void* kernel, int bytes) {
   static std::mutex mu;
-  static struct { const void* kernel; uint64_t devices; } done[16];
+  static struct { const void* kernel; uint64_t devices; } done[32];
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return e;
   if (dev < 0 || dev >= MAX_DEVICES) return hipErrorInvalidDevice;
   std::lock_guard<std::mutex> lk(mu);
   int i = 0;
-  while (i < 15 && done[i].kernel && done[i].kernel != kernel) ++i;
+  while (i < 31 && done[i].kernel && done[i].kernel != kernel) ++i;
   if (done[i].kernel == kernel && (done[i].devices >> dev & 1)) return hipSuccess;
   if ((e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes)) != hipSuccess) return e;
   if (done[i].kernel != kernel) done[i].devices = 0;
@@ -255,14 +255,29 @@ static F8Plan f8_plan(int out_dtype, int R, int K) {
 // The kernel's LDS limit is raised once per device, whatever call comes first.
 template <int CN, int MT, bool F8>
 static hipError_t launch_f8_tile(F8Args a, hipStream_t st) {
-  constexpr int least = 8 * 32 * (32 * CN * 4 + 16), lds = f8_tile_lds<CN, MT, F8>() > least ? f8_tile_lds<CN, MT, F8>() : least;
-  static_assert(lds <= 160 * 1024, "a workgroup's LDS");
-  const hipError_t e = lds_limit(reinterpret_cast<const void*>(&f8_tile_kernel<CN, MT, F8>), lds);
+  typedef F8Tile<CN, MT, F8> T;
+  const hipError_t e = lds_limit(reinterpret_cast<const void*>(&f8_tile_kernel<CN, MT, F8>), T::LDS);
   if (e != hipSuccess) return e;
-  const long long sets = (long long)((a.N + 128 * CN - 1) / (128 * CN)) * a.row_tiles;
+  const long long sets = (long long)((a.N + T::N - 1) / T::N) * a.row_tiles;
   a.per_xcd = (int)((sets + 7) / 8);
-  hipLaunchKernelGGL((f8_tile_kernel<CN, MT, F8>), dim3((unsigned)a.per_xcd * 8), dim3(F8T_NT), lds, st, a);
+  hipLaunchKernelGGL((f8_tile_kernel<CN, MT, F8>), dim3((unsigned)a.per_xcd * 8), dim3(F8T_NT), T::LDS, st, a);
   return hipGetLastError();
+}
+
+// Column tiles of 256 or 128 weight rows, a workgroup a CU: whichever takes the
+// least time in whole rounds of the chip, a tile of 128 counted as 0.55 of one of
+// 256, from four row tiles a wavefront on (whose operands it reads for half the
+// products) as 0.62.  In us, 256 and 128 (K = 4096):
+//   N=32000:   R=64  54.6, 38.7   R=128  60.2, 39.5   R=320  83.4, 65.4
+//   N=152064:  R=64   178,  164   R=128   194,  170   R=320   279,  297
+static bool f8_wide(const F8Args& a, int mt) {
+  const long long wide = (long long)((a.N + 255) / 256) * a.row_tiles, narrow = (long long)((a.N + 127) / 128) * a.row_tiles;
+  return (wide + 255) / 256 * 100 <= (narrow + 255) / 256 * (mt >= 4 ? 62 : 55);
+}
+
+template <int MT, bool F8>
+static hipError_t launch_f8_tile(const F8Args& a, hipStream_t st) {
+  return f8_wide(a, MT) ? launch_f8_tile<2, MT, F8>(a, st) : launch_f8_tile<1, MT, F8>(a, st);
 }
 
 template <typename XT>
@@ -281,14 +296,14 @@ static hipError_t launch_f8(F8Args a, const F8Plan& p, hipStream_t st) {
   if (e != hipSuccess) return e;
   if (p.f8) {
     switch (p.mt) {
-      case 1: return launch_f8_tile<2, 1, true>(a, st);
-      case 2: return launch_f8_tile<2, 2, true>(a, st);
-      case 3: return launch_f8_tile<2, 3, true>(a, st);
-      case 4: return launch_f8_tile<2, 4, true>(a, st);
-      default: return launch_f8_tile<2, 5, true>(a, st);
+      case 1: return launch_f8_tile<1, true>(a, st);
+      case 2: return launch_f8_tile<2, true>(a, st);
+      case 3: return launch_f8_tile<3, true>(a, st);
+      case 4: return launch_f8_tile<4, true>(a, st);
+      default: return launch_f8_tile<5, true>(a, st);
     }
   }
-  return p.mt == 1 ? launch_f8_tile<2, 1, false>(a, st) : launch_f8_tile<2, 2, false>(a, st);
+  return p.mt == 1 ? launch_f8_tile<1, false>(a, st) : launch_f8_tile<2, false>(a, st);
 }
 
 }  // namespace sl
