@@ -114,8 +114,14 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+# torch.cuda.current_stream makes a Stream object; the handle is all that is needed.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream_handle(stream) -> Optional[int]:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device()) or None
         stream = torch.cuda.current_stream()
     h = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     return h or None
@@ -164,8 +170,8 @@ def spec_verify_workspace_init(workspace: torch.Tensor, B: int, gamma_max: int, 
 
 
 def _check(t: Optional[torch.Tensor], name: str, dtype, shape, device):
-    if t is None:
-        return
+    if t is None or (t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()):
+        return   # (these checks are a good part of a small call's time)
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if tuple(t.shape) != tuple(shape):
