@@ -297,6 +297,14 @@ def _logits_buffer(head, hidden, buffer, shape, dtype, dev, stream):
     return out
 
 
+def _on_device(dev: torch.device, call) -> int:
+    """call() with the tensors' device as the current one."""
+    if torch.cuda.device_count() == 1 or dev.index == torch.cuda.current_device():
+        return call()
+    with torch.cuda.device(dev):
+        return call()
+
+
 def spec_verify_min_p_workspace_bytes(B: int, gamma_max: int, V: int, dtype: int) -> int:
     return int(lib().spec_verify_min_p_workspace_bytes(B, gamma_max, V, dtype))
 
@@ -370,11 +378,11 @@ class Verifier:
         if min_p is None:
             _enqueue_verify(*args, self.workspace, stream, lenience, self.hints, *sizes)
             return self.tokens, self.n_accepted, self.alpha, self.pq
-        rc = lib().spec_verify_min_p(_ptr(p_logits), _ptr(q_logits), dt, _ptr(draft_tokens), _ptr(gamma_len), _ptr(uniforms),
+        rc = _on_device(p_logits.device, lambda: lib().spec_verify_min_p(_ptr(p_logits), _ptr(q_logits), dt, _ptr(draft_tokens), _ptr(gamma_len), _ptr(uniforms),
                                      _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(lenience),
                                      self.min_p_hints, B, G, V, _ptr(self.tokens), _ptr(self.n_accepted), _ptr(self.alpha),
                                      _ptr(self.pq), _ptr(self.min_p_workspace), self.min_p_workspace.numel(),
-                                     _stream_handle(stream))
+                                     _stream_handle(stream)))
         if rc != SV_OK:
             raise SpecVerifyError(rc, "spec_verify_min_p")
         return self.tokens, self.n_accepted, self.alpha, self.pq
@@ -505,6 +513,8 @@ class Sampler:
             _check(min_p, "min_p", torch.float32, (R,), dev)
             if self.min_p_workspace is None:
                 raise ValueError("min_p needs a Sampler(min_p=True)")
+            if dev != self.tokens.device:
+                raise ValueError(f"logits are on {dev}, the sampler's workspace on {self.tokens.device}")
             if self.hints & ~SV_HINT_ALL_MIN_P:
                 raise ValueError("the sampler takes no other hint than SV_HINT_ALL_MIN_P")
         if processor is not None:   # after every check: a call that is refused leaves the logits as they were
@@ -516,9 +526,9 @@ class Sampler:
             processor(logits, draft_tokens, 0 if draft_tokens is None else draft_tokens.shape[1], mask_rows,
                       stream=stream)
         if min_p is not None:
-            rc = lib().spec_sample_min_p(_ptr(logits), dt, _ptr(uniforms), _ptr(temperature), _ptr(top_k), _ptr(top_p),
+            rc = _on_device(dev, lambda: lib().spec_sample_min_p(_ptr(logits), dt, _ptr(uniforms), _ptr(temperature), _ptr(top_k), _ptr(top_p),
                                          _ptr(min_p), self.hints, R, V, _ptr(self.tokens), _ptr(self.prob),
-                                         _ptr(self.min_p_workspace), self.min_p_workspace.numel(), _stream_handle(stream))
+                                         _ptr(self.min_p_workspace), self.min_p_workspace.numel(), _stream_handle(stream)))
             if rc != SV_OK:
                 raise SpecVerifyError(rc, "spec_sample_min_p")
             return self.tokens

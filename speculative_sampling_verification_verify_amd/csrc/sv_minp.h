@@ -20,9 +20,9 @@
 //                         none of the first, minp_left_kernel in place of the
 //                         three, one workgroup a sequence
 //
-// Probabilities, normalisers and nucleus masses are held in 64 bits (the masses
-// as fixed-point numbers, whose sum does not depend on its order), so that a
-// decision differs from the exact one only within about 1e-12 of its border.
+// Probabilities and normalisers are held in 64 bits, nucleus masses as multiples
+// of 2^-42 of the largest value's (whole numbers, whose sum does not depend on
+// its order): what decides is within V 2^-42 of its exact value.
 #pragma once
 
 #include "sv_common.h"
@@ -402,9 +402,9 @@ __device__ __forceinline__ unsigned long long mp_fixed(double e) { return (unsig
 
 // The largest key t with mass(key >= t) >= tau, of the keys that feed gives
 // (with their masses; `above`: the mass of those it leaves out, all larger), a
-// radix select from the top digit down; 0 if there is none.
+// radix select from the top digit down; 0 if there is none.  *mass: mass(key >= t).
 template <int LEVELS, int NTHR, class Feed>
-__device__ __forceinline__ uint32_t mp_nucleus(Feed feed, unsigned long long above, double tau, MinpScratch& s) {
+__device__ __forceinline__ uint32_t mp_nucleus(Feed feed, unsigned long long above, double tau, MinpScratch& s, unsigned long long* mass) {
   uint32_t prefix = 0, pmask = 0;
   for (int lvl = 0; lvl < LEVELS; ++lvl) {
     const int shift = 8 * (LEVELS - 1 - lvl);
@@ -441,18 +441,25 @@ __device__ __forceinline__ uint32_t mp_nucleus(Feed feed, unsigned long long abo
           for (int q = 0; q <= i; ++q) upto += c[q];
           if ((double)upto >= tau) d = i;
         }
+        unsigned long long at = 0;
 #pragma unroll
-        for (int q = 0; q < 3; ++q)
+        for (int q = 0; q < 4; ++q) {
           if (q < d) run += c[q];
+          if (q == d) at = c[q];
+        }
+        at += run;
         s.bc[0] = (uint32_t)(first - d);
         s.bc[1] = (uint32_t)run;
         s.bc[2] = (uint32_t)(run >> 32);
+        s.bc[5] = (uint32_t)at;
+        s.bc[6] = (uint32_t)(at >> 32);
       }
       if (lane == 0 && hit < 0) s.bc[0] = NONE;
     }
     mp_sync<NTHR>();
     const uint32_t d = s.bc[0];
     above = ((unsigned long long)s.bc[2] << 32) | s.bc[1];
+    *mass = ((unsigned long long)s.bc[6] << 32) | s.bc[5];
     if (d == NONE) return 0;
     prefix |= d << shift;
     pmask |= 255u << shift;
@@ -481,6 +488,7 @@ __device__ __forceinline__ double mp_filter(Feed feed, const MinpMode& mm, uint3
   const bool nucleus = mm.m.tp < 1.0f && mm.m.tp > 0.0f;
   if (mm.m.tp <= 0.0f) *thr = kmax;
   double S = 0.0;
+  unsigned long long mass;
 #pragma unroll 1
   for (int pass = 0; pass < (nucleus ? 2 : 1); ++pass) {
     if (pass == 1) {
@@ -488,7 +496,7 @@ __device__ __forceinline__ double mp_filter(Feed feed, const MinpMode& mm, uint3
         feed([&](uint32_t key, double e) {
           if (key >= *thr) fn(key, e);
         });
-      }, 0ull, (double)mm.m.tp * S * (double)(1ull << MP_FIX), s);
+      }, 0ull, (double)mm.m.tp * S * (double)(1ull << MP_FIX), s, &mass);
       *thr = max(*thr, t);
     }
     double x = 0.0;
@@ -548,7 +556,7 @@ __device__ __forceinline__ void mp_for_row(const ET* row, int V, F fn) {
 
 // A row's distribution; false: it has no valid one.  Passes over the row: its
 // maximum; the sum, with the masses by bins of the value; the keys of the bin in
-// which the nucleus ends; the sum of what is kept.
+// which the nucleus ends.
 template <typename ET, int NTHR>
 __device__ __forceinline__ bool mp_row_stats(const ET* row, int V, const MinpMode& mm, MinpScratch& s, uint32_t* few, int cap, MinpRow* out) {
   constexpr int VEC = Key<ET>::VEC;
@@ -626,24 +634,21 @@ __device__ __forceinline__ bool mp_row_stats(const ET* row, int V, const MinpMod
       __syncthreads();
       const uint32_t found = s.bc[3];
       uint32_t t;
+      unsigned long long mass;
       if (found <= (uint32_t)cap) {
         t = mp_nucleus<Key<ET>::LEVELS, NTHR>([&](auto fn) {
           for (uint32_t j = threadIdx.x; j < found; j += NTHR) fn(few[j], mp_exp(exponent(few[j])));
-        }, above, tau, s);
+        }, above, tau, s, &mass);
       } else {
         t = mp_nucleus<Key<ET>::LEVELS, NTHR>([&](auto fn) {
           keys([&](uint32_t key) {
             if (of_bin(key)) fn(key, mp_exp(exponent(key)));
           });
-        }, above, tau, s);
+        }, above, tau, s, &mass);
       }
-      if (t > thr) {
+      if (t > thr) {   // what is kept has the mass found (another pass would take as long as the first)
         thr = t;
-        sum = 0.0;
-        keys([&](uint32_t key) {
-          if (key >= thr) sum += mp_exp(exponent(key));
-        });
-        S = mp_sum<NTHR>(sum, s.red);
+        S = (double)mass / (double)(1ull << MP_FIX);
       }
     }
   }
@@ -682,19 +687,31 @@ __device__ __forceinline__ PosRec mp_position_from_rows(const MinpArgs& ma, cons
     *overlap += fmin(p, q);
     return fmax(p - q, 0.0);
   };
-  // fn(key of the target's row, of the draft's, id) for the unit at id v.
-  const auto both = [&](const u32x4& raw, int v, auto fn) {
-    u32x4 other = two ? mp_load(row[1], v, V) : raw;
+  // fn(key of the target's row, of the draft's, id) for the units at id v.
+  const auto both = [&](const u32x4& raw, u32x4 other, int v, auto fn) {
     mp_for_words<ET>(raw, v, [&](uint32_t key, int id) {
       fn(key, mp_key_of<ET>(other, sizeof(ET) == 2 ? (id - v) & 1 : 0), id);
       if (sizeof(ET) == 4 || ((id - v) & 1)) other = u32x4{other.y, other.z, other.w, other.x};
     });
   };
+  const ET* second = two ? row[1] : row[0];
   const auto sums = [&]() {   // of the runs, in s.red; their total
     z = 0.0;
-    mp_for_units(row[0], wave * run + lane * PER, v1, 64 * PER, V, [&](const u32x4& raw, int e) {
-      both(raw, e, [&](uint32_t kp, uint32_t kq, int) { z += weight(kp, kq, &al); });   // (runs end with a unit or the row)
-    });
+    int e = wave * run + lane * PER;
+    u32x4 next0 = {0, 0, 0, 0}, next1 = {0, 0, 0, 0};
+    if (e < v1) {
+      next0 = mp_load(row[0], e, V);
+      next1 = mp_load(second, e, V);
+    }
+#pragma unroll 1
+    for (; e < v1; e += 64 * PER) {   // (runs end with a unit or the row)
+      const u32x4 raw0 = next0, raw1 = next1;
+      if (e + 64 * PER < v1) {
+        next0 = mp_load(row[0], e + 64 * PER, V);
+        next1 = mp_load(second, e + 64 * PER, V);
+      }
+      both(raw0, raw1, e, [&](uint32_t kp, uint32_t kq, int) { z += weight(kp, kq, &al); });
+    }
     return mp_sum<NTHR>(z, s.red);
   };
   double Z = sums();
@@ -722,17 +739,20 @@ __device__ __forceinline__ PosRec mp_position_from_rows(const MinpArgs& ma, cons
     for (; t0 < V && hit == NONE; t0 += NTHR * PER) {
       const int v0 = t0 + (int)threadIdx.x * PER;
       double loc = 0.0, tot, none = 0.0;
-      u32x4 raw = {0, 0, 0, 0};
-      if (v0 < V) raw = mp_load(row[0], v0, V);
+      u32x4 raw = {0, 0, 0, 0}, other = raw;
       const bool some = v0 < V;
-      if (some) both(raw, v0, [&](uint32_t kp, uint32_t kq, int v) {
+      if (some) {
+        raw = mp_load(row[0], v0, V);
+        other = mp_load(second, v0, V);
+      }
+      if (some) both(raw, other, v0, [&](uint32_t kp, uint32_t kq, int v) {
         const double w = weight(kp, kq, &none);
         loc += w;
         if (w > 0.0) last = (uint32_t)(v + 1);
       });
       double c = base + mp_scan<NTHR>(loc, s.red, &tot);
       uint32_t mine = NONE;
-      if (some && c + loc > target) both(raw, v0, [&](uint32_t kp, uint32_t kq, int v) {
+      if (some && c + loc > target) both(raw, other, v0, [&](uint32_t kp, uint32_t kq, int v) {
         const double w = weight(kp, kq, &none);
         c += w;
         if (mine == NONE && w > 0.0 && c > target) mine = (uint32_t)v;
