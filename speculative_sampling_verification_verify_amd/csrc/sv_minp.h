@@ -38,6 +38,7 @@ constexpr int MP_PART_CAP = 512;  // list entries of a row part
 constexpr int MP_ROW_NT = 1024;   // threads of a row workgroup
 constexpr int MP_ROW_GRID = 512;
 constexpr int MP_LEFT_GRID = 256;
+constexpr int MP_QUEUE = 128;
 constexpr int MP_FEW_KEYS = 8192; // keys of one bin that a row workgroup holds
 constexpr int MP_BINS = 256;      // bins of a row's masses, 1/8 wide in (zmax - z) / T; also a digit's
 constexpr int MP_FIX = 42;        // fraction bits of a mass: at most 2^20 masses of at most 1
@@ -659,10 +660,10 @@ __device__ __forceinline__ bool mp_row_stats(const ET* row, int V, const MinpMod
 }
 
 // The position's record from its two rows' distributions (the second is used
-// where the position has a draft).
+// where the position has a draft).  queue: MP_QUEUE entries a wavefront.
 template <typename ET, int NTHR>
 __device__ __forceinline__ PosRec mp_position_from_rows(const MinpArgs& ma, const MinpMode& mm, int b, int i, const MinpRow& r0,
-                                                        const MinpRow& r1, MinpScratch& s) {
+                                                        const MinpRow& r1, MinpScratch& s, uint2* queue) {
   const Args& a = ma.a;
   const int V = a.V;
   const bool two = i < mm.m.g;
@@ -695,23 +696,49 @@ __device__ __forceinline__ PosRec mp_position_from_rows(const MinpArgs& ma, cons
     });
   };
   const ET* second = two ? row[1] : row[0];
-  const auto sums = [&]() {   // of the runs, in s.red; their total
+  // The sums of the runs, in s.red, and their total.  Where a few values are kept,
+  // these first go through a queue of the wavefront's, so that it forms their
+  // probabilities 64 at a time.
+  const bool few = r[0].thr > Key<ET>::NEG_INF + 1;
+  const auto sums = [&]() {
     z = 0.0;
-    int e = wave * run + lane * PER;
+    uint2* mine = queue + wave * MP_QUEUE;
+    int have = 0;
     u32x4 next0 = {0, 0, 0, 0}, next1 = {0, 0, 0, 0};
-    if (e < v1) {
-      next0 = mp_load(row[0], e, V);
-      next1 = mp_load(second, e, V);
+    const int e0 = wave * run;
+    if (e0 + lane * PER < v1) {
+      next0 = mp_load(row[0], e0 + lane * PER, V);
+      next1 = mp_load(second, e0 + lane * PER, V);
     }
 #pragma unroll 1
-    for (; e < v1; e += 64 * PER) {   // (runs end with a unit or the row)
+    for (int t = e0; t < v1; t += 64 * PER) {   // (runs end with a unit or the row)
+      const int e = t + lane * PER;
+      const bool in = e < v1;
       const u32x4 raw0 = next0, raw1 = next1;
       if (e + 64 * PER < v1) {
         next0 = mp_load(row[0], e + 64 * PER, V);
         next1 = mp_load(second, e + 64 * PER, V);
       }
-      both(raw0, raw1, e, [&](uint32_t kp, uint32_t kq, int) { z += weight(kp, kq, &al); });
+      both(raw0, raw1, e, [&](uint32_t kp, uint32_t kq, int) {
+        if (!few) {
+          if (in) z += weight(kp, kq, &al);
+          return;
+        }
+        const bool keep = in && kp >= r[0].thr;
+        const unsigned long long mask = __ballot(keep);
+        if (keep) mine[have + __popcll(mask & ((1ull << lane) - 1))] = make_uint2(kp, kq);
+        have += __popcll(mask);
+        if (have < 64) return;
+        wave_lds_sync();
+        const uint2 now = mine[lane], rest = mine[64 + lane];   // (MP_QUEUE entries)
+        wave_lds_sync();
+        mine[lane] = rest;
+        have -= 64;
+        z += weight(now.x, now.y, &al);
+      });
     }
+    wave_lds_sync();
+    if (lane < have) z += weight(mine[lane].x, mine[lane].y, &al);
     return mp_sum<NTHR>(z, s.red);
   };
   double Z = sums();
@@ -802,6 +829,7 @@ __global__ __launch_bounds__(MP_ROW_NT) void minp_row_kernel(MinpArgs ma) {
 template <typename ET>
 __global__ __launch_bounds__(MP_ROW_NT) void minp_row_position_kernel(MinpArgs ma) {
   __shared__ MinpScratch s;
+  __shared__ uint2 queue[MP_ROW_NT / 64 * MP_QUEUE];
   const Args& a = ma.a;
   const uint32_t n = a.dense_count[0];
   for (uint32_t j = blockIdx.x; j < n; j += gridDim.x) {
@@ -809,7 +837,7 @@ __global__ __launch_bounds__(MP_ROW_NT) void minp_row_position_kernel(MinpArgs m
     const MinpMode mm = minp_mode(ma, b);
     const MinpRow r0 = ma.rows[2 * (size_t)id], r1 = i < mm.m.g ? ma.rows[2 * (size_t)id + 1] : r0;
     PosRec rec{0.0, 0.0, 0.0, -1, 1u};
-    if (r0.thr && r1.thr) rec = mp_position_from_rows<ET, MP_ROW_NT>(ma, mm, b, i, r0, r1, s);
+    if (r0.thr && r1.thr) rec = mp_position_from_rows<ET, MP_ROW_NT>(ma, mm, b, i, r0, r1, s, queue);
     if (threadIdx.x == 0) {
       if (a.sampler) mp_put_sample(ma, b, rec);
       else a.pos[id] = rec;
@@ -1120,7 +1148,8 @@ __global__ __launch_bounds__(MP_POS_NT, 4) void minp_position_kernel(MinpArgs ma
 template <typename ET>
 __global__ __launch_bounds__(MP_POS_NT) void minp_left_kernel(MinpArgs ma) {
   __shared__ MinpScratch s;
-  __shared__ uint32_t few[MP_FEW_KEYS];
+  __shared__ __align__(8) uint32_t few[MP_FEW_KEYS];   // keys, then the queues
+  static_assert(MP_POS_NT / 64 * MP_QUEUE * 2 <= MP_FEW_KEYS, "the queues");
   const Args& a = ma.a;
   const uint32_t n = a.dense_count[0];
   for (uint32_t j = blockIdx.x; j < n; j += gridDim.x) {
@@ -1137,7 +1166,7 @@ __global__ __launch_bounds__(MP_POS_NT) void minp_left_kernel(MinpArgs ma) {
       if (ok && i < mm.m.g) ok = mp_row_stats<ET, MP_POS_NT>(row_ptr<ET>(a, b, false, i), a.V, mm, s, few, MP_FEW_KEYS, &r1);
       __syncthreads();
       PosRec rec{0.0, 0.0, 0.0, -1, 1u};
-      if (ok) rec = mp_position_from_rows<ET, MP_POS_NT>(ma, mm, b, i, r0, r1, s);
+      if (ok) rec = mp_position_from_rows<ET, MP_POS_NT>(ma, mm, b, i, r0, r1, s, reinterpret_cast<uint2*>(few));
       __syncthreads();   // (everyone has read pos[i])
       if (threadIdx.x == 0) {
         if (a.sampler) mp_put_sample(ma, b, rec);
