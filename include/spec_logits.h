@@ -117,8 +117,9 @@ int spec_quantize_f8(const void* x, int x_dtype, int rows, int R, int K, uint8_t
  * even, at the end.  An output in bf16 of more than 64 rows is formed by the matrix cores' 8-bit
  * products, which cut off, in the sum of 8 consecutive k, what lies below 2^-13 of the largest of
  * the 8 products' binade: an error well below a step of bf16 for sums of many products of like
- * size (1e-4 of their norm).  Ask for fp32 where every bit of float32 counts.  A row of `hidden` with a NaN or an infinity gives a row of NaN, a weight
- * code of NaN a column of NaN; others are not affected.
+ * size (1e-4 of their norm).  Ask for fp32 where every bit of float32 counts.
+ * A row of `hidden` with a NaN or an infinity gives a row of NaN, a weight code of NaN a column
+ * of NaN; others are not affected.
  * Returns SV_OK or a negative code (nothing enqueued).
  */
 #define SL_F8 2 /* hidden_dtype: e4m3 codes */

@@ -374,14 +374,15 @@ int spec_verify_spectr(const void* p_logits, const void* q_logits, int dtype, co
  *  min_p        [B] or [R] float: above 0 and at most 1; 0 or less: no min-p; above 1 or NaN makes
  *               the sequence invalid.  NULL: none has min-p.  T = 0 is argmax, whatever min_p is.
  *  hints        0, or SV_HINT_ALL_MIN_P: the caller knows that every sequence has min_p > 0 or
- *               T = 0, and the launches that take the other sequences, row by row, are replaced by one.  One that breaks
- *               the promise, or keeps more than the call's lists hold (1024 values of a row), still
- *               gets its exact result, from a slower path.
+ *               T = 0.  One launch then replaces those that take other sequences row by row.  A
+ *               sequence without, or one that keeps more than the call's lists hold (1024 values
+ *               of a row), still gets its exact result, from that launch, only later.
  *  out_prob     [R] float or NULL: the processed probability of the token drawn (NaN for an invalid
  *               row), which a verify reports as q(x).
  *  workspace    spec_verify_min_p_workspace_bytes(B, gamma_max, V, dtype) bytes (gamma_max = 0 and
- *               B = R rows for spec_sample_min_p), 256-byte aligned.  It needs no preparation and
- *               holds nothing after the call; calls that share one must be ordered.
+ *               B = R rows for spec_sample_min_p), 256-byte aligned; enough for fewer sequences
+ *               too.  It needs no preparation and holds nothing after the call; calls that share
+ *               one must be ordered.
  * Every other argument, the outputs and the error behaviour are those of spec_verify_ex and
  * spec_sample; base pointers need only be aligned to their element.  Probabilities, normalisers and
  * nucleus masses are held in 64 bits.  At most 2^24 row parts of 2^11 to 2^14 values

@@ -16,7 +16,11 @@
 // Up to 16 rows the weight bytes bound: the rows of x are quantised into LDS by
 // every workgroup and the weights are streamed (f8_stream_kernel).  With more
 // rows x is quantised into operand order first (f8_order_kernel), then tiles
-// over rows and columns (f8_tile_kernel).
+// over rows and columns (f8_tile_kernel).  At K = 4096, bf16:
+//   1 row,     N = 152064: 116 us a call, 5.4 TB/s of weight bytes (a 1 GiB copy: 5.05)
+//   320 rows,  N = 128255: 198 us, 1.70 PFLOP/s (the library's product with one scale
+//                          for everything, N = 128256: 260 us)
+//   2048 rows, N = 152064: 1.32 ms, 1.94 PFLOP/s (such a library product: 1.09 ms)
 #pragma once
 
 #include "sl_common.h"
@@ -124,7 +128,9 @@ __device__ __forceinline__ void fq_store(uint8_t* row, int k, int K, uint2 c) {
   }
 }
 
-// A scale for each row and 128 of k: 16 lanes to a block.
+// A scale for each row and 128 of k: 16 lanes to a block, whose values are in
+// registers from the one read to the write.  Memory bounds it: 128256 x 4096 in bf16
+// with a scale a tile (below) takes 301 us, 1.58 GB at 5.2 TB/s.
 template <typename XT, bool WIDE>
 __global__ __launch_bounds__(FQ_NT) void quantize_rows_kernel(F8QuantArgs a) {
   const int u = threadIdx.x & 15;

@@ -25,6 +25,8 @@
 // given, launch 1 only lists the pairs and launch 2 is mixed_hist_kernel,
 // which streams the select units as well (see sv_phist.h).
 //
+// The calls with min-p are other launches: see sv_minp.h.
+//
 // Definitions followed (page titles and sections): the acceptance rule and
 // the residual, "Fast Inference from Transformers via Speculative Decoding"
 // (mtandhj.com summary), "Speculative Sampling: theoretical basis"; the
@@ -967,14 +969,18 @@ struct MinpPlan {
 // Row parts of 32 KB; of 8 KB in calls of few, which then spread over the chip.
 constexpr long long MP_FEW = 1024;
 
+// (A row may begin up to a unit behind the first part's start.)
+static int minp_parts(int V, int dtype, int vpl) {
+  const int vec = dtype == SV_BF16 ? 8 : 4, part = MP_NT * vpl * vec;
+  return (V + vec - 1 + part - 1) / part;
+}
+
 static MinpPlan minp_plan(int B, int G, int V, int dtype) {
   MinpPlan p;
   const int vec = dtype == SV_BF16 ? 8 : 4;
   const size_t rows = (size_t)B * (2 * G + 1), np = (size_t)B * (G + 1);
-  // (a row may begin up to a unit behind the first part's start)
-  const auto parts = [&](int vpl) { return (V + vec - 1 + MP_NT * vpl * vec - 1) / (MP_NT * vpl * vec); };
-  p.vpl = (long long)rows * parts(8) < MP_FEW ? 2 : 8;
-  p.NP = parts(p.vpl);
+  p.vpl = (long long)rows * minp_parts(V, dtype, 8) < MP_FEW ? 2 : 8;
+  p.NP = minp_parts(V, dtype, p.vpl);
   p.PL = MP_NT * p.vpl * vec;
   const size_t units = rows * p.NP;
   const auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
@@ -991,7 +997,12 @@ static MinpPlan minp_plan(int B, int G, int V, int dtype) {
 
 static size_t minp_bytes(int B, int G, int V, int dtype) {
   if (B < 0 || G < 0 || G > SV_MAX_GAMMA || V < 1 || V > SV_MAX_VOCAB || (dtype != SV_BF16 && dtype != SV_FP32)) return 0;
-  return B == 0 ? 256 : minp_plan(B, G, V, dtype).total;
+  if (B == 0) return 256;
+  // Enough for fewer sequences too: the short parts of a smaller call take more lists.
+  size_t total = minp_plan(B, G, V, dtype).total;
+  const int few = (int)((MP_FEW - 1) / ((2 * G + 1) * minp_parts(V, dtype, 8)));
+  if (few >= 1 && few < B && minp_plan(few, G, V, dtype).total > total) total = minp_plan(few, G, V, dtype).total;
+  return total;
 }
 
 template <typename ET>

@@ -127,6 +127,20 @@ def test_real_values(R, K, N, x, out):
     assert not bad.any(), (R, K, N, np.argwhere(bad)[:4], np.abs(got - ref).max())
 
 
+@pytest.mark.parametrize("R,out", [(1, "bf16"), (2, "fp32"), (70, "bf16")])
+def test_the_longest_k(R, out):
+    """K = 2^16: not even one row fits the streaming kernel's LDS.  Integers, as above."""
+    rng = np.random.default_rng(R)
+    K, N = L.SL_MAX_K, 140
+    KB = K // 128
+    h, w = (f8.encode(rng.integers(-2, 3, (n, K)).astype(np.float32)) for n in (R, N))
+    hs = (2.0 ** rng.integers(0, 3, (R, KB))).astype(np.float32)
+    ws = (2.0 ** rng.integers(-3, 2, (2, KB))).astype(np.float32)
+    assert 128 * 2 * 2 * 4 * 2 * KB * 8 <= 2 ** 24
+    got = L.spec_logits_f8(dev(h).view(torch.float8_e4m3fn), dev(w), dev(ws), dev(hs), out_dtype=TYPES[out])
+    assert torch.equal(got.cpu(), torch.from_numpy(f8.product(h, hs, w, ws)[0]).float().to(TYPES[out]))
+
+
 @pytest.mark.parametrize("R", [3, 40, 300])
 def test_given_codes_are_the_same_call(R):
     """Hidden states quantised before the call give the same bits."""

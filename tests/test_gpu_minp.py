@@ -68,6 +68,57 @@ def test_sample(V, dtype, hints):
     assert check_sample(logits(rng, (R, V), dtype), rng.random(R).astype(np.float32), s, hints) > 0.9
 
 
+@pytest.mark.parametrize("hints", [0, binding.SV_HINT_ALL_MIN_P])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_the_longest_rows(dtype, hints):
+    """2^20 values: a row alone has more parts than a position's workgroup has threads."""
+    rng = np.random.default_rng(5)
+    R, V = 3, 1 << 20
+    z = logits(rng, (R, V), dtype)
+    s = dict(T=np.array([1.0, 0.7, 1.0], np.float32), top_k=np.array([0, 40, 0], np.int32),
+             top_p=np.array([1.0, 0.9, 0.95], np.float32), min_p=np.array([0.1, 0.02, 0.0], np.float32))
+    z[:, -1] = z[:, 5] = 16.0   # kept in the first and in the last part
+    for r in range(R):          # (one row, whose parts are the shortest, and three)
+        one = {k: v[r:r + 1] for k, v in s.items()}
+        assert check_sample(z[r:r + 1].contiguous(), rng.random(1).astype(np.float32), one, hints) == 1.0
+    u = np.array([0.99, 0.01, 0.5], np.float32)
+    check_sample(z, u, s, hints)
+
+
+def test_a_workspace_of_more_sequences():
+    """The C calls take a larger batch's workspace, whose parts are longer."""
+    rng = np.random.default_rng(6)
+    V, big, R = 32001, 700, 9
+    ws = torch.empty(binding.spec_verify_min_p_workspace_bytes(big, 0, V, binding.SV_BF16), dtype=torch.uint8, device="cuda")
+    z, s, u = logits(rng, (R, V), "bf16"), settings(rng, R), rng.random(R).astype(np.float32)
+    want = sample(z, u, s)
+    call = binding.Sampler(R, V, min_p=True)
+    call.min_p_workspace = ws
+    got = call(z, dev(u), dev(s["T"]), dev(s["top_k"]), dev(s["top_p"]), min_p=dev(s["min_p"]))
+    assert (got.cpu().numpy() == want[0]).all()
+    np.testing.assert_array_equal(call.prob.cpu().numpy(), want[1])
+
+
+def test_calls_on_two_streams_at_once():
+    """Each with its own workspace, while the other runs."""
+    rng = np.random.default_rng(8)
+    R, V = 300, 32001
+    cases = []
+    for _ in range(2):
+        z, s, u = logits(rng, (R, V), "bf16"), settings(rng, R), rng.random(R).astype(np.float32)
+        cases.append((z, [dev(u), dev(s["T"]), dev(s["top_k"]), dev(s["top_p"])], dev(s["min_p"]), sample(z, u, s)))
+    calls = [binding.Sampler(R, V, min_p=True) for _ in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for (z, args, mp, _), call, st in zip(cases, calls, streams):
+            call(z, *args, min_p=mp, stream=st)
+    torch.cuda.synchronize()
+    for (_, _, _, want), call in zip(cases, calls):
+        assert (call.tokens.cpu().numpy() == want[0]).all()
+        np.testing.assert_array_equal(call.prob.cpu().numpy(), want[1])
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_sample_many_rows(dtype):
     """Enough rows for the longer parts."""

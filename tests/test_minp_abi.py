@@ -37,6 +37,14 @@ def test_workspace():
         assert need(*bad) == 0, bad
 
 
+def test_workspace_serves_smaller_batches():
+    """Also where a smaller batch is cut into shorter parts, which take more lists."""
+    for dt in (Bn.SV_BF16, Bn.SV_FP32):
+        for G, V in ((0, 1), (0, 32000), (4, 128256), (7, 152064), (64, 1000), (1, 1 << 20), (64, 1 << 20)):
+            sizes = [need(B, G, V, dt) for B in range(1, 300)] + [need(B, G, V, dt) for B in (500, 1000, 1023, 1024, 1025, 4096)]
+            assert sizes == sorted(sizes), (G, V, dt)
+
+
 def test_verify_refusals():
     assert verify(B=0) == Bn.SV_OK
     assert verify(dt=3) == verify(G=65) == verify(V=(1 << 20) + 1) == Bn.SV_ERR_UNSUPPORTED
