@@ -966,8 +966,13 @@ struct MinpPlan {
   size_t flags_off, pos_off, rows_off, redo_off, max_off, count_off, list_off, total;
 };
 
-// Row parts of 32 KB; of 8 KB in calls of few, which then spread over the chip.
-constexpr long long MP_FEW = 1024;
+// Row parts of 32 KB; of 8 KB in calls of few, whose reads then spread over the
+// chip, and for rows of at most two such, of which a long part would be mostly
+// padding.  (Else the more lists of a row cost the position kernel more than the
+// cut gains.)  In us, samplers with min-p, parts of 32 and of 8 KB:
+//   bf16  1 x 152064  13.3, 11.4    4 x 152064  19.0, 15.6    8 x 152064  21.5, 23.9    250 x 32000  17.2, 18.1
+//   fp32  2000 x 1000 18.9, 14.8    2000 x 3000 20.8, 18.9    2000 x 5000 22.5, 23.2
+constexpr long long MP_FEW = 64;
 
 // (A row may begin up to a unit behind the first part's start.)
 static int minp_parts(int V, int dtype, int vpl) {
@@ -979,7 +984,7 @@ static MinpPlan minp_plan(int B, int G, int V, int dtype) {
   MinpPlan p;
   const int vec = dtype == SV_BF16 ? 8 : 4;
   const size_t rows = (size_t)B * (2 * G + 1), np = (size_t)B * (G + 1);
-  p.vpl = (long long)rows * minp_parts(V, dtype, 8) < MP_FEW ? 2 : 8;
+  p.vpl = (long long)rows * minp_parts(V, dtype, 8) < MP_FEW || minp_parts(V, dtype, 2) <= 2 ? 2 : 8;
   p.NP = minp_parts(V, dtype, p.vpl);
   p.PL = MP_NT * p.vpl * vec;
   const size_t units = rows * p.NP;
@@ -1064,7 +1069,8 @@ static int run_minp(const void* p_logits, const void* q_logits, int dtype, const
   a.NP = p.NP;
   a.PL = p.PL;
   // Rows to sample of a workgroup: one where they fit the chip at once (its long
-  // lists then wait for nobody), up to one a wavefront.
+  // lists then wait for nobody), up to one a wavefront.  In us, fp32 rows of 1000,
+  // always one and so: 1000 rows 17.0, 13.2; 2000 rows 27.2, 14.8; 4000 rows 47.7, 19.5.
   a.split = (B + 511) / 512;
   a.split = a.split > MP_POS_WAVES ? MP_POS_WAVES : a.split;
   a.out_tokens = out_tokens;

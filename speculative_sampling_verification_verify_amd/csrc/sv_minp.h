@@ -131,8 +131,7 @@ __device__ __forceinline__ uint32_t mp_key_from(double c) {
 // exp(x) for x <= 0 in 64 bits: 2^k times the Taylor polynomial of exp on
 // [-ln 2 / 2, ln 2 / 2], whose 13th term is below 2^-53.
 __device__ __forceinline__ double mp_exp(double x) {
-  const double y = x;
-  x = fmax(x, -746.0);   // (no branch: -inf, too, takes this way)
+  x = fmax(x, -746.0);   // -inf, too: 2^-1076 and a bit, which ldexp rounds to 0
   const double k = rint(x * 1.4426950408889634);
   const double r = fma(k, -0x1.cf79abc9e3b3ap-40, fma(k, -0x1.62e42fefap-1, x));   // ln 2 in two parts, the first of 36 bits
   double p = 1.0 / 6227020800.0;
@@ -149,7 +148,7 @@ __device__ __forceinline__ double mp_exp(double x) {
   p = fma(p, r, 0.5);
   p = fma(p, r, 1.0);
   p = fma(p, r, 1.0);
-  return y > -745.0 ? ldexp(p, (int)k) : 0.0;
+  return ldexp(p, (int)k);
 }
 
 // ---------------------------------------------------------------------------
@@ -408,7 +407,11 @@ struct MinpScratch {
   uint32_t bc[8];
 };
 
-__device__ __forceinline__ unsigned long long mp_fixed(double e) { return (unsigned long long)(e * (double)(1ull << MP_FIX)); }
+// e in [0, 1] as a multiple of 2^-42, to the nearest: the fraction bits of 2^52 + e 2^42
+// (a conversion to 64-bit integers takes ten instructions).
+__device__ __forceinline__ unsigned long long mp_fixed(double e) {
+  return (unsigned long long)__double_as_longlong(fma(e, (double)(1ull << MP_FIX), 0x1p52)) & ((1ull << 52) - 1);
+}
 
 // The largest key t with mass(key >= t) >= tau, of the keys that feed gives
 // (with their masses; `above`: the mass of those it leaves out, all larger), a

@@ -1,7 +1,7 @@
 """spec_sample_min_p and spec_verify_min_p on the GPU against the float64 oracle.
 
 Probabilities and masses are held in 64 bits on both sides (a mass as a multiple
-of 2^-42, cut off), so tokens and counts have to be equal wherever the oracle's
+of 2^-42), so tokens and counts have to be equal wherever the oracle's
 decision margin is at least that of V masses, 4 V 2^-42 with a factor to spare, and
 there probabilities agree within their rounding to float32 (2^-24)."""
 import numpy as np
