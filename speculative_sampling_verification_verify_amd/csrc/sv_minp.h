@@ -523,11 +523,11 @@ __device__ __forceinline__ double mp_filter(Feed feed, const MinpMode& mm, uint3
 
 // ---------------------------------------------------------------------------
 // One position from the logits, for rows without min-p or whose lists do not hold
-// what is kept.  A pass over a row of 128255 takes 10 to 15 us of a workgroup, of
-// which an exponential in 64 bits for each value is most; so what the passes form
+// what is kept.  A pass over a row of 128255 takes 10 to 40 us of a workgroup, where it
+// forms an exponential in 64 bits for each value; so what the passes form
 // is what they need, once: two exponentials a value at most, fewer behind a nucleus.
-// At 32 such sequences of 8 drafts (17 rows of 128255 each, 140 MB): 123 us for the
-// distributions, 99 us for the positions.  `few` holds `cap` keys.
+// At 32 such sequences of up to 8 drafts (264 rows of 128255 in all, bf16): 120 us for
+// the distributions, 93 us for the positions.  `few` holds `cap` keys.
 // ---------------------------------------------------------------------------
 template <typename ET>
 __device__ __forceinline__ uint32_t mp_key_of(const u32x4& raw, int i) {   // of value i of a unit
@@ -1094,7 +1094,7 @@ __device__ __forceinline__ void mp_finish(const MinpArgs& ma, int b, const Mode&
 }
 
 // One workgroup per sequence, or per a.split rows to sample: 17 us for 256
-// sequences of 7 drafts, 16 us for one.  A wavefront
+// sequences of 7 drafts, 5 us for one row to sample.  A wavefront
 // takes a position whose rows keep at most MinpWave::CAP values each; the whole
 // workgroup takes the longer ones after that, up to MinpBlock::CAP; what then is
 // left goes to other launches, which also finish the sequence: listed by
