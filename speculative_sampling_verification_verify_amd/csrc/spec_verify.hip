@@ -968,11 +968,13 @@ struct MinpPlan {
 
 // Row parts of 32 KB; of 8 KB in calls of few, whose reads then spread over the
 // chip, and for rows of at most two such, of which a long part would be mostly
-// padding.  (Else the more lists of a row cost the position kernel more than the
-// cut gains.)  In us, samplers with min-p, parts of 32 and of 8 KB:
-//   bf16  1 x 152064  13.3, 11.4    4 x 152064  19.0, 15.6    8 x 152064  21.5, 23.9    250 x 32000  17.2, 18.1
-//   fp32  2000 x 1000 18.9, 14.8    2000 x 3000 20.8, 18.9    2000 x 5000 22.5, 23.2
-constexpr long long MP_FEW = 64;
+// padding.  In us, parts of 32 and of 8 KB:
+//   bf16 samplers  1 x 152064  13.5, 10.9    16 x 152064  16.0, 11.9    128 x 152064  19.1, 20.6
+//   verify, 4 drafts, V = 128256  1 sequence  17.3, 15.7    8  18.3, 19.2    16  22.2, 26.1
+//   fp32 samplers  2000 x 1000  18.9, 14.8    2000 x 3000  20.8, 18.9    2000 x 5000  22.5, 23.2
+// Flat rows that keep hundreds of values give more lists to gather, and turn
+// earlier: 4 x 152064  19.0, 15.6    8 x 152064  21.5, 23.9.
+constexpr long long MP_FEW = 512;
 
 // (A row may begin up to a unit behind the first part's start.)
 static int minp_parts(int V, int dtype, int vpl) {
