@@ -109,20 +109,24 @@ int spec_quantize_f8(const void* x, int x_dtype, int rows, int R, int K, uint8_t
  *  scales   [ceil(N / 128)][ceil(K / 128)] float.
  *  R, K, N  R >= 0 and <= SL_MAX_ROWS (R == 0 is a no-op), K a multiple of 16, 16 <= K <= SL_MAX_K,
  *           1 <= N <= SV_MAX_VOCAB.  R * N and R * K below 2^34 (SV_ERR_UNSUPPORTED beyond).
- *  out      [R][N] bf16 or fp32 (out_dtype), aligned to its element; overlaps no input (SV_ERR_ARG).
+ *  out      [R][N] bf16 or fp32 (out_dtype SV_BF16, SL_BF16_F8 or SV_FP32), aligned to its element;
+ *           overlaps no input (SV_ERR_ARG).
  *  workspace  as for spec_logits_w4, of spec_logits_f8_workspace_bytes(out_dtype, R, K)
  *           bytes.
  *
  * The products of the codes are exact; sums are held in float32 and rounded once, to nearest
- * even, at the end.  An output in bf16 of more than 64 rows is formed by the matrix cores' 8-bit
- * products, which cut off, in the sum of 8 consecutive k, what lies below 2^-13 of the largest of
- * the 8 products' binade: an error well below a step of bf16 for sums of many products of like
- * size (1e-4 of their norm).  Ask for fp32 where every bit of float32 counts.
+ * even, at the end.
+ * With out_dtype SL_BF16_F8 the output is bf16, and of more than 64 rows formed by the matrix cores'
+ * 8-bit products, in half the time.  These cut off, in the sum of 8 consecutive k, what lies below
+ * 2^-13 of the largest of the 8 products' binade: for sums of many products of like size an error
+ * of 2.5e-4 of their norm (a step of bf16 is 2^-8), but small products next to large ones that cancel
+ * are lost.
  * A row of `hidden` with a NaN or an infinity gives a row of NaN, a weight code of NaN a column
  * of NaN; others are not affected.
  * Returns SV_OK or a negative code (nothing enqueued).
  */
-#define SL_F8 2 /* hidden_dtype: e4m3 codes */
+#define SL_F8 2      /* hidden_dtype: e4m3 codes                                  */
+#define SL_BF16_F8 4 /* out_dtype: bf16, from 8-bit products where these are faster */
 size_t spec_logits_f8_workspace_bytes(int out_dtype, int R, int K);
 int spec_logits_f8(const void* hidden, int hidden_dtype, const float* hidden_scales, const uint8_t* weights,
                    const float* scales, int R, int K, int N, void* out, int out_dtype, void* workspace,

@@ -8,19 +8,22 @@
 // the products of 8 consecutive codes to the largest and cut off what lies below
 // 2^-13 of its binade (measured, the same for every instruction that takes these
 // codes); only sums of those have 24 bits.  For sums of N(0, 1) values that is an
-// error of about 1e-4 of their norm.  Expanded to bf16, which is exact, the
-// products are summed as float32.  So the codes are multiplied as they are only
-// where the result is rounded to bf16 (2^-9) and the products' rate bounds: more
-// than F8_EXACT_ROWS rows.  Everywhere else they are expanded.
+// error of about 2.5e-4 of their norm, and beside large products that cancel small
+// ones are lost altogether.  Expanded to bf16, which is exact, the products are
+// summed as float32.  So the codes are multiplied as they are only where the caller
+// asks for it (SL_BF16_F8) and the products' rate bounds.  Everywhere else they are
+// expanded.
 //
 // Up to 16 rows the weight bytes bound: the rows of x are quantised into LDS by
 // every workgroup and the weights are streamed (f8_stream_kernel).  With more
 // rows x is quantised into operand order first (f8_order_kernel), then tiles
 // over rows and columns (f8_tile_kernel).  At K = 4096, bf16:
 //   1 row,     N = 152064: 115 us a call, 5.4 TB/s of weight bytes (a 1 GiB copy: 5.05)
-//   320 rows,  N = 128255: 197 us, 1.71 PFLOP/s (the library's product with one scale
+//   320 rows,  N = 128255: 409 us, 0.82 PFLOP/s; with 8-bit products 195 us, 1.72
+//                          PFLOP/s (the library's product of such codes with one scale
 //                          for everything, N = 128256: 260 us)
-//   2048 rows, N = 152064: 1.30 ms, 1.96 PFLOP/s (such a library product: 1.09 ms)
+//   2048 rows, N = 152064: 2.55 ms, 1.00 PFLOP/s; with 8-bit products 1.30 ms, 1.96
+//                          PFLOP/s (such a library product: 1.09 ms)
 #pragma once
 
 #include "sl_common.h"

@@ -222,14 +222,50 @@ static int launch_quantize(const F8QuantArgs& a, int rows, hipStream_t st) {
 }
 
 // The plan of a product, a function of its sizes and types alone: few rows go to
-// the streaming kernel where they fit LDS.
+// the streaming kernel where they fit LDS.  products8: the caller takes the matrix
+// cores' 8-bit products, which pay from the second 64 rows on (us at K = 4096,
+// N = 128255: up to 64 rows 120 expanded; 65 rows 145 expanded, 117 in 8 bits).
 constexpr int F8_EXACT_ROWS = 64;
 
 struct F8Plan {
-  int stream, rp, mt, f8, row_tiles;   // mt: tiles of 32 rows of a wavefront, half of a workgroup's
+  int stream, rp, f8;
+  int cn, mt, row_tiles;   // 128 cn weight rows and 64 mt rows of x a workgroup
   size_t op_bytes, bytes;
 };
-static F8Plan f8_plan(int out_dtype, int R, int K) {
+
+// Tiles of the expanded form: whichever takes the least time in whole rounds of the
+// chip, a workgroup a CU.  A tile (cn, mt) takes about, in us at K = 4096,
+// (1,1) 25, (2,1) 44, (1,2) 42, (2,2) 65; calls, in that order, bf16:
+//   N=32000:   R=64   33,  45,  46,  61   R=128   57,  49,  47,  61   R=192   81,  85,  82,  66
+//              R=320 128, 124, 118, 120   R=448  173, 159, 155, 125   R=2048 799, 673, 656, 523
+//   N=128255:  R=64  126, 120, 177, 145   R=128  216, 195, 186, 157   R=192  310, 278, 340, 269
+//              R=320 494, 443, 503, 397   R=448  683, 603, 669, 527   R=2048 3229, 2767, 2706, 2120
+static void f8_expanded_tiles(F8Plan& p, int R, int N) {
+  static const struct { int cn, mt, us; } tile[] = {{2, 2, 65}, {1, 2, 42}, {2, 1, 44}, {1, 1, 25}};
+  long long best = 0;
+  for (const auto& t : tile) {
+    const int rows = (R + 64 * t.mt - 1) / (64 * t.mt);
+    const long long sets = (long long)((N + 128 * t.cn - 1) / (128 * t.cn)) * rows, us = (sets + 255) / 256 * t.us;
+    if (best && us >= best) continue;
+    best = us;
+    p.cn = t.cn;
+    p.mt = t.mt;
+    p.row_tiles = rows;
+  }
+}
+
+// Column tiles of the 8-bit products, of 256 or 128 weight rows, the same way: a tile
+// of 128 counted as 0.55 of one of 256, from four row tiles a wavefront on (whose
+// operands it reads for half the products) as 0.62.  In us, 256 and 128 (K = 4096):
+//   N=32000:   R=128  60.2, 39.5   R=320  83.4, 65.4
+//   N=152064:  R=128   194,  170   R=320   279,  297
+static bool f8_wide(int row_tiles, int mt, int N) {
+  const long long wide = (long long)((N + 255) / 256) * row_tiles, narrow = (long long)((N + 127) / 128) * row_tiles;
+  return (wide + 255) / 256 * 100 <= (narrow + 255) / 256 * (mt >= 4 ? 62 : 55);
+}
+
+// N only chooses among tiles: `bytes` is enough for every N.
+static F8Plan f8_plan(bool products8, int R, int K, int N) {
   F8Plan p;
   memset(&p, 0, sizeof p);
   const int KB = (K + 127) / 128;
@@ -239,14 +275,21 @@ static F8Plan f8_plan(int out_dtype, int R, int K) {
     p.stream = 1;
     return p;
   }
-  p.f8 = out_dtype == SV_BF16 && R > F8_EXACT_ROWS;
-  // The widest tile that wastes the fewest rows.
-  const int most = p.f8 ? 5 : 2;
-  p.mt = 1;
-  for (int mt = 2; mt <= most; ++mt)
-    if ((R + 64 * mt - 1) / (64 * mt) * mt <= (R + 64 * p.mt - 1) / (64 * p.mt) * p.mt) p.mt = mt;
-  p.row_tiles = (R + 64 * p.mt - 1) / (64 * p.mt);
-  const size_t blocks = (size_t)p.row_tiles * 2 * p.mt * KB;
+  p.f8 = products8 && R > F8_EXACT_ROWS;
+  size_t units;   // of 64 rows
+  if (p.f8) {
+    // The widest tile that wastes the fewest rows.
+    p.mt = 1;
+    for (int mt = 2; mt <= 5; ++mt)
+      if ((R + 64 * mt - 1) / (64 * mt) * mt <= (R + 64 * p.mt - 1) / (64 * p.mt) * p.mt) p.mt = mt;
+    p.row_tiles = (R + 64 * p.mt - 1) / (64 * p.mt);
+    p.cn = f8_wide(p.row_tiles, p.mt, N) ? 2 : 1;
+    units = (size_t)p.row_tiles * p.mt;
+  } else {
+    f8_expanded_tiles(p, R, N);
+    units = (size_t)(R + 127) / 128 * 2;
+  }
+  const size_t blocks = units * 2 * KB;
   p.op_bytes = blocks * (p.f8 ? f8_block_bytes<true>() : f8_block_bytes<false>());
   p.bytes = p.op_bytes + blocks * 128;
   return p;
@@ -264,20 +307,9 @@ static hipError_t launch_f8_tile(F8Args a, hipStream_t st) {
   return hipGetLastError();
 }
 
-// Column tiles of 256 or 128 weight rows, a workgroup a CU: whichever takes the
-// least time in whole rounds of the chip, a tile of 128 counted as 0.55 of one of
-// 256, from four row tiles a wavefront on (whose operands it reads for half the
-// products) as 0.62.  In us, 256 and 128 (K = 4096):
-//   N=32000:   R=64  54.6, 38.7   R=128  60.2, 39.5   R=320  83.4, 65.4
-//   N=152064:  R=64   178,  164   R=128   194,  170   R=320   279,  297
-static bool f8_wide(const F8Args& a, int mt) {
-  const long long wide = (long long)((a.N + 255) / 256) * a.row_tiles, narrow = (long long)((a.N + 127) / 128) * a.row_tiles;
-  return (wide + 255) / 256 * 100 <= (narrow + 255) / 256 * (mt >= 4 ? 62 : 55);
-}
-
 template <int MT, bool F8>
-static hipError_t launch_f8_tile(const F8Args& a, hipStream_t st) {
-  return f8_wide(a, MT) ? launch_f8_tile<2, MT, F8>(a, st) : launch_f8_tile<1, MT, F8>(a, st);
+static hipError_t launch_f8_tile(const F8Args& a, int cn, hipStream_t st) {
+  return cn == 2 ? launch_f8_tile<2, MT, F8>(a, st) : launch_f8_tile<1, MT, F8>(a, st);
 }
 
 template <typename XT>
@@ -296,14 +328,14 @@ static hipError_t launch_f8(F8Args a, const F8Plan& p, hipStream_t st) {
   if (e != hipSuccess) return e;
   if (p.f8) {
     switch (p.mt) {
-      case 1: return launch_f8_tile<1, true>(a, st);
-      case 2: return launch_f8_tile<2, true>(a, st);
-      case 3: return launch_f8_tile<3, true>(a, st);
-      case 4: return launch_f8_tile<4, true>(a, st);
-      default: return launch_f8_tile<5, true>(a, st);
+      case 1: return launch_f8_tile<1, true>(a, p.cn, st);
+      case 2: return launch_f8_tile<2, true>(a, p.cn, st);
+      case 3: return launch_f8_tile<3, true>(a, p.cn, st);
+      case 4: return launch_f8_tile<4, true>(a, p.cn, st);
+      default: return launch_f8_tile<5, true>(a, p.cn, st);
     }
   }
-  return p.mt == 1 ? launch_f8_tile<1, false>(a, st) : launch_f8_tile<2, false>(a, st);
+  return p.mt == 1 ? launch_f8_tile<1, false>(a, p.cn, st) : launch_f8_tile<2, false>(a, p.cn, st);
 }
 
 }  // namespace sl
@@ -334,12 +366,15 @@ extern "C" int spec_quantize_f8(const void* x, int x_dtype, int rows, int R, int
 }
 
 extern "C" size_t spec_logits_f8_workspace_bytes(int out_dtype, int R, int K) {
-  return known(out_dtype) && f8_sizes(R, K) == SV_OK && K % 16 == 0 && R > 0 ? f8_plan(out_dtype, R, K).bytes : 0;
+  const bool products8 = out_dtype == SL_BF16_F8;
+  return (known(out_dtype) || products8) && f8_sizes(R, K) == SV_OK && K % 16 == 0 && R > 0 ? f8_plan(products8, R, K, 1).bytes : 0;
 }
 
 extern "C" int spec_logits_f8(const void* hidden, int hidden_dtype, const float* hidden_scales, const uint8_t* weights,
                               const float* scales, int R, int K, int N, void* out, int out_dtype, void* workspace,
                               size_t workspace_bytes, void* stream) {
+  const bool products8 = out_dtype == SL_BF16_F8;
+  if (products8) out_dtype = SV_BF16;
   if ((!known(hidden_dtype) && hidden_dtype != SL_F8) || !known(out_dtype) || N > SV_MAX_VOCAB) return SV_ERR_UNSUPPORTED;
   const int rc = f8_sizes(R, K);
   if (rc != SV_OK) return rc;
@@ -351,7 +386,7 @@ extern "C" int spec_logits_f8(const void* hidden, int hidden_dtype, const float*
   if (misaligned(hidden, 16) || misaligned(weights, 16) || misaligned(scales, 4) || misaligned(hidden_scales, 4) ||
       misaligned(out, size_of(out_dtype)))
     return SV_ERR_ARG;
-  const F8Plan p = f8_plan(out_dtype, R, K);
+  const F8Plan p = f8_plan(products8, R, K, N);
   if (p.bytes && (!workspace || workspace_bytes < p.bytes || misaligned(workspace, 256))) return SV_ERR_WORKSPACE;
   F8Args a;
   memset(&a, 0, sizeof a);
