@@ -388,6 +388,13 @@ __device__ __forceinline__ void f8_word_to_lds(const void* base, uint32_t off, u
 // All but the last N of this wavefront's loads have landed.
 template <int N> __device__ __forceinline__ void f8_landed() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
 
+// What this wavefront's lanes wrote to LDS before is there for all of them after it.
+__device__ __forceinline__ void f8_wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // Eight wavefronts, four along the weight rows (32 CN of them each) by two along
 // the rows of x (32 MT each).  Weight rows are the products' rows, rows of x
 // their columns: a lane's results share a row of x, hence one scale a block.
@@ -587,6 +594,7 @@ __global__ __launch_bounds__(F8T_NT, 2) void f8_tile_kernel(F8Args a) {
           *reinterpret_cast<f32x4*>(put + n * 4) = v;
         }
       }
+    f8_wave_sync();   // the lanes read what others wrote
     const int row0 = (rt + wr * MT + m) * 32, unit = 16 / es, per = 32 * CN / unit;   // 16-byte units of a row
     char* out = reinterpret_cast<char*>(a.out);
     for (int u = lane; u < 32 * per; u += 64) {
@@ -598,11 +606,12 @@ __global__ __launch_bounds__(F8T_NT, 2) void f8_tile_kernel(F8Args a) {
         __builtin_memcpy(to, from, 16);
       } else {
         for (int e = 0; n + e < cols; ++e) {
-          if (a.out_bf16) reinterpret_cast<uint16_t*>(to)[e] = reinterpret_cast<const uint16_t*>(from)[e];
-          else reinterpret_cast<float*>(to)[e] = reinterpret_cast<const float*>(from)[e];
+          if (a.out_bf16) __builtin_memcpy(to + e * 2, from + e * 2, 2);
+          else __builtin_memcpy(to + e * 4, from + e * 4, 4);
         }
       }
     }
+    f8_wave_sync();   // and have read it before the next row tile's are written
   }
 }
 
