@@ -37,3 +37,34 @@ def test_results_through_lds_are_ordered(tmp_path, form):
     assert kinds.count("write") >= 2 and kinds.count("read") >= 2
     for a, b in zip(kinds, kinds[1:]):
         assert (a, b) not in (("write", "read"), ("read", "write")), kinds
+
+
+def test_loads_into_lds_leave_m0_to_the_compiler(tmp_path):
+    """f8_to_lds and f8_word_to_lds write m0.  A load that the compiler itself sends to LDS behind them goes
+    to its own address again."""
+    code = assembly(tmp_path, """
+__global__ void probe(const char* a, const char* b, char* out) {
+  extern __shared__ __align__(16) char lds[];
+  typedef __attribute__((address_space(3))) void* L;
+  typedef __attribute__((address_space(1))) const void* G;
+  __builtin_amdgcn_global_load_lds((G)(a + threadIdx.x * 16), (L)lds, 16, 0, 0);
+  sl::f8_to_lds(b, threadIdx.x * 16, 4096);
+  __builtin_amdgcn_global_load_lds((G)(a + threadIdx.x * 16), (L)lds, 16, 1024, 0);
+  sl::f8_word_to_lds(b, threadIdx.x * 4, 8192);
+  __builtin_amdgcn_global_load_lds((G)(a + threadIdx.x * 16), (L)lds, 16, 2048, 0);
+  __syncthreads();
+  out[threadIdx.x] = lds[threadIdx.x * 97];
+}
+""")
+    seen = [("asm" if inside else "own", "m0" if re.match(r"s_mov_b32 m0\b", line) else "load")
+            for line, inside in zip(code, _inside_asm(code)) if re.match(r"s_mov_b32 m0\b|global_load_lds", line)]
+    assert seen == [("own", "m0"), ("own", "load"), ("asm", "m0"), ("asm", "load")] + \
+        [("own", "m0"), ("own", "load"), ("asm", "m0"), ("asm", "load")] + [("own", "m0"), ("own", "load")], seen
+
+
+def _inside_asm(code):
+    """Of each line, whether it was written in inline assembly."""
+    inside = False
+    for line in code:
+        inside = line == ";;#ASMSTART" or inside and line != ";;#ASMEND"
+        yield inside
