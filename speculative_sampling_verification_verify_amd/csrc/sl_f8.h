@@ -379,12 +379,15 @@ __global__ __launch_bounds__(512) void f8_order_kernel(F8Args a) {
 // from byte `at` on, past the registers.  In assembly, because the compiler lets
 // any later read of LDS wait for such a load: who uses this waits himself
 // (f8_landed), before he reads what it brings, and has read what lay there before.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"   // (m0 named as written: that the compiler then sets it again is meant)
 __device__ __forceinline__ void f8_to_lds(const void* base, uint32_t off, uint32_t at) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(off), "s"(base) : "memory", "m0");
 }
 __device__ __forceinline__ void f8_word_to_lds(const void* base, uint32_t off, uint32_t at) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(at), "v"(off), "s"(base) : "memory", "m0");
 }
+#pragma clang diagnostic pop
 // All but the last N of this wavefront's loads have landed.
 template <int N> __device__ __forceinline__ void f8_landed() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
 
