@@ -128,6 +128,12 @@ __device__ __forceinline__ uint32_t mp_key_from(double c) {
   return mp_key_of_order<ET>(o);
 }
 
+// The smallest key that min-p keeps in a row whose largest is kmax.  (T = inf and min_p = 1: every finite value.)
+template <typename ET>
+__device__ __forceinline__ uint32_t mp_least_key(const MinpMode& mm, uint32_t kmax) {
+  return min(mp_key_from<ET>((double)Key<ET>::value(kmax) + (double)mm.m.T * log((double)mm.mp)), kmax);
+}
+
 // exp(x) for x <= 0 in 64 bits: 2^k times the Taylor polynomial of exp on
 // [-ln 2 / 2, ln 2 / 2], whose 13th term is below 2^-53.
 __device__ __forceinline__ double mp_exp(double x) {
@@ -593,7 +599,7 @@ __device__ __forceinline__ bool mp_row_stats(const ET* row, int V, const MinpMod
   if (bad || kmax <= Key<ET>::NEG_INF) return false;
   const float zmax = Key<ET>::value(kmax);
   const double z0 = (double)zmax;
-  uint32_t thr = mm.mp > 0.0f ? min(mp_key_from<ET>(z0 + (double)mm.m.T * log((double)mm.mp)), kmax) : Key<ET>::NEG_INF + 1;
+  uint32_t thr = mm.mp > 0.0f ? mp_least_key<ET>(mm, kmax) : Key<ET>::NEG_INF + 1;
   const auto keys = [&](auto fn) { mp_for_row<ET, NTHR>(row, V, [&](uint32_t key, int) { fn(key); }); };
   const auto exponent = [&](uint32_t key) { return ((double)Key<ET>::value(key) - z0) * invT; };
   mp_top_k<ET, NTHR>(keys, mm, s, &thr);
@@ -891,7 +897,7 @@ __device__ __forceinline__ MinpPart mp_part(const MinpArgs& ma, long long rowid,
 }
 
 // One row's processed distribution from its lists: the values that min-p keeps, in
-// ascending id, into key[h], id[h] and w[h], exp((z - zmax) / T) >= min_p each; then
+// ascending id, into key[h], id[h] and w[h], exp((z - zmax) / T) each; then
 // the probabilities of what top-k and top-p leave, 0 for the others.  first: the
 // thread's part among the first NTHR.  (All of this is executed about once in a
 // launch, from memory: its time is that of fetching the instructions, so there is
@@ -914,17 +920,16 @@ __device__ __forceinline__ int mp_list_row(const MinpArgs& ma, const MinpMode& m
   if ((flags & MP_BAD) || kmax <= Key<ET>::NEG_INF) return MP_IS_BAD;
   if (flags & MP_OVER) return MP_TOO_LONG;
   const bool greedy = mm.kind == MP_GREEDY;
-  const double z0 = (double)Key<ET>::value(kmax), invT = greedy ? 0.0 : 1.0 / (double)mm.m.T, least = (double)mm.mp;
-  // A part whose maximum is well below what is kept has nothing that is.
-  const float near = Key<ET>::value(kmax) + mm.m.T * (__logf(mm.mp) - 0.001f);
-  const float floor_ = greedy ? Key<ET>::value(kmax) : near - 1e-5f * fabsf(near);
+  const double z0 = (double)Key<ET>::value(kmax), invT = greedy ? 0.0 : 1.0 / (double)mm.m.T;
+  // The smallest key that is kept.  (By its weight a value close to the border cannot be told from it.)
+  const uint32_t least = greedy ? kmax : mp_least_key<ET>(mm, kmax);
   const int lead = mp_lead(row);
   int have = 0;
 #pragma unroll 1
   for (int p0 = 0; p0 < NP; p0 += NTHR) {   // NTHR parts at a time
     uint32_t total;
     const MinpPart q = p0 == 0 ? first : mp_part(ma, rowid, p0 + tid);
-    s.base[tid] = mp_scan_u32<NTHR>(q.top != 0u && !(Key<ET>::value(q.top) < floor_) ? q.count : 0u, s.s.red_u, &total);
+    s.base[tid] = mp_scan_u32<NTHR>(q.top >= least ? q.count : 0u, s.s.red_u, &total);
     mp_sync<NTHR>();
     const int np = min(NP - p0, NTHR);
 #pragma unroll 1
@@ -943,7 +948,7 @@ __device__ __forceinline__ int mp_list_row(const MinpArgs& ma, const MinpMode& m
         id = (uint32_t)((p0 + lo) * ma.a.PL - lead) + E::index(e);
       }
       const double w = mp_exp(((double)Key<ET>::value(key) - z0) * invT);
-      const bool keep = i < total && (greedy ? key == kmax : w >= least);
+      const bool keep = i < total && key >= least;
       uint32_t all, at = (uint32_t)have;
       if constexpr (NTHR == 64) {
         const unsigned long long mask = __ballot(keep);
