@@ -325,7 +325,8 @@ class Verifier:
     def __init__(self, B: int, gamma_max: int, V: int, dtype: int = SV_BF16, device="cuda", with_pq=True,
                  hints: int = 0, min_p: bool = False):
         self.B, self.G, self.V, self.dtype = B, gamma_max, V, dtype
-        self.hints, self.min_p_hints = hints & ~SV_HINT_ALL_MIN_P, hints & SV_HINT_ALL_MIN_P
+        self.min_p_hints = hints & SV_HINT_ALL_MIN_P if min_p else 0
+        self.hints = hints & ~self.min_p_hints
         dev = torch.device(device)
         nbytes = spec_verify_workspace_bytes(B, gamma_max, V, dtype)
         if nbytes == 0:
@@ -470,8 +471,9 @@ def spec_sample_workspace_bytes(R: int, V: int, dtype: int) -> int:
 class Sampler:
     """One token per row from the processed distribution, by inverse CDF at a
     uniform (spec_sample); owns the workspace and the output for one shape.
-    With min_p=True, also those of calls with min_p (spec_sample_min_p, whose
-    hints these are), which leave the drawn tokens' probabilities in self.prob."""
+    With min_p=True, also those of calls with min_p (spec_sample_min_p), which
+    leave the drawn tokens' probabilities in self.prob; the one hint,
+    SV_HINT_ALL_MIN_P, concerns those calls alone."""
 
     def __init__(self, R: int, V: int, dtype: int = SV_BF16, device="cuda", hints: int = 0, min_p: bool = False):
         self.R, self.V, self.dtype, self.hints = R, V, dtype, hints
@@ -509,14 +511,14 @@ class Sampler:
         _check(temperature, "temperature", torch.float32, (R,), dev)
         _check(top_k, "top_k", torch.int32, (R,), dev)
         _check(top_p, "top_p", torch.float32, (R,), dev)
+        if self.hints and (self.min_p_workspace is None or self.hints & ~SV_HINT_ALL_MIN_P):
+            raise ValueError("a sampler takes no other hint than SV_HINT_ALL_MIN_P, and that one with min_p=True")
         if min_p is not None:
             _check(min_p, "min_p", torch.float32, (R,), dev)
             if self.min_p_workspace is None:
                 raise ValueError("min_p needs a Sampler(min_p=True)")
             if dev != self.tokens.device:
                 raise ValueError(f"logits are on {dev}, the sampler's workspace on {self.tokens.device}")
-            if self.hints & ~SV_HINT_ALL_MIN_P:
-                raise ValueError("the sampler takes no other hint than SV_HINT_ALL_MIN_P")
         if processor is not None:   # after every check: a call that is refused leaves the logits as they were
             _require(uniforms=uniforms, temperature=temperature)
             need, ws = (spec_sample_workspace_bytes, self.workspace) if min_p is None else \
