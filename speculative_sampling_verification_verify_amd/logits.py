@@ -280,12 +280,23 @@ class F8Head:
     logits (f8_products: as in spec_logits_f8, for logits in bf16)."""
 
     def __init__(self, weights: torch.Tensor, scales: torch.Tensor, f8_products: bool = False):
+        self.N, self.K = self._sizes(weights)
+        _check(scales, "scales", scales.dtype, (_blocks(self.N), _blocks(self.K)), scales.device)
         self.weights, self.scales, self.f8_products = weights, scales, f8_products
-        self.N, self.K = weights.shape
+
+    @staticmethod
+    def _sizes(weights):
+        if weights.dim() != 2:
+            raise ValueError("weights must be [N, K]")
+        N, K = weights.shape
+        if K % 16 or not 0 < K <= SL_MAX_K:
+            raise ValueError(f"a head's K is a multiple of 16 of at most {SL_MAX_K}, got {K}")
+        return N, K
 
     @classmethod
     def quantize(cls, weights: torch.Tensor, stream=None, f8_products: bool = False) -> "F8Head":
         """The head of bf16 or fp32 weights [N, K], quantised."""
+        cls._sizes(weights)
         return cls(*spec_quantize_f8(weights, SL_F8_BLOCK, stream=stream), f8_products)
 
     def __call__(self, hidden, out=None, out_dtype=None, stream=None):
