@@ -375,8 +375,10 @@ int spec_verify_spectr(const void* p_logits, const void* q_logits, int dtype, co
  *               the sequence invalid.  NULL: none has min-p.  T = 0 is argmax, whatever min_p is.
  *  hints        0, or SV_HINT_ALL_MIN_P: the caller knows that every sequence has min_p > 0 or
  *               T = 0.  One launch then replaces those that take other sequences row by row.  A
- *               sequence without, or one that keeps more than the call's lists hold (1024 values
- *               of a row), still gets its exact result, from that launch, only later.
+ *               sequence without, or one with a row that the call's lists do not hold (1024 values
+ *               of a row, and 512 of a row part within min_p of that part's own largest, which
+ *               flat logits also exceed far below what is kept), still gets its exact result, from
+ *               that launch, only later.
  *  out_prob     [R] float or NULL: the processed probability of the token drawn (NaN for an invalid
  *               row), which a verify reports as q(x).
  *  workspace    spec_verify_min_p_workspace_bytes(B, gamma_max, V, dtype) bytes (gamma_max = 0 and

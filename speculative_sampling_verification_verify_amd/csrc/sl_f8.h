@@ -19,10 +19,10 @@
 // rows x is quantised into operand order first (f8_order_kernel), then tiles
 // over rows and columns (f8_tile_kernel).  At K = 4096, bf16:
 //   1 row,     N = 152064: 115 us a call, 5.4 TB/s of weight bytes (a 1 GiB copy: 5.05)
-//   320 rows,  N = 128255: 409 us, 0.82 PFLOP/s; with 8-bit products 195 us, 1.72
+//   320 rows,  N = 128255: 405 us, 0.83 PFLOP/s; with 8-bit products 200 us, 1.68
 //                          PFLOP/s (the library's product of such codes with one scale
 //                          for everything, N = 128256: 260 us)
-//   2048 rows, N = 152064: 2.55 ms, 1.00 PFLOP/s; with 8-bit products 1.30 ms, 1.96
+//   2048 rows, N = 152064: 2.50 ms, 1.02 PFLOP/s; with 8-bit products 1.30 ms, 1.96
 //                          PFLOP/s (such a library product: 1.09 ms)
 #pragma once
 
@@ -101,10 +101,10 @@ struct F8QuantArgs {
   uint8_t* q;
   float* s;
   int R, K, KB;
-  int wide;   // rows of whole 16-byte units, aligned bases
 };
 
-// Eight values from column k of a row on, zeros behind its end.
+// Eight values from column k of a row on, zeros behind its end.  WIDE: rows of whole
+// units of eight, aligned bases.
 template <typename XT, bool WIDE>
 __device__ __forceinline__ void fq_load(const XT* row, int k, int K, float (&v)[8]) {
   if (WIDE) {
@@ -133,7 +133,9 @@ __device__ __forceinline__ void fq_store(uint8_t* row, int k, int K, uint2 c) {
 
 // A scale for each row and 128 of k: 16 lanes to a block, whose values are in
 // registers from the one read to the write.  Memory bounds it: 128256 x 4096 in bf16
-// with a scale a tile (below) takes 300 us, 1.58 GB at 5.3 TB/s.
+// with a scale a tile (below) takes 298 us, 1.58 GB at 5.3 TB/s.  Where K is no multiple of
+// 8 or a base not aligned (WIDE false) values and codes go one by one: 1048 us at
+// 128256 x 4095 in tiles; 4096 rows of 4096 and of 4095 with a scale a row: 12 and 27 us.
 template <typename XT, bool WIDE>
 __global__ __launch_bounds__(FQ_NT) void quantize_rows_kernel(F8QuantArgs a) {
   const int u = threadIdx.x & 15;
@@ -406,9 +408,10 @@ __device__ __forceinline__ void f8_wave_sync() {
 // are loaded in whole lines and read in operand order; position q of a row holds
 // its 16-byte unit q ^ (row / 2 % 8), so that the reads do not conflict (4 cycles a
 // 16-byte read of a wavefront, measured alone; with row % 8, 8).
-// At R = 2048, N = 152064, K = 4096 the matrix cores are busy 46% of the time, the
-// vector units 40% (mostly the scaling), at 1.85 GHz; without its loads the kernel
-// would take 1.03 ms of 1.30.
+// At R = 2048, N = 152064, K = 4096: 8-bit products, matrix cores busy 46% of the time,
+// vector units 40% (mostly the scaling), at 2.0 GHz, without its loads 1.03 ms of 1.30;
+// expanded, matrix cores 45%, vector units 39% (the expansion and the scaling), and two
+// row tiles a wavefront are what LDS holds twice beside 256 weight rows.
 constexpr int F8T_NT = 512;
 constexpr int F8T_SW = 4096;   // bytes of the weights' scales: SL_MAX_K / 128 blocks, twice
 

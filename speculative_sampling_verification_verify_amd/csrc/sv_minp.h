@@ -15,14 +15,18 @@
 //                         then the acceptance
 //   minp_row_kernel, minp_row_position_kernel, minp_finish_kernel
 //                         the same from the logits, for rows without min-p and
-//                         rows that keep more than the lists hold, one
-//                         workgroup a row; where the caller says that there are
+//                         rows with more than the lists hold, one
+//                         workgroup a row (a part's list is cut against the part's
+//                         maximum: one flat part overflows it, also far below
+//                         what the row keeps); where the caller says that there are
 //                         none of the first, minp_left_kernel in place of the
 //                         three, one workgroup a sequence
 //
 // Probabilities and normalisers are held in 64 bits, nucleus masses as multiples
 // of 2^-42 of the largest value's (whole numbers, whose sum does not depend on
-// its order): what decides is within V 2^-42 of its exact value.
+// its order): what decides is within V 2^-42 of its exact value.  (So is the
+// normaliser behind a nucleus that minp_row_kernel or minp_left_kernel found: that
+// mass.  From the lists it is a sum in float64.)
 //
 // What bounds it, at B = 256, V = 152064, 7 drafts, bf16 (1.17 GB of logits; all
 // with min-p 0.05): the cut takes 173 of 193 us, 6.75 TB/s, which is what the
@@ -134,8 +138,8 @@ __device__ __forceinline__ uint32_t mp_least_key(const MinpMode& mm, uint32_t km
   return min(mp_key_from<ET>((double)Key<ET>::value(kmax) + (double)mm.m.T * log((double)mm.mp)), kmax);
 }
 
-// exp(x) for x <= 0 in 64 bits: 2^k times the Taylor polynomial of exp on
-// [-ln 2 / 2, ln 2 / 2], whose 13th term is below 2^-53.
+// exp(x) for x <= 0 in 64 bits: 2^k times the Taylor polynomial of degree 13 of exp on
+// [-ln 2 / 2, ln 2 / 2]; the first term left out, r^14 / 14!, is at most 4.2e-18, below 2^-57.
 __device__ __forceinline__ double mp_exp(double x) {
   x = fmax(x, -746.0);   // -inf, too: 2^-1076 and a bit, which ldexp rounds to 0
   const double k = rint(x * 1.4426950408889634);
