@@ -222,9 +222,14 @@ static int launch_quantize(const F8QuantArgs& a, int rows, hipStream_t st) {
 }
 
 // The plan of a product, a function of its sizes and types alone: few rows go to
-// the streaming kernel where they fit LDS.  products8: the caller takes the matrix
-// cores' 8-bit products, which pay from the second 64 rows on (us at K = 4096,
-// N = 128255: up to 64 rows 120 expanded; 65 rows 145 expanded, 117 in 8 bits).
+// the streaming kernel where they fit LDS.  In us, streamed and in tiles (K = 4096):
+//   N=32000:   R=1 23, 32   R=8 28, 31   R=16 34, 31
+//   N=128255:  R=1 100, 113 R=8 109, 114 R=16 118, 115
+// products8: the caller takes the matrix cores' 8-bit products.  They halve the time
+// only where one tile does not hold all rows; up to F8_EXACT_ROWS sums stay in float32.
+// In us, expanded and 8-bit:
+//   N=32000:   R=64  33,  26   R=65  49,  31   R=320 120,  55
+//   N=128255:  R=64 126, 116   R=65 156, 119   R=320 405, 200
 constexpr int F8_EXACT_ROWS = 64;
 
 struct F8Plan {
@@ -278,7 +283,10 @@ static F8Plan f8_plan(bool products8, int R, int K, int N) {
   p.f8 = products8 && R > F8_EXACT_ROWS;
   size_t units;   // of 64 rows
   if (p.f8) {
-    // The widest tile that wastes the fewest rows.
+    // The widest tile that pads the fewest rows.  For 7, 11, 13 and 17 units of 64 rows
+    // that is the narrowest one, where a wider one would take less time.  In us, as it is
+    // and at its best, N = 128255:  R=448 394, 282 (mt 4)   R=640 367, 353 (mt 5)
+    //   R=704 609, 418 (mt 4)   R=832 698, 504 (mt 5)   R=1088 921, 674 (mt 5)   R=2048 1140, 1140
     p.mt = 1;
     for (int mt = 2; mt <= 5; ++mt)
       if ((R + 64 * mt - 1) / (64 * mt) * mt <= (R + 64 * p.mt - 1) / (64 * p.mt) * p.mt) p.mt = mt;
