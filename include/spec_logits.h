@@ -115,8 +115,8 @@ int spec_quantize_f8(const void* x, int x_dtype, int rows, int R, int K, uint8_t
  *           bytes.
  *
  * The products of the codes are exact; sums are held in float32 and rounded once, to nearest
- * even, at the end.  So is hs * scales, before it meets a block's sum: it has to be 0 or a normal
- * float32 number.
+ * even, at the end.  So is hs * scales, before it meets a block's sum: where that product leaves
+ * float32's normal range, what the block adds does too.
  * With out_dtype SL_BF16_F8 the output is bf16, and of more than 64 rows formed by the matrix cores'
  * 8-bit products, in half the time.  These cut off, in the sum of 8 consecutive k, what lies below
  * 2^-13 of the largest of the 8 products' binade: for sums of many products of like size an error
